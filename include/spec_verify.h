@@ -311,6 +311,128 @@ int spec_build_tree(const int32_t* candidates, int B, int M, int L, int N, int32
 int spec_philox_uniform(uint64_t key0, uint64_t key1, uint64_t counter, int64_t n, float* out,
                         hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Paged key/value cache: the target model's side of a drafting step.
+ *
+ * The keys and values of a sequence's tokens lie in pages of page_size rows; entry j of its row
+ * of page_table names the page of positions j * page_size and up.  A step writes the drafted
+ * nodes' keys and values behind the committed tokens (spec_cache_append; node i at position
+ * seq_lens + i, in every layer), attends from the nodes (spec_tree_attention), verifies
+ * (spec_verify_tree or spec_verify) and moves the accepted path's rows together
+ * (spec_cache_commit).  spec_cache_resize and spec_cache_fork manage the pages.
+ *
+ * Keys and values do not overlap (calls that write them refuse k == v).  A cache's arrays are
+ * changed by one call at a time.
+ *
+ * Rules for device values: a length below 0 counts as 0 and one beyond the table as the table's
+ * end; a page outside [0, pages) holds nothing (its keys are seen by no row, writes to it are
+ * dropped).  Nothing outside the cache's pages is ever read or written.
+ * ---------------------------------------------------------------------------------------------
+ */
+typedef struct {
+  void* k;             /* element (layer, page, slot, head, d) of the keys lies at         */
+  void* v;             /*   layer * layer_stride + page * page_stride + slot *             */
+                       /*   token_stride + head * head_stride + d; the values likewise     */
+  sv_dtype dtype;      /* of keys, values and queries                                      */
+  int32_t layers;      /* >= 1                                                             */
+  int32_t pages;       /* >= 1                                                             */
+  int32_t page_size;   /* tokens a page, >= 1 (any size)                                   */
+  int32_t kv_heads;    /* 1..1024                                                          */
+  int32_t head_dim;    /* a row of it is a multiple of 16 bytes, at most 1024              */
+  int64_t layer_stride, page_stride, token_stride, head_stride; /* elements, in any order of
+                          size; multiples of 16 bytes; rows do not overlap                 */
+  int32_t seqs;        /* sequences, 1..8192                                               */
+  int32_t table_width; /* entries a sequence; table_width * page_size <= 2^30              */
+  int32_t* page_table; /* [seqs, table_width] device                                       */
+  int32_t* seq_lens;   /* [seqs] device: committed tokens                                  */
+  int32_t* seq_pages;  /* [seqs] device: entries in use (resize and fork; else NULL)       */
+  int32_t* refcount;   /* [pages] device: sequences that hold the page, 0 = free (likewise) */
+} sv_cache;
+
+/*
+ * Attention of every sequence's drafted nodes over the committed tokens and the nodes that each
+ * may see.
+ *   q           [seqs, N, q_heads, head_dim], element strides q_strides[3] of sequence, node and
+ *               head (NULL: dense); 16-byte aligned rows.  Query head x reads kv head
+ *               x / (q_heads / kv_heads).  head_dim is 64, 96, 128 or 256
+ *   N           nodes a sequence, 1..2048 (1: plain decoding of a token)
+ *   mask        [seqs, N, N] uint8 or NULL: node i sees node j iff mask[., i, j] != 0, as
+ *               spec_build_tree's out_mask says; NULL: a chain, i sees j <= i.  Every committed
+ *               token is seen by every node
+ *   num_nodes   [seqs] or NULL (N each): rows past it get zeros (lse -inf), and nobody sees them
+ *   scale       > 0, of the products q.k
+ *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype
+ *   out_lse     [seqs, N, q_heads] float or NULL: natural logarithm of the sum of exponentials
+ * A row that sees nothing gives zeros and -inf.  Keys and values that a row does not see do not
+ * reach it, whatever they hold (NaN and infinities too).  Sums and softmax statistics are kept
+ * in fp32; with bf16 the weights are rounded to bf16 for the product with the values.
+ * Equal inputs give bitwise equal outputs; a sequence's last bits may change with the lengths
+ * of the others in the batch (the work is cut evenly over the GPU).
+ */
+size_t spec_tree_attention_workspace_size(const sv_cache* cache, int N, int q_heads);
+int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_heads,
+                        const sv_cache* cache, int layer, const uint8_t* mask,
+                        const int32_t* num_nodes, float scale, void* out, float* out_lse,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Writes the keys and values of each sequence's nodes to positions seq_lens + 0 .. num_nodes - 1
+ * of one layer.  k_new, v_new [seqs, N, kv_heads, head_dim] of the cache's dtype with element
+ * strides new_strides[3] (NULL: dense), 16-byte aligned rows; num_nodes [seqs] or NULL (N each).
+ * The pages written are the sequence's own (spec_cache_fork shares full pages below seq_lens
+ * only).  seq_lens stays: the nodes are not committed yet.
+ */
+int spec_cache_append(const void* k_new, const void* v_new, const int64_t* new_strides, int N,
+                      const sv_cache* cache, int layer, const int32_t* num_nodes,
+                      hipStream_t stream);
+
+/*
+ * Keeps the rows of the path from the root to last_node of each sequence's tree: in every layer
+ * the row at position seq_lens + path[d] moves to seq_lens + d.
+ *   last_node  [seqs]: spec_verify_tree's out_last_node
+ *   parent     [seqs, N] as spec_verify_tree takes it (parents precede their children); NULL: a
+ *              chain, node i's parent is i - 1 (last_node = spec_verify's out_num_accepted), and
+ *              nothing has to move
+ *   out_lens   [seqs]: seq_lens + depth of last_node + 1 (the root is committed too).  A
+ *              sequence whose last_node is outside [0, N), whose path meets an invalid parent or
+ *              whose path lies on a missing page is left alone: its out_lens is seq_lens.
+ *              Must not overlap seq_lens (spec_cache_resize stores it there)
+ */
+int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int32_t* parent,
+                      int N, int32_t* out_lens, hipStream_t stream);
+
+/*
+ * Makes every sequence hold exactly the pages of want[b] tokens: pages past them are given back
+ * (their count falls by one), missing ones are taken from the free pages, lowest index first,
+ * and entered in page_table; seq_pages follows.  Entries of page_table from seq_pages on are
+ * unspecified.  All pages given back in a call are free for it.
+ *   want      [seqs]: < 0 leaves the sequence alone; 0 frees it and sets seq_lens to 0;
+ *             otherwise seq_lens <= want <= table_width * page_size (committed tokens are not
+ *             cut)
+ *   new_lens  [seqs] or NULL: stored to seq_lens first (0 <= new_lens <= the pages held), as
+ *             after spec_cache_commit
+ *   out_ok    [seqs]: 1, or 0 where a value is out of range or the free pages did not suffice
+ *             (sequences are served in order until one does not fit; it and the later ones that
+ *             need pages keep what they hold).  A failing sequence's pages are untouched
+ * The arrays of one call must not overlap.
+ */
+int spec_cache_resize(const sv_cache* cache, const int32_t* want, const int32_t* new_lens,
+                      int32_t* out_ok, hipStream_t stream);
+
+/*
+ * Continues sequences src[f] as dst[f], f < F (0 <= F <= seqs): full pages are shared (their
+ * count rises by one), a page begun is copied in every layer to the free page of lowest index;
+ * page_table, seq_pages and seq_lens of dst follow.  Drafted rows past seq_lens are not taken.
+ *   src, dst  [F]: dst[f] must hold no page and be the source of no fork in the call; of
+ *             several forks into one slot the first counts
+ *   out_ok    [F]: 1, or 0 where that does not hold, an index or the source's state is out of
+ *             range, its begun page is missing, or no page is free (forks are served in order).
+ *             A failing fork changes nothing
+ */
+int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* dst, int F,
+                    int32_t* out_ok, hipStream_t stream);
+
 /* Static string for a status code. */
 const char* spec_verify_status_string(int status);
 

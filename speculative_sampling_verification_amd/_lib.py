@@ -29,12 +29,26 @@ class SVSampling(ctypes.Structure):
                 ("mentor_kl", ctypes.c_float)]
 
 
+class SVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("layers", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("seq_pages", ctypes.c_void_p),
+                ("refcount", ctypes.c_void_p)]
+
+
 EXPORTS = [
     "spec_verify_workspace_size", "spec_verify", "spec_verify_profiled",
     "spec_sample_workspace_size", "spec_sample",
     "spec_verify_tree_workspace_size", "spec_verify_tree", "spec_verify_tree_profiled",
     "spec_build_tree", "spec_philox_uniform", "spec_acceptance_rate", "spec_verify_rates",
     "spec_verify_presampled", "spec_verify_noalloc",
+    "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append",
+    "spec_cache_commit", "spec_cache_resize", "spec_cache_fork",
     "spec_expected_tokens",
     "spec_walltime_speedup", "spec_ops_factor", "spec_optimal_gamma",
     "spec_verify_status_string",
@@ -80,6 +94,20 @@ def load(path=LIB_PATH):
     lib.spec_philox_uniform.restype = i32
     lib.spec_acceptance_rate.argtypes = [vp, vp, i32, i32, i32, i32, i32, psamp, vp, vp, sz, vp]
     lib.spec_acceptance_rate.restype = i32
+    pcache, f32 = ctypes.POINTER(SVCache), ctypes.c_float
+    lib.spec_tree_attention_workspace_size.argtypes = [pcache, i32, i32]
+    lib.spec_tree_attention_workspace_size.restype = sz
+    lib.spec_tree_attention.argtypes = [vp, vp, i32, i32, pcache, i32, vp, vp, f32, vp, vp, vp,
+                                        sz, vp]
+    lib.spec_tree_attention.restype = i32
+    lib.spec_cache_append.argtypes = [vp, vp, vp, i32, pcache, i32, vp, vp]
+    lib.spec_cache_append.restype = i32
+    lib.spec_cache_commit.argtypes = [pcache, vp, vp, i32, vp, vp]
+    lib.spec_cache_commit.restype = i32
+    lib.spec_cache_resize.argtypes = [pcache, vp, vp, vp, vp]
+    lib.spec_cache_resize.restype = i32
+    lib.spec_cache_fork.argtypes = [pcache, vp, vp, i32, vp, vp]
+    lib.spec_cache_fork.restype = i32
     dbl = ctypes.c_double
     lib.spec_expected_tokens.argtypes = [dbl, i32]
     lib.spec_expected_tokens.restype = dbl
@@ -160,7 +188,8 @@ def workspace(device, nbytes, stream=None):
     if buf is None or buf.numel() < nbytes:
         if buf is not None:
             _outgrown.append(buf)
-        buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+        with torch.cuda.stream(s):  # memory whose earlier users are ordered before the work on s
+            buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
         _workspaces[key] = buf
     return buf
 
@@ -454,6 +483,213 @@ def spec_acceptance_rate(target_logits, draft_logits, *, temperature=1.0, top_k=
     _check("spec_acceptance_rate", _lib.spec_acceptance_rate(
         _ptr(target_logits), _ptr(draft_logits), dt, B, K, V, draft_logits.shape[1],
         ctypes.byref(samp), _ptr(out), _ptr(ws), ws.numel(), _stream(dev, stream)))
+    return out
+
+
+class PagedCache:
+    """A paged key/value cache (sv_cache of include/spec_verify.h): the caller's tensors, checked
+    once and kept.
+
+    k, v        [layers, pages, page_size, kv_heads, head_dim], or without the layers; bf16 or
+                fp32, any strides with rows on 16 bytes and apart (both tensors alike)
+    page_table  [seqs, width] int32
+    seq_lens    [seqs] int32, committed tokens
+    seq_pages, refcount   [seqs], [pages] int32: needed by spec_cache_resize and spec_cache_fork
+    """
+
+    def __init__(self, k, v, page_table, seq_lens, *, seq_pages=None, refcount=None):
+        dev = k.device
+        if k.dim() == 4:
+            k, v = k.unsqueeze(0), v.unsqueeze(0)
+        if k.dim() != 5:
+            raise ValueError("k must be [layers, pages, page_size, kv_heads, head_dim]")
+        if v.device != dev or v.dtype != k.dtype or v.shape != k.shape:
+            raise ValueError("k and v must agree in device, dtype and shape")
+        strides = k.stride()
+        if any(n > 1 and x != y for n, x, y in zip(k.shape, strides, v.stride())):
+            raise ValueError("k and v must have the same strides")
+        if k.shape[4] > 1 and strides[4] != 1:
+            raise ValueError("head_dim must be contiguous")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [seqs, width]")
+        seqs, width = page_table.shape
+        _need(page_table, "page_table", dev, torch.int32)
+        _need(seq_lens, "seq_lens", dev, torch.int32, (seqs,))
+        if seq_pages is not None:
+            _need(seq_pages, "seq_pages", dev, torch.int32, (seqs,))
+        if refcount is not None:
+            _need(refcount, "refcount", dev, torch.int32, (k.shape[1],))
+        self.k, self.v, self.page_table, self.seq_lens = k, v, page_table, seq_lens
+        self.seq_pages, self.refcount = seq_pages, refcount
+        self.device, self.dtype = dev, k.dtype
+        self.layers, self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self.seqs = seqs
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._c = SVCache(ptr(k), ptr(v), _dtype_code(k), *k.shape, *strides[:4], seqs, width,
+                          ptr(page_table), ptr(seq_lens), ptr(seq_pages), ptr(refcount))
+        self._ref = ctypes.byref(self._c)
+        self._workspace_bytes = {}
+
+    def _attention_workspace(self, N, q_heads):
+        need = self._workspace_bytes.get((N, q_heads))
+        if need is None:
+            need = _lib.spec_tree_attention_workspace_size(self._ref, N, q_heads)
+            if need == 0:
+                raise SpecVerifyError("spec_tree_attention_workspace_size", 1)
+            self._workspace_bytes[(N, q_heads)] = need
+        return need
+
+
+def _new(shape, dtype, device, stream):
+    """An output tensor of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cache_call(cache, stream, fn, name, *args):
+    """Calls fn(*args, stream) with the cache's device current (a null stream is that device's)."""
+    dev = cache.device
+    if dev.index == torch.cuda.current_device():
+        _check(name, fn(*args, _stream(dev, stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, fn(*args, _stream(dev, stream)))
+
+
+def _row_strides(t, name, cache, heads):
+    """The element strides of a [seqs, N, heads, head_dim] tensor, None where it is dense."""
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != cache.seqs or shape[3] != cache.head_dim or (
+            heads is not None and shape[2] != heads):
+        raise ValueError(f"{name} must be [{cache.seqs}, N, {heads or 'heads'}, "
+                         f"{cache.head_dim}], got {tuple(shape)}")
+    if t.is_contiguous():
+        return None
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name}'s head_dim must be contiguous")
+    return (ctypes.c_int64 * 3)(*(x if n > 1 else 0 for n, x in zip(shape, s[:3])))
+
+
+def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=None,
+                        want_lse=False, out=None, stream=None):
+    """Attention of drafted nodes over a PagedCache's committed tokens and the nodes each may see
+    (see include/spec_verify.h).
+
+    q [seqs, N, q_heads, head_dim] of the cache's dtype (strided views with contiguous head_dim
+    are taken as they are); node i's own key lies at position seq_lens + i (spec_cache_append).
+    mask [seqs, N, N] uint8 as spec_build_tree makes it, or None for a chain (and for N = 1,
+    plain decoding); num_nodes [seqs] int32 or None; scale defaults to head_dim ** -0.5.
+    Returns a dict: out (like q, dense) and, if want_lse, lse [seqs, N, q_heads] float32.
+    ``out`` may hold preallocated tensors under the same keys.
+    """
+    strides = _row_strides(q, "q", cache, None)
+    B, N, H, D = q.shape
+    dev = cache.device
+    if mask is not None:
+        _need(mask, "mask", dev, torch.uint8, (B, N, N))
+    if num_nodes is not None:
+        _need(num_nodes, "num_nodes", dev, torch.int32, (B,))
+    out = dict(out) if out else {}
+    o = out.get("out")
+    if o is None:
+        o = out["out"] = _new((B, N, H, D), q.dtype, dev, stream)
+    else:
+        _need(o, "out out", dev, q.dtype, (B, N, H, D))
+    lse = out.get("lse")
+    if lse is not None:
+        _need(lse, "out lse", dev, torch.float32, (B, N, H))
+    elif want_lse:
+        lse = out["lse"] = _new((B, N, H), torch.float32, dev, stream)
+    need = cache._attention_workspace(N, H)
+    ws = workspace(dev, need, stream)
+    _cache_call(cache, stream, _lib.spec_tree_attention, "spec_tree_attention", q.data_ptr(),
+                strides, N, H, cache._ref, layer, _ptr(mask), _ptr(num_nodes),
+                D ** -0.5 if scale is None else scale, o.data_ptr(), _ptr(lse), ws.data_ptr(),
+                ws.numel())
+    return out
+
+
+def spec_cache_append(k_new, v_new, cache, *, layer=0, num_nodes=None, stream=None):
+    """Writes k_new, v_new [seqs, N, kv_heads, head_dim] of each sequence's nodes to positions
+    seq_lens + 0 .. num_nodes - 1 of one layer (see include/spec_verify.h).  Both tensors may be
+    strided views, with the same strides."""
+    strides = _row_strides(k_new, "k_new", cache, cache.kv_heads)
+    v_strides = _row_strides(v_new, "v_new", cache, cache.kv_heads)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    if (strides is None) != (v_strides is None) or (
+            strides is not None and list(strides) != list(v_strides)):
+        raise ValueError("k_new and v_new must have the same strides")
+    if num_nodes is not None:
+        _need(num_nodes, "num_nodes", cache.device, torch.int32, (cache.seqs,))
+    _cache_call(cache, stream, _lib.spec_cache_append, "spec_cache_append", k_new.data_ptr(),
+                v_new.data_ptr(), strides, k_new.shape[1], cache._ref, layer, _ptr(num_nodes))
+
+
+def spec_cache_commit(cache, last_node, *, parent=None, num_nodes=None, out=None, stream=None):
+    """Moves the rows of each sequence's accepted path together in every layer and returns the
+    new lengths [seqs] int32 (see include/spec_verify.h); seq_lens itself stays until
+    spec_cache_resize(new_lens=...) stores it.
+
+    last_node [seqs] int32: spec_verify_tree's last_node with its parent [seqs, N]; without
+    parent (a chain of num_nodes nodes, default 2048) spec_verify's num_accepted."""
+    dev = cache.device
+    _need(last_node, "last_node", dev, torch.int32, (cache.seqs,))
+    if parent is not None:
+        _need(parent, "parent", dev, torch.int32)
+        if parent.dim() != 2 or parent.shape[0] != cache.seqs:
+            raise ValueError("parent must be [seqs, N]")
+        N = parent.shape[1]
+    else:
+        N = 2048 if num_nodes is None else int(num_nodes)
+    if out is None:
+        out = _new((cache.seqs,), torch.int32, dev, stream)
+    else:
+        _need(out, "out", dev, torch.int32, (cache.seqs,))
+    _cache_call(cache, stream, _lib.spec_cache_commit, "spec_cache_commit", cache._ref,
+                last_node.data_ptr(), _ptr(parent), N, out.data_ptr())
+    return out
+
+
+def spec_cache_resize(cache, want, *, new_lens=None, out=None, stream=None):
+    """Gives back and takes pages so that each sequence holds those of want [seqs] int32 tokens
+    (< 0: left alone, 0: freed); new_lens [seqs] int32 is stored to seq_lens first.  Returns ok
+    [seqs] int32 (see include/spec_verify.h)."""
+    dev = cache.device
+    _need(want, "want", dev, torch.int32, (cache.seqs,))
+    if new_lens is not None:
+        _need(new_lens, "new_lens", dev, torch.int32, (cache.seqs,))
+    if out is None:
+        out = _new((cache.seqs,), torch.int32, dev, stream)
+    else:
+        _need(out, "out", dev, torch.int32, (cache.seqs,))
+    _cache_call(cache, stream, _lib.spec_cache_resize, "spec_cache_resize", cache._ref,
+                want.data_ptr(), _ptr(new_lens), out.data_ptr())
+    return out
+
+
+def spec_cache_fork(cache, src, dst, *, out=None, stream=None):
+    """Continues sequences src [F] int32 as the empty sequences dst [F] int32: full pages shared,
+    a begun page copied in every layer.  Returns ok [F] int32 (see include/spec_verify.h)."""
+    dev = cache.device
+    _need(src, "src", dev, torch.int32)
+    if src.dim() != 1:
+        raise ValueError("src must be [F]")
+    F = src.shape[0]
+    _need(dst, "dst", dev, torch.int32, (F,))
+    if out is None:
+        out = _new((F,), torch.int32, dev, stream)
+    else:
+        _need(out, "out", dev, torch.int32, (F,))
+    _cache_call(cache, stream, _lib.spec_cache_fork, "spec_cache_fork", cache._ref,
+                src.data_ptr(), dst.data_ptr(), F, out.data_ptr())
     return out
 
 

@@ -1,0 +1,437 @@
+// Rows and pages of a paged key/value cache on gfx950: drafted nodes written behind the
+// committed tokens (k_append), an accepted path's rows moved together (k_commit), sequences
+// grown, trimmed and freed in a pool of counted pages (k_pool_resize) and forked with shared
+// full pages (k_pool_fork, k_fork_copy).  All of it moves or counts; nothing is computed.
+//
+// The pool's state is one reference count a page: a page is free iff its count is 0, and the
+// free pages of lowest index are taken first.  Which page a sequence gets therefore depends on
+// the counts alone, not on the order in which earlier pages came back, and the counts are
+// changed by integer atomics whose order does not matter.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "sv_cache.hpp"
+
+namespace sv {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMoveThreads = 256;
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWaves = kPoolThreads / 64;
+
+// Byte offset of a position's row in the pages of sequence b; -1 where the table has no page.
+__device__ __forceinline__ int64_t row_offset(const CacheView& c, int b, int pos) {
+  if (pos < 0 || pos >= c.cap) return -1;
+  const uint32_t pi = fast_div(c.page_div, (uint32_t)pos);
+  const int page = c.table[(size_t)b * c.width + pi];
+  if (page < 0 || page >= c.pages) return -1;
+  return (int64_t)page * c.page_stride + (int64_t)(pos - (int)(pi * c.page_div.d)) * c.token_stride;
+}
+
+__device__ __forceinline__ int clamp_len(const CacheView& c, int len) {
+  return len < 0 ? 0 : len > c.cap ? c.cap : len;
+}
+
+// One thread per 16 bytes of a node's keys, and the same of its values.
+__global__ __launch_bounds__(kMoveThreads) void k_append(CacheView c, const char* k_new,
+                                                         const char* v_new, int64_t new_seq,
+                                                         int64_t new_node, int64_t new_head,
+                                                         const int32_t* nodes, int N,
+                                                         FastDiv row_div, FastDiv head_div) {
+  const int b = blockIdx.y;
+  const uint32_t x = blockIdx.x * kMoveThreads + threadIdx.x;
+  const int i = (int)fast_div(row_div, x);
+  const uint32_t y = x - (uint32_t)i * row_div.d;
+  const int h = (int)fast_div(head_div, y);
+  const int at = (int)(y - (uint32_t)h * head_div.d) * 16;
+  const int n = nodes ? nodes[b] : N;
+  if (i >= n || i >= N) return;
+  const int64_t row = row_offset(c, b, clamp_len(c, c.lens[b]) + i);
+  if (row < 0) return;
+  const int64_t from = (int64_t)b * new_seq + (int64_t)i * new_node + (int64_t)h * new_head + at;
+  const int64_t to = row + (int64_t)h * c.head_stride + at;
+  const u32x4 kx = *reinterpret_cast<const u32x4*>(k_new + from);
+  const u32x4 vx = *reinterpret_cast<const u32x4*>(v_new + from);
+  *reinterpret_cast<u32x4*>(c.k + to) = kx;
+  *reinterpret_cast<u32x4*>(c.v + to) = vx;
+}
+
+// Accepted path of a breadth-first tree: node path[d] at depth d has path[d] >= d, so row
+// len + path[d] moves down to len + d and, taken in increasing d, no move overwrites a row that
+// a later one reads.  A thread owns 16 bytes of a row in one layer's keys or values and moves
+// them for every depth, eight rows in flight; no other thread touches them.
+__global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int32_t* parent,
+                                                         const int32_t* last, int N,
+                                                         int32_t* out_lens, FastDiv row_div,
+                                                         FastDiv head_div) {
+  __shared__ int32_t up[kCacheMaxNodes];    // parents, then the path from its end
+  __shared__ int16_t walk[kCacheMaxNodes];
+  __shared__ int64_t from[kCacheMaxNodes], to[kCacheMaxNodes];
+  __shared__ int depth_sh, bad_sh;
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int len = clamp_len(c, c.lens[b]);
+  const int end = last[b];
+  bool ok = end >= 0 && end < N;
+  if (tid == 0) bad_sh = 0;
+  if (parent) {
+    for (int i = tid; i < N; i += kMoveThreads) up[i] = parent[(size_t)b * N + i];
+    __syncthreads();
+    if (tid == 0) {
+      int d = -1;
+      if (ok) {
+        d = 0;
+        for (int node = end; node != 0; ++d) {
+          walk[d] = (int16_t)node;
+          const int p = up[node];
+          if (p < 0 || p >= node) {
+            d = -1;
+            break;
+          }
+          node = p;
+        }
+      }
+      depth_sh = d;
+    }
+  } else if (tid == 0) {
+    depth_sh = ok ? end : -1;
+  }
+  __syncthreads();
+  const int depth = depth_sh;
+  for (int d = tid; d <= depth; d += kMoveThreads) {
+    const int node = !parent ? d : d == 0 ? 0 : walk[depth - d];
+    const int64_t src = row_offset(c, b, len + node), dst = row_offset(c, b, len + d);
+    if (src < 0 || dst < 0) bad_sh = 1;
+    from[d] = src;
+    to[d] = dst;
+  }
+  __syncthreads();
+  ok = depth >= 0 && bad_sh == 0;
+  if (blockIdx.x == 0 && tid == 0) out_lens[b] = ok ? len + depth + 1 : len;
+  if (!ok || !parent) return;
+  const uint32_t x = blockIdx.x * kMoveThreads + tid;  // (layer, k or v, head, vector)
+  const uint32_t lk = fast_div(row_div, x);
+  const uint32_t y = x - lk * row_div.d;
+  const uint32_t h = fast_div(head_div, y);
+  if ((int)(lk >> 1) >= c.layers) return;
+  char* base = (lk & 1 ? c.v : c.k) + (int64_t)(lk >> 1) * c.layer_stride +
+               (int64_t)h * c.head_stride + (int64_t)(y - h * head_div.d) * 16;
+  int d0 = 1;
+  while (d0 <= depth && from[d0] == to[d0]) ++d0;
+  for (; d0 <= depth; d0 += 8) {
+    u32x4 r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (d0 + i <= depth) r[i] = *reinterpret_cast<const u32x4*>(base + from[d0 + i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (d0 + i <= depth) *reinterpret_cast<u32x4*>(base + to[d0 + i]) = r[i];
+  }
+}
+
+// ------------------------------------------------------------------------------- page pool
+// One workgroup: the counts of a full pool are at most a few hundred kilobytes, and each step
+// depends on the one before.
+
+struct PoolScan {
+  int wave[kPoolWaves];
+};
+
+// Exclusive prefix of one value a thread over the workgroup; total in *all.
+__device__ __forceinline__ int block_prefix(PoolScan& s, int x, int* all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(incl, d);
+    incl += lane >= d ? y : 0;
+  }
+  __syncthreads();
+  if (lane == 63) s.wave[wave] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kPoolWaves; ++i) {
+    before += i < wave ? s.wave[i] : 0;
+    total += s.wave[i];
+  }
+  *all = total;
+  return before + incl - x;
+}
+
+// Replaces the counts count[0..n) in LDS by their exclusive prefix sums;
+// returns the total.
+__device__ __forceinline__ int prefix_counts(PoolScan& s, int* count, int n) {
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += kPoolThreads) {
+    const int i = i0 + threadIdx.x;
+    int all;
+    const int p = block_prefix(s, i < n ? count[i] : 0, &all);
+    if (i < n) count[i] = base + p;
+    base += all;
+  }
+  __syncthreads();
+  return base;
+}
+
+// Largest i with prefix[i] <= r (prefix ascending, prefix[0] = 0): the owner of item r.
+__device__ __forceinline__ int owner_of(const int* prefix, int n, int r) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Calls take(rank, page) for the free pages of lowest index, rank < want; returns how many
+// there were (at most want).  16 pages a thread and round.
+template <class F>
+__device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, int want, F take) {
+  constexpr int kPer = 16;
+  const bool vec = (reinterpret_cast<uintptr_t>(c.refcount) & 15u) == 0;
+  int base = 0;
+  for (int64_t p0 = 0; p0 < c.pages && base < want; p0 += kPoolThreads * kPer) {
+    const int64_t p = p0 + (int64_t)threadIdx.x * kPer;
+    uint32_t free = 0;
+    if (vec && p + kPer <= c.pages) {
+      int4 x[kPer / 4];
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i)
+        x[i] = reinterpret_cast<const int4*>(c.refcount + p)[i];
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i)
+        free |= ((x[i].x == 0) | (x[i].y == 0) << 1 | (x[i].z == 0) << 2 | (x[i].w == 0) << 3)
+                << (4 * i);
+    } else {
+      for (int i = 0; i < kPer; ++i)
+        if (p + i < c.pages) free |= (c.refcount[p + i] == 0 ? 1u : 0u) << i;
+    }
+    int all;
+    int rank = base + block_prefix(s, __popc(free), &all);
+    while (free && rank < want) {
+      const int i = __ffs(free) - 1;
+      free &= free - 1;
+      take(rank++, (int)p + i);
+    }
+    base += all;
+  }
+  __threadfence_block();
+  __syncthreads();
+  return base < want ? base : want;
+}
+
+__global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const int32_t* want,
+                                                              const int32_t* new_lens,
+                                                              int32_t* out_ok) {
+  __shared__ int drop[kCacheMaxSeqs], grow[kCacheMaxSeqs];
+  __shared__ PoolScan s;
+  const int n = c.seqs;
+  // what each sequence gives back and takes; out_ok: 2 = leave alone and report 0
+  auto need_of = [&](int b, int held) {
+    const int w = want[b];
+    return w < 0 ? held : (int)fast_div(c.page_div, (uint32_t)w + c.page_div.d - 1);
+  };
+  for (int b = threadIdx.x; b < n; b += kPoolThreads) {
+    const int held = c.held[b], w = want[b];
+    bool ok = held >= 0 && held <= c.width;
+    int len = c.lens[b];
+    if (ok && new_lens) {
+      const int nl = new_lens[b];
+      ok = nl >= 0 && nl <= (int64_t)held * c.page_size;
+      if (ok) c.lens[b] = len = nl;
+    }
+    ok = ok && (w <= 0 || (w >= len && w <= c.cap));
+    const int need = ok ? need_of(b, held) : held;
+    drop[b] = need < held ? held - need : 0;
+    grow[b] = need > held ? need - held : 0;
+    out_ok[b] = ok ? 1 : 2;
+  }
+  __syncthreads();
+  const int dropped = prefix_counts(s, drop, n);
+  const int wanted = prefix_counts(s, grow, n);
+
+  for (int r = threadIdx.x; r < dropped; r += kPoolThreads) {
+    const int b = owner_of(drop, n, r);
+    const int j = need_of(b, c.held[b]) + r - drop[b];
+    const int page = c.table[(size_t)b * c.width + j];
+    if (page >= 0 && page < c.pages) atomicSub(&c.refcount[page], 1);
+  }
+  __threadfence();
+  __syncthreads();
+
+  const int got = for_free_pages(s, c, wanted, [&](int r, int page) {
+    const int b = owner_of(grow, n, r);
+    c.table[(size_t)b * c.width + c.held[b] + r - grow[b]] = page;
+    c.refcount[page] = 1;
+  });
+
+  // sequences are served in order until one does not fit; what that one was given goes back
+  for (int b = threadIdx.x; b < n; b += kPoolThreads) {
+    const int g = (b + 1 < n ? grow[b + 1] : wanted) - grow[b];
+    const int held = c.held[b];
+    int ok = out_ok[b] == 1;
+    if (ok && g > 0 && grow[b] + g > got) {
+      ok = 0;
+      for (int r = grow[b]; r < got; ++r)
+        c.refcount[c.table[(size_t)b * c.width + held + r - grow[b]]] = 0;
+    }
+    if (ok) {
+      c.held[b] = need_of(b, held);
+      if (want[b] == 0) c.lens[b] = 0;
+    }
+    out_ok[b] = ok;
+  }
+}
+
+__global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const int32_t* src,
+                                                            const int32_t* dst, int F,
+                                                            int32_t* out_ok) {
+  // first[s]: the first fork into slot s, F if none; bit 31: s is some fork's source
+  __shared__ uint32_t first[kCacheMaxSeqs];
+  __shared__ int count[kCacheMaxSeqs];
+  __shared__ PoolScan s;
+  for (int i = threadIdx.x; i < c.seqs; i += kPoolThreads) first[i] = (uint32_t)F;
+  __syncthreads();
+  for (int f = threadIdx.x; f < F; f += kPoolThreads) {
+    const int d = dst[f];
+    if (d >= 0 && d < c.seqs) atomicMin(&first[d], (uint32_t)f);
+  }
+  __syncthreads();
+  for (int f = threadIdx.x; f < F; f += kPoolThreads) {
+    const int x = src[f];
+    if (x >= 0 && x < c.seqs) atomicOr(&first[x], 0x80000000u);
+  }
+  __syncthreads();
+  // a fork needs a page where its source's last page is begun
+  for (int f = threadIdx.x; f < F; f += kPoolThreads) {
+    const int x = src[f], d = dst[f];
+    bool ok = x >= 0 && x < c.seqs && d >= 0 && d < c.seqs;
+    // into an empty slot that is no fork's source, and by its first fork
+    ok = ok && first[d] == (uint32_t)f && c.held[d] == 0;
+    bool part = false;
+    if (ok) {
+      const int len = c.lens[x], held = c.held[x];
+      ok = len >= 0 && held >= 0 && held <= c.width && len <= (int64_t)held * c.page_size;
+      const int full = ok ? (int)fast_div(c.page_div, (uint32_t)len) : 0;
+      part = ok && len != full * c.page_size;
+      if (part) {
+        const int page = c.table[(size_t)x * c.width + full];
+        ok = page >= 0 && page < c.pages;
+        part = ok;
+      }
+    }
+    count[f] = part ? 1 : 0;
+    out_ok[f] = ok ? 1 : 0;
+  }
+  __syncthreads();
+  const int wanted = prefix_counts(s, count, F);
+  const int got = for_free_pages(s, c, wanted, [&](int r, int page) {
+    const int f = owner_of(count, F, r);
+    c.table[(size_t)dst[f] * c.width + fast_div(c.page_div, (uint32_t)c.lens[src[f]])] = page;
+    c.refcount[page] = 1;
+  });
+  // forks without a page fail; the others share the full pages
+  for (int f0 = 0; f0 < F; f0 += kPoolThreads) {
+    const int f = f0 + threadIdx.x;
+    int full = 0;
+    bool ok = f < F && out_ok[f] == 1;
+    int part = 0;
+    if (ok) {
+      part = (f + 1 < F ? count[f + 1] : wanted) - count[f];
+      ok = part == 0 || count[f] < got;
+      full = ok ? (int)fast_div(c.page_div, (uint32_t)c.lens[src[f]]) : 0;
+    }
+    __syncthreads();  // count[f + 1] of the last thread is read before it is replaced
+    if (f < F) {
+      out_ok[f] = ok ? 1 : 0;
+      if (ok) {
+        c.held[dst[f]] = full + part;
+        c.lens[dst[f]] = c.lens[src[f]];
+      }
+      count[f] = full;
+    }
+    __syncthreads();
+  }
+  const int shared = prefix_counts(s, count, F);
+  for (int r = threadIdx.x; r < shared; r += kPoolThreads) {
+    const int f = owner_of(count, F, r), j = r - count[f];
+    const int page = c.table[(size_t)src[f] * c.width + j];
+    c.table[(size_t)dst[f] * c.width + j] = page;
+    if (page >= 0 && page < c.pages) atomicAdd(&c.refcount[page], 1);
+  }
+}
+
+// Copies the begun page of every fork: workgroup (layer and k or v, fork).
+__global__ __launch_bounds__(kMoveThreads) void k_fork_copy(CacheView c, const int32_t* src,
+                                                            const int32_t* dst,
+                                                            const int32_t* ok, FastDiv row_div,
+                                                            FastDiv head_div) {
+  const int f = blockIdx.y;
+  if (ok[f] != 1) return;
+  const int x = src[f], y = dst[f], len = c.lens[x];
+  const int full = (int)fast_div(c.page_div, (uint32_t)len);
+  const int rest = len - full * c.page_size;
+  if (rest == 0) return;
+  const int64_t from = (int64_t)c.table[(size_t)x * c.width + full] * c.page_stride;
+  const int64_t to = (int64_t)c.table[(size_t)y * c.width + full] * c.page_stride;
+  char* base = (blockIdx.x & 1 ? c.v : c.k) + (int64_t)(blockIdx.x >> 1) * c.layer_stride;
+  const uint32_t all = (uint32_t)rest * row_div.d;
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < all; i += kMoveThreads) {
+    const uint32_t row = fast_div(row_div, i), z = i - row * row_div.d;
+    const uint32_t h = fast_div(head_div, z);
+    const int64_t at = (int64_t)row * c.token_stride + (int64_t)h * c.head_stride +
+                       (int64_t)(z - h * head_div.d) * 16;
+    *reinterpret_cast<u32x4*>(base + to + at) = *reinterpret_cast<const u32x4*>(base + from + at);
+  }
+}
+
+int head_vecs(const CacheView& c) { return c.head_dim * c.esize / 16; }
+
+}  // namespace
+
+hipError_t launch_cache_append(const CacheView& c, const char* k_new, const char* v_new,
+                               int64_t new_seq, int64_t new_node, int64_t new_head,
+                               const int32_t* nodes, int N, hipStream_t stream) {
+  const int hv = head_vecs(c), rv = hv * c.kv_heads;
+  const unsigned blocks = (unsigned)(((int64_t)N * rv + kMoveThreads - 1) / kMoveThreads);
+  hipLaunchKernelGGL(k_append, dim3(blocks, c.seqs), dim3(kMoveThreads), 0, stream, c, k_new,
+                     v_new, new_seq, new_node, new_head, nodes, N, make_fast_div(rv),
+                     make_fast_div(hv));
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_commit(const CacheView& c, const int32_t* parent, const int32_t* last,
+                               int N, int32_t* out_lens, hipStream_t stream) {
+  const int hv = head_vecs(c), rv = hv * c.kv_heads;
+  const int64_t cols = parent ? (int64_t)c.layers * 2 * rv : 1;
+  const unsigned blocks = (unsigned)((cols + kMoveThreads - 1) / kMoveThreads);
+  hipLaunchKernelGGL(k_commit, dim3(blocks, c.seqs), dim3(kMoveThreads), 0, stream, c, parent,
+                     last, N, out_lens, make_fast_div(rv), make_fast_div(hv));
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_resize(const CacheView& c, const int32_t* want, const int32_t* new_lens,
+                               int32_t* out_ok, hipStream_t stream) {
+  hipLaunchKernelGGL(k_pool_resize, dim3(1), dim3(kPoolThreads), 0, stream, c, want, new_lens,
+                     out_ok);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_fork(const CacheView& c, const int32_t* src, const int32_t* dst, int F,
+                             int32_t* out_ok, hipStream_t stream) {
+  hipLaunchKernelGGL(k_pool_fork, dim3(1), dim3(kPoolThreads), 0, stream, c, src, dst, F, out_ok);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int hv = head_vecs(c), rv = hv * c.kv_heads;
+  hipLaunchKernelGGL(k_fork_copy, dim3(2 * c.layers, F), dim3(kMoveThreads), 0, stream, c, src,
+                     dst, out_ok, make_fast_div(rv), make_fast_div(hv));
+  return hipGetLastError();
+}
+
+}  // namespace sv
