@@ -23,6 +23,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_cache.hpp"
 
@@ -39,6 +40,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLn2 = 0.69314718055994530942f;
 
 #define SV_LDS(T) __attribute__((address_space(3))) T
+#define SV_GLOBAL(T) __attribute__((address_space(1))) T
 
 // max / sum with the lane 32 away
 __device__ __forceinline__ float half_max(float x) {
@@ -106,34 +108,49 @@ __device__ __forceinline__ bool clear_non_finite(u32x4& x) {
   return any;
 }
 
-// WM waves share the rows (32 each), WK the keys of a tile (KS blocks of 32 each).
-template <bool BF16, int D, int WM, int WK, int KS>
+// WM waves share the rows (RB blocks of 32 each), WK the keys of a tile (KS blocks of 32 each);
+// NST tiles are kept in LDS, loaded there directly from global memory.
+template <bool BF16, int D, int WM, int WK, int KS, int RB, int NST>
 struct Attn {
   static constexpr int kES = BF16 ? 2 : 4;
   static constexpr int kNW = WM * WK;
   static constexpr int kNT = 64 * kNW;
-  static constexpr int kMT = 32 * WM;
+  static constexpr int kMT = 32 * WM * RB;
   static constexpr int kBN = 32 * WK * KS;
-  static constexpr int kRow = D * kES;        // bytes of a row
+  static constexpr int kRow = D * kES;        // bytes of a row, in memory and in LDS
   static constexpr int kVecs = kRow / 16;     // 16-byte vectors of a row
-  // Row pitches in LDS.  K is read 16 bytes a lane down 32 rows: a pitch of an odd number of
-  // 16-byte units spreads 16 rows over all 64 banks.  V (bf16) is read 64 bytes wide over 4
-  // rows: a pitch of 64 bytes mod 128 puts those in different banks; V (fp32) is read 128 bytes
-  // wide in two rows 4 apart: a pitch of 32 bytes mod 64.
-  static constexpr int kPitchK = kRow + 16;
-  static constexpr int kPitchV = BF16 ? (kRow % 128 == 0 ? kRow + 64 : kRow) : kRow + 32;
   static constexpr int kND = D / 32;
-  static constexpr int kLoads = kBN * kVecs / kNT;  // vectors a thread stages per tensor
-  static constexpr int kTileBytes = kBN * (kPitchK + kPitchV);
+  static constexpr int kLoads = kBN * kVecs / kNT;  // vectors a thread loads per tensor
+  static constexpr int kTileBytes = 2 * kBN * kRow;
   static constexpr int kJoinBytes = WK > 1 ? kNW * kND * 16 * 64 * 4 : 0;
-  static constexpr int kPool = kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes;
+  static constexpr int kPool = NST * kTileBytes > kJoinBytes ? NST * kTileBytes : kJoinBytes;
   static_assert(D % 32 == 0 && (kBN * kVecs) % kNT == 0 && kBN % 64 == 0 && kBN <= kNT, "tile");
+  static_assert(RB == 1 || WK == 1, "waves join one block of rows");
+
+  // Direct loads fill LDS in lane order, so rows are not padded; instead vector c of row r lies
+  // at place c ^ swz(r) of its row, which a lane gets by loading that vector.
+  // K is read 16 bytes a lane down 32 rows: 16 consecutive rows have to cover all 64 banks (16
+  // places of 16 bytes).  V (bf16) is read 64 bytes wide from 4 consecutive rows at once: those
+  // have to lie in four different quarters of the banks.  V (fp32) is read 128 bytes wide, and
+  // the matrix instructions take 16 times as long: no swizzle.
+  __device__ static __forceinline__ int swz_k(int r) {
+    if constexpr (kRow % 256 == 0) return r & 15;
+    else if constexpr (kRow == 128) return (r >> 1) & 7;
+    else return (r >> 2) & 3;  // 192, 384: the pitch itself spreads 4 (2) rows
+  }
+  __device__ static __forceinline__ int swz_v(int r) {
+    if constexpr (!BF16) return 0;
+    else if constexpr (kRow % 256 == 0) return (r & 3) * 4;
+    else if constexpr (kRow == 128) return (r >> 1 & 1) * 4;
+    else return 0;             // 192: the pitch itself spreads 4 rows
+  }
 
   struct Lds {
-    alignas(16) char pool[kPool];          // K tile, V tile; the parts when waves join
-    long long rowoff[2][kBN];              // byte offset of a key's row, -1: no such row
-    uint32_t valid[2][kBN / 32];           // keys that exist
-    uint32_t badv[2][kBN / 32];            // drafted nodes with non-finite values
+    alignas(1024) char pool[kPool];        // NST times (K tile, V tile); the parts when waves join
+    long long rowoff[4][kBN];              // byte offset of a key's row (that of page 0: none)
+    uint32_t valid[4][kBN / 32];           // keys that exist
+    uint32_t badv[4][kBN / 32];            // drafted nodes with non-finite values
+    uint32_t sees[kMT][kBN / 32];          // keys of a rough tile that a node sees
     float m[kNW][32], l[kNW][32];
     long long scan[kNW + 1];
     long long start_off;
@@ -141,16 +158,46 @@ struct Attn {
   };
 };
 
-template <bool BF16, int D, int WM, int WK, int KS, int OCC>
-__global__ __launch_bounds__(64 * WM * WK, OCC) void k_tree_attn(AttnArgs a) {
-  using C = Attn<BF16, D, WM, WK, KS>;
+// A value the compiler takes for a new one: what is computed from it in a loop is computed there
+// and does not occupy registers all along.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// 16 bytes a lane from global memory to LDS at `to` (uniform) + 16 * lane.  In assembly because
+// the compiler would wait for it before every LDS read it cannot tell apart; the kernel waits
+// where it has to (tile_barrier).  No register is written.
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(from), "s"(to)
+               : "memory");
+}
+
+// Waits for this wave's loads to LDS, then for the other waves'.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Waits for this wave's LDS accesses, then for the other waves'; loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <bool BF16, int D, int WM, int WK, int KS, int RB, int NST, int OCC>
+__global__ __launch_bounds__(64 * WM * WK) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+void k_tree_attn(AttnArgs a) {
+  using C = Attn<BF16, D, WM, WK, KS, RB, NST>;
   constexpr int MT = C::kMT, BN = C::kBN, NT = C::kNT, ND = C::kND;
   constexpr int QF = BF16 ? D / 16 : D / 8;  // 16-byte pieces of a Q row a lane holds
   __shared__ typename C::Lds S;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wk = wave / WM;
   const int half = lane >> 5, col = lane & 31;
   const float sl2 = a.scale * 1.44269504088896340736f;  // scores to log2 units
+  const uint32_t pool_at = (uint32_t)reinterpret_cast<uintptr_t>((SV_LDS(char)*)S.pool);
 
   // worker number: consecutive workers share keys and should share an XCD's L2 (workgroups are
   // handed to the eight XCDs in turn)
@@ -235,274 +282,401 @@ __global__ __launch_bounds__(64 * WM * WK, OCC) void k_tree_attn(AttnArgs a) {
     const long long left = end - pos;
     const int t1 = (long long)(sw.tiles - t0) < left ? sw.tiles : t0 + (int)left;
     const int rows = sw.n * a.G;             // live rows of the (sequence, kv head)
-    const int my_row = mt * MT + wm * 32 + col;
-    const int my_node = my_row / a.G, my_g = my_row - my_node * a.G;
-    const bool row_live = my_row < rows;
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     const char* kbase = a.c.k + (long long)h * a.c.head_stride;
     const char* vbase = a.c.v + (long long)h * a.c.head_stride;
-
-    u32x4 qf[QF];
-    {
-      const char* qp = a.q + (long long)b * a.q_seq + (long long)my_node * a.q_node +
-                       (long long)(h * a.G + my_g) * a.q_head + half * 16;
+    // live nodes of the row tile, and the node of each row of this lane (dead rows: the last one;
+    // what they compute is dropped)
+    const int first_node = mt * MT / a.G;
+    const int last_node = (rows < (mt + 1) * MT ? sw.n : ((mt + 1) * MT - 1) / a.G + 1) - 1;
+    int my_node[RB];
+    u32x4 qf[RB][QF];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int row = mt * MT + (wm * RB + rb) * 32 + col;
+      const bool row_live = row < rows;
+      const int node = row_live ? row / a.G : last_node, g = row - node * a.G;
+      my_node[rb] = node;
+      const char* qp = a.q + (long long)b * a.q_seq + (long long)node * a.q_node +
+                       (long long)(h * a.G + g) * a.q_head + half * 16;
 #pragma unroll
       for (int s = 0; s < QF; ++s)
-        qf[s] = row_live ? *reinterpret_cast<const u32x4*>(qp + s * 32) : u32x4{0, 0, 0, 0};
+        qf[rb][s] = row_live ? *reinterpret_cast<const u32x4*>(qp + s * 32)
+                                      : u32x4{0, 0, 0, 0};
     }
 
+    // row that this thread's vector of pass i belongs to (a pass covers whole rows, or not)
+    auto row_of = [&](int i) {
+      return NT % C::kVecs == 0 ? tid / C::kVecs + i * (NT / C::kVecs)
+                                : (tid + i * NT) / C::kVecs;
+    };
     auto load_entry = [&](int t) -> int {  // page of key t * BN + tid, -1: none
-      const int key = t * BN + tid;
+      const int key = t * BN + fresh(tid);
       if (tid >= BN || key >= sw.keys) return -1;
       return table[fast_div(a.c.page_div, (uint32_t)key)];
     };
     auto put_rows = [&](int t, int page) {
       if (tid < BN) {
-        const int key = t * BN + tid;
+        const int key = t * BN + fresh(tid);
         const bool ok = page >= 0 && page < a.c.pages;
         const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
         const int slot = key - (int)(pi * a.c.page_div.d);
-        S.rowoff[t & 1][tid] = ok ? (long long)page * a.c.page_stride +
+        S.rowoff[t & 3][tid] = ok ? (long long)page * a.c.page_stride +
                                         (long long)slot * a.c.token_stride
-                                  : -1ll;
+                                  : 0ll;
         const unsigned long long bits = __ballot(ok);
         if (lane == 0) {
-          S.valid[t & 1][(tid >> 5)] = (uint32_t)bits;
-          S.valid[t & 1][(tid >> 5) + 1] = (uint32_t)(bits >> 32);
-          S.badv[t & 1][(tid >> 5)] = 0u;
-          S.badv[t & 1][(tid >> 5) + 1] = 0u;
+          S.valid[t & 3][(tid >> 5)] = (uint32_t)bits;
+          S.valid[t & 3][(tid >> 5) + 1] = (uint32_t)(bits >> 32);
+          S.badv[t & 3][(tid >> 5)] = 0u;
+          S.badv[t & 3][(tid >> 5) + 1] = 0u;
         }
       }
     };
-    u32x4 kr[C::kLoads], vr[C::kLoads];
-    uint32_t missing = 0;  // bit i: vector i's row does not exist (its load reads page 0)
-    auto issue = [&](int t) {
-      missing = 0;
+    // Loads of tile t into LDS, 1 KB per wave, instruction and tensor: the row offsets of its
+    // kLoads passes, then pass i.
+    long long at_row[C::kLoads];
+    auto find_rows = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) {
-        const int x = tid + i * NT, r = x / C::kVecs, cv = x - r * C::kVecs;
-        const long long o = S.rowoff[t & 1][r];
-        missing |= (o < 0 ? 1u : 0u) << i;
-        const long long at = (o < 0 ? 0 : o) + cv * 16;
-        kr[i] = *reinterpret_cast<const u32x4*>(kbase + at);
-        vr[i] = *reinterpret_cast<const u32x4*>(vbase + at);
-      }
+      for (int i = 0; i < C::kLoads; ++i) at_row[i] = S.rowoff[t & 3][row_of(i)];
     };
-    auto stage = [&](int t) {
-      if (__any(missing != 0)) {
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-          const uint32_t keep = (missing >> i & 1u) - 1u;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            kr[i][j] &= keep;
-            vr[i][j] &= keep;
+    auto issue = [&](int t, int i) {
+      const uint32_t to =
+          pool_at + (NST > 1 ? (t & 1) * C::kTileBytes : 0) + wave * 1024 + i * (NT * 16);
+      const int r = row_of(i), p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
+      load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to);
+      load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow);
+    };
+    // A tile that ends behind the committed tokens or holds keys that do not exist: their values
+    // are cleared, and non-finite values of drafted nodes, which may be hidden from some rows
+    // (0 * inf must not reach them), are set aside.
+    auto mend = [&](int t) {
+      char* vt = S.pool + (NST > 1 ? (t & 1) * C::kTileBytes : 0) + BN * C::kRow;
+      const int x0 = fresh(tid);
+#pragma unroll 1
+      for (int i = 0; i < C::kLoads; ++i) {
+        const int x = x0 + i * NT, r = x / C::kVecs;
+        u32x4* p = reinterpret_cast<u32x4*>(vt + x * 16);
+        if (!(S.valid[t & 3][r >> 5] >> (r & 31) & 1u)) {
+          *p = u32x4{0, 0, 0, 0};
+        } else if (t * BN + r >= sw.len) {
+          u32x4 y = *p;
+          if (clear_non_finite<BF16>(y)) {
+            *p = y;
+            atomicOr(&S.badv[t & 3][r >> 5], 1u << (r & 31));
           }
         }
       }
-      // a node's values may be hidden from some rows: 0 * inf must not reach them
-      if ((t + 1) * BN > sw.len) {
+      // which keys a node sees: a wave takes a node and 64 keys at a time, eight loads in flight
+      // (of a key that is no node or a node past the tile's last, those of its nearest one)
+#pragma unroll 1
+      for (int k0 = 0; k0 < BN; k0 += 64) {
+        const int node = t * BN + k0 + fresh(lane) - sw.len;
+        const int near = node < 0 ? 0 : node < a.N ? node : a.N - 1;
+        const unsigned long long there =
+            S.valid[t & 3][k0 / 32] | (unsigned long long)S.valid[t & 3][k0 / 32 + 1] << 32;
+#pragma unroll 1
+        for (int r0 = wave; first_node + r0 <= last_node; r0 += 8 * C::kNW) {
+          uint8_t shown[8];
 #pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) {
-          const int r = (tid + i * NT) / C::kVecs;
-          if (t * BN + r >= sw.len && clear_non_finite<BF16>(vr[i]))
-            atomicOr(&S.badv[t & 1][r >> 5], 1u << (r & 31));
+          for (int i = 0; i < 8; ++i) {
+            const int me = first_node + r0 + i * C::kNW;
+            shown[i] = me >= near;
+            if (a.mask) {
+              const int row = me < last_node ? me : last_node;
+              shown[i] = a.mask[((size_t)b * a.N + row) * a.N + near];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const unsigned long long bits = __ballot(shown[i] != 0 || node < 0) & there;
+            const int row = r0 + i * C::kNW;
+            if (lane < 2 && first_node + row <= last_node)
+              S.sees[row][k0 / 32 + lane] = (uint32_t)(bits >> (32 * lane));
+          }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) {
-        const int x = tid + i * NT, r = x / C::kVecs, cv = x - r * C::kVecs;
-        *reinterpret_cast<u32x4*>(S.pool + r * C::kPitchK + cv * 16) = kr[i];
-        *reinterpret_cast<u32x4*>(S.pool + BN * C::kPitchK + r * C::kPitchV + cv * 16) = vr[i];
       }
     };
 
-    float m = -INFINITY, l = 0.0f;
-    f32x16 acc[ND];
+    float m[RB], l[RB];
+    f32x16 acc[RB][ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int rb = 0; rb < RB; ++rb) {
+      m[rb] = -INFINITY;
+      l[rb] = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[rb][d][r] = 0.0f;
+    }
 
-    put_rows(t0, load_entry(t0));
-    int entry = t0 + 1 < t1 ? load_entry(t0 + 1) : -1;
-    __syncthreads();
-    issue(t0);
-
-    for (int t = t0; t < t1; ++t) {
-      __syncthreads();  // the waves are done with the last tile
-      stage(t);
-      if (t + 1 < t1) put_rows(t + 1, entry);
-      __syncthreads();
-      if (t + 1 < t1) issue(t + 1);
-      entry = t + 2 < t1 ? load_entry(t + 2) : -1;
-
+    // One tile: scores of this wave's keys, softmax, product with the values.  `Rough` tiles hold
+    // keys that do not exist or drafted nodes; the others need no masks.
+    auto step = [&](int t, auto rough) {
+      constexpr bool Rough = decltype(rough)::value;
+      const char* tile = S.pool + (NST > 1 ? (t & 1) * C::kTileBytes : 0);
+      // scores: lane = row, register r = key 8 (r / 4) + 4 half + r % 4.  LDS reads run kAhead
+      // fragments ahead of the matrix instructions (the order is pinned: left alone, the
+      // compiler waits for each read)
+      constexpr int kAhead = 4, kKeyFrags = KS * QF;
+      constexpr int kPace = kKeyFrags / C::kLoads > 0 ? kKeyFrags / C::kLoads : 1;
+      static_assert(NST == 1 || kKeyFrags >= C::kLoads, "a pass per fragment at most");
+      f32x16 s[KS][RB];
+      const int kr = wk * KS * 32 + col;
+      const char* kp = tile + kr * C::kRow;
+      const int sw_k = C::swz_k(kr);  // the same for every block of 32 keys
+      auto key_frag = [&](int n) {
+        return *reinterpret_cast<const u32x4*>(kp + n / QF * (32 * C::kRow) +
+                                               (((2 * (n % QF) + half) ^ sw_k) * 16));
+      };
+      u32x4 kf[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) kf[n] = key_frag(n);
       __builtin_amdgcn_sched_barrier(0);
-      // scores of this wave's keys: lane = row, register r = key 8 (r / 4) + 4 half + r % 4
-      f32x16 s[KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const char* kp = S.pool + ((wk * KS + ks) * 32 + col) * C::kPitchK + half * 16;
+      for (int n = 0; n < kKeyFrags; ++n) {
+        const int ks = n / QF, q = n % QF;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[ks][r] = 0.0f;
+        for (int rb = 0; rb < RB; ++rb) {
+          if (q == 0)
 #pragma unroll
-        for (int q = 0; q < QF; ++q) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(kp + q * 32);
+            for (int r = 0; r < 16; ++r) s[ks][rb][r] = 0.0f;
           if constexpr (BF16) {
-            s[ks] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, kf), __builtin_bit_cast(bf16x8, qf[q]), s[ks], 0, 0, 0);
+            s[ks][rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, kf[n % kAhead]), __builtin_bit_cast(bf16x8, qf[rb][q]),
+                s[ks][rb], 0, 0, 0);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[ks] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                  __uint_as_float(kf[e]), __uint_as_float(qf[q][e]), s[ks], 0, 0, 0);
+              s[ks][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                  __uint_as_float(kf[n % kAhead][e]), __uint_as_float(qf[rb][q][e]), s[ks][rb],
+                  0, 0, 0);
           }
         }
+        if (n + kAhead < kKeyFrags) kf[n % kAhead] = key_frag(n + kAhead);
+        // the next tile's loads start in the shadow of these products
+        if (NST > 1 && n % kPace == 0 && n / kPace < C::kLoads && t + 1 < t1)
+          issue(t + 1, n / kPace);
+        __builtin_amdgcn_sched_barrier(0);
       }
 
-      __builtin_amdgcn_sched_barrier(0);  // keeps the phases' registers apart
-      // hide keys that do not exist and nodes that the row does not see
-      uint32_t seen[KS];
+      // hide keys that the row does not see
+      uint32_t seen[KS][RB];
+      if constexpr (Rough) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int blk = wk * KS + ks, key0 = t * BN + blk * 32;
-        const uint32_t have = S.valid[t & 1][blk];
-        seen[ks] = 0xFFFFu;
-        if (have != 0xFFFFFFFFu || key0 + 32 > sw.len) {
-          // bit r of `bits`: the row sees register r's key.  Nodes: node0 is that of register 0
-          const int node0 = key0 + 4 * half - sw.len;
-          const int me = row_live ? my_node : 0;
-          uint32_t bits = 0;
-          if (a.mask) {
-            const uint8_t* mrow = a.mask + ((size_t)b * a.N + me) * a.N;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int node = node0 + 8 * (r >> 2) + (r & 3);
-              const int at = node < 0 ? 0 : node < a.N ? node : a.N - 1;
-              bits |= (mrow[at] != 0 || node < 0 ? 1u : 0u) << r;
-            }
-          } else {
-            const int lim = me - node0;  // the last key offset that a chain's node sees
-            bits = of_half(lim < 0 ? 0u : lim > 30 ? 0xFFFFFFFFu : (2u << lim) - 1u);
+          for (int rb = 0; rb < RB; ++rb) {
+            const uint32_t bits = of_half(
+                S.sees[my_node[rb] - first_node][wk * KS + ks] >> (4 * half));
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              s[ks][rb][r] = bits & (1u << r) ? s[ks][rb][r] : -INFINITY;
+            seen[ks][rb] = bits;
           }
-          bits &= of_half(have >> (4 * half));
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[ks][r] = bits & (1u << r) ? s[ks][r] : -INFINITY;
-          seen[ks] = bits;
-        }
       }
 
       // running maximum in units of log2 (z log2 e, so that P and every later rescaling use the
       // same rounded number); P = exp(z - m); O and l rescaled when the maximum grew
-      float mx = s[0][0];
+      float shift[RB];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int rb = 0; rb < RB; ++rb) {
+        float mx = s[0][rb][0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[ks][r]);
-      const float m_new = fmaxf(m, half_max(mx) * sl2);
-      const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-      if (__any(m_new > m)) {
-        const float f = __builtin_amdgcn_exp2f(m - m_use);
-        l *= f;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[ks][rb][r]);
+        const float m_new = fmaxf(m[rb], half_max(mx) * sl2);
+        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+        if (__any(m_new > m[rb])) {
+          const float f = __builtin_amdgcn_exp2f(m[rb] - m_use);
+          l[rb] *= f;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[d][r] *= f;
-        m = m_new;
-      }
-      float sum = 0.0f;
+          for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[ks][r] = __builtin_amdgcn_exp2f(s[ks][r] * sl2 - m_use);
-          sum += s[ks][r];
+            for (int r = 0; r < 16; ++r) acc[rb][d][r] *= f;
+          m[rb] = m_new;
         }
-      l += sum;
+        shift[rb] = m_use;
+      }
+      // P of registers [8 j + r0, 8 j + r0 + n) of the wave's 16 KS keys a lane
+      auto weigh = [&](int j, int r0, int n) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int r = r0; r < r0 + n; ++r) {
+            const int i = 8 * (j & 1) + r;
+            s[j >> 1][rb][i] = __builtin_amdgcn_exp2f(s[j >> 1][rb][i] * sl2 - shift[rb]);
+            l[rb] += s[j >> 1][rb][i];
+          }
+      };
 
-      __builtin_amdgcn_sched_barrier(0);
       // O^T += V^T P^T
+      const char* vp = tile + BN * C::kRow + wk * KS * 32 * C::kRow;
+      if constexpr (BF16) {
+        // 16 lanes read 4 keys x 16 columns; lane i supplies row i / 4, 8 bytes i % 4.  The
+        // swizzle moves 64-byte pieces and depends on the row's two lowest bits alone
+        const int vr = 4 * half + ((lane & 15) >> 2);
+        const char* vt = vp + vr * C::kRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        const int sw_v = C::swz_v(vr) * 16;
+        typedef short short8v __attribute__((ext_vector_type(8)));
+        auto value_frag = [&](int n) {  // 16 keys n / ND, columns 32 (n % ND) and up
+          const char* at = vt + n / ND * (16 * C::kRow) + ((n % ND * 64) ^ sw_v);
+          const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)at);
+          const short4v hi =
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)(at + 8 * C::kRow));
+          return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        constexpr int kChunks = 2 * KS, kFrags = kChunks * ND;
+        short8v vf[kAhead];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) vf[n] = value_frag(n);
+        weigh(0, 0, 8);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          // P rounded to bf16 for the matrix instruction: half a step of 2^-8 per weight, the
+          // rounding the inputs carry; the sum l keeps the unrounded weights
+          bf16x8 pf[RB];
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pf[rb][i] = (__bf16)s[j >> 1][rb][8 * (j & 1) + i];
+          // the next keys' weights are computed in the shadow of these products
+          constexpr int kShare = (8 + ND - 1) / ND;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const int n = j * ND + d;
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+              acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf[rb], acc[rb][d], 0, 0, 0);
+            if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(n + kAhead);
+            if (j + 1 < kChunks && d * kShare < 8)
+              weigh(j + 1, d * kShare, 8 - d * kShare < kShare ? 8 - d * kShare : kShare);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2 * KS; ++j) weigh(j, 0, 8);
+        auto value_frag = [&](int n) {  // key register n / ND, columns 32 (n % ND) and up
+          const int r = n / ND;
+          return *reinterpret_cast<const float*>(
+              vp + (8 * (r >> 2) + 4 * half + (r & 3)) * C::kRow + col * 4 + n % ND * 128);
+        };
+        constexpr int kFrags = 16 * KS * ND;
+        float vf[kAhead];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) vf[n] = value_frag(n);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kFrags; ++n) {
+          const int r = n / ND, d = n % ND;
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+            acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf[n % kAhead],
+                                                              s[r >> 4][rb][r & 15], acc[rb][d],
+                                                              0, 0, 0);
+          if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(n + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const int blk = wk * KS + ks;
-        const char* vp = S.pool + BN * C::kPitchK + blk * 32 * C::kPitchV;
-        if constexpr (BF16) {
-          // P rounded to bf16 for the matrix instruction: half a step of 2^-8 per weight, the
-          // rounding the inputs carry; the sum l keeps the unrounded weights
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            bf16x8 pf;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) pf[j] = (__bf16)s[ks][8 * c + j];
-            // 16 lanes read 4 keys x 16 columns; lane i supplies row i / 4, 8 bytes i % 4
-            const char* vt = vp + (16 * c + 4 * half + ((lane & 15) >> 2)) * C::kPitchV +
-                             ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (SV_LDS(short4v)*)(vt + d * 64));
-              const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (SV_LDS(short4v)*)(vt + 8 * C::kPitchV + d * 64));
-              typedef short short8v __attribute__((ext_vector_type(8)));
-              const short8v vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-              acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf), pf,
-                                                               acc[d], 0, 0, 0);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const char* vt = vp + (8 * (r >> 2) + 4 * half + (r & 3)) * C::kPitchV + col * 4;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-              acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                  *reinterpret_cast<const float*>(vt + d * 128), s[ks][r], acc[d], 0, 0, 0);
-          }
-        }
-
         // non-finite values of drafted nodes, for the rows that see them (rare: a rolled loop
         // over a copy of O in scratch memory keeps it out of the registers of the common path)
-        uint32_t bad = S.badv[t & 1][blk];
-        if (__builtin_expect(bad != 0, 0)) {
-          float o[ND * 16];
+        const uint32_t bad = Rough ? S.badv[t & 3][blk] : 0u;
+        if (Rough && __builtin_expect(bad != 0, 0)) {
 #pragma unroll
-          for (int i = 0; i < ND * 16; ++i) o[i] = acc[i >> 4][i & 15];
-          while (bad) {
-            const int kk = __builtin_amdgcn_readfirstlane(__ffs(bad) - 1);
-            bad &= bad - 1;
-            const int hk = (kk >> 2) & 1, rk = ((kk >> 3) << 2) | (kk & 3);
-            float p = 0.0f;
-            int sees = 0;
+          for (int rb = 0; rb < RB; ++rb) {
+            float o[ND * 16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              p = r == rk ? s[ks][r] : p;
-              sees = r == rk ? (int)(seen[ks] >> r & 1u) : sees;
-            }
-            p = __shfl(p, col + 32 * hk);
-            sees = __shfl(sees, col + 32 * hk);
-            const char* row = vbase + S.rowoff[t & 1][blk * 32 + kk];
+            for (int i = 0; i < ND * 16; ++i) o[i] = acc[rb][i >> 4][i & 15];
+            for (uint32_t left = bad; left; left &= left - 1) {
+              const int kk = __builtin_amdgcn_readfirstlane(__ffs(left) - 1);
+              const int hk = (kk >> 2) & 1, rk = ((kk >> 3) << 2) | (kk & 3);
+              float p = 0.0f;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) p = r == rk ? s[ks][rb][r] : p;
+              p = __shfl(p, col + 32 * hk);
+              const int sees = __shfl((int)(seen[ks][rb] >> rk & 1u), col + 32 * hk);
+              const char* row = vbase + S.rowoff[t & 3][blk * 32 + kk];
 #pragma unroll 1
-            for (int i = 0; i < ND * 16; ++i) {
-              const int e = (i >> 4) * 32 + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
-              float x;
-              if constexpr (BF16)
-                x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
-              else
-                x = reinterpret_cast<const float*>(row)[e];
-              if (sees && non_finite(__float_as_uint(x))) o[i] += p * x;
+              for (int i = 0; i < ND * 16; ++i) {
+                const int e = (i >> 4) * 32 + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
+                float x;
+                if constexpr (BF16)
+                  x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
+                else
+                  x = reinterpret_cast<const float*>(row)[e];
+                if (sees && non_finite(__float_as_uint(x))) o[i] += p * x;
+              }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < ND * 16; ++i) acc[i >> 4][i & 15] = o[i];
+            for (int i = 0; i < ND * 16; ++i) acc[rb][i >> 4][i & 15] = o[i];
+          }
+          __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) here: not in the common path's tiles
         }
       }
+    };
+
+    put_rows(t0, load_entry(t0));
+    if (t0 + 1 < t1) put_rows(t0 + 1, load_entry(t0 + 1));
+    int entry = t0 + 2 < t1 ? load_entry(t0 + 2) : -1;
+    __syncthreads();
+    auto issue_all = [&](int t) {
+      find_rows(t);
+#pragma unroll
+      for (int i = 0; i < C::kLoads; ++i) issue(t, i);
+    };
+    issue_all(t0);
+
+    // Turns to tile t: waits for it; true if it is rough.
+    auto turn = [&](int t) -> bool {
+      tile_barrier();  // tile t is there; the waves are done with the one before
+      if (NST > 1 && t + 1 < t1) find_rows(t + 1);
+      if (t + 2 < t1) {
+        put_rows(t + 2, entry);
+        entry = t + 3 < t1 ? load_entry(t + 3) : -1;
+      }
+      bool rough = (t + 1) * BN > sw.len;
+#pragma unroll
+      for (int i = 0; i < BN / 32; ++i) rough |= S.valid[t & 3][i] != 0xFFFFFFFFu;
+      return __builtin_amdgcn_readfirstlane(rough);
+    };
+    auto leave = [&](int t) {
+      if (NST == 1 && t + 1 < t1) {
+        lds_barrier();
+        issue_all(t + 1);
+      }
+    };
+    // plain tiles up to the first rough one (usually where the drafted nodes begin), then the
+    // rest as rough ones
+    int t = t0;
+    bool rough = turn(t);
+    while (!rough) {
+      step(t, std::false_type{});
+      leave(t);
+      if (++t == t1) break;
+      rough = turn(t);
+    }
+    while (t < t1) {
+      mend(t);
+      lds_barrier();
+      step(t, std::true_type{});
+      leave(t);
+      if (++t < t1) turn(t);
     }
 
     // ------------------------------------------------------------------ the part's result
-    l = half_sum(l);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) l[rb] = half_sum(l[rb]);
     if constexpr (WK > 1) {  // join the waves that share rows
-      if (half == 0) S.m[wave][col] = m;
-      if (half == 0) S.l[wave][col] = l;
+      if (half == 0) S.m[wave][col] = m[0];
+      if (half == 0) S.l[wave][col] = l[0];
       __syncthreads();
       float mt_all = -INFINITY;
 #pragma unroll
@@ -511,71 +685,80 @@ __global__ __launch_bounds__(64 * WM * WK, OCC) void k_tree_attn(AttnArgs a) {
       float lt = 0.0f;
 #pragma unroll
       for (int i = 0; i < WK; ++i)
-        lt += S.l[i * WM + wm][col] *
-              __builtin_amdgcn_exp2f(S.m[i * WM + wm][col] - mu);
-      const float f = __builtin_amdgcn_exp2f(m - mu);
+        lt += S.l[i * WM + wm][col] * __builtin_amdgcn_exp2f(S.m[i * WM + wm][col] - mu);
+      const float f = __builtin_amdgcn_exp2f(m[0] - mu);
       f32x4* box = reinterpret_cast<f32x4*>(S.pool);
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           box[((wave * ND + d) * 4 + r) * 64 + lane] =
-              f32x4{acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f,
-                    acc[d][4 * r + 3] * f};
+              f32x4{acc[0][d][4 * r] * f, acc[0][d][4 * r + 1] * f, acc[0][d][4 * r + 2] * f,
+                    acc[0][d][4 * r + 3] * f};
       __syncthreads();
-      m = mt_all;
-      l = lt;
+      m[0] = mt_all;
+      l[0] = lt;
     }
 
     const long long first = pos - t0;  // the group's first piece
     const bool whole = t0 == 0 && t1 == sw.tiles;
     const int slot = 2 * w + (pos == begin ? 0 : 1);
     const int hq = a.c.kv_heads * a.G;
-    const size_t orow = ((size_t)b * a.N + my_node) * hq + h * a.G + my_g;
-    const bool row_out = my_node < a.N;  // padding nodes get zeros
-    const float inv = !row_live || l == 0.0f ? 0.0f : 1.0f / l;
-    auto emit = [&](int d, int r4, f32x4 x) {
-      const int e = d * 32 + 8 * r4 + 4 * half;
-      if (whole) {
-        if (!row_out) return;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int fcol = fresh(col), fhalf = fresh(half);
+      const int row = mt * MT + (wm * RB + rb) * 32 + fcol;
+      const int node = row / a.G, g = row - node * a.G;
+      const bool row_live = row < rows;
+      const bool row_out = node < a.N;  // padding nodes get zeros
+      const size_t orow = ((size_t)b * a.N + node) * hq + h * a.G + g;
+      const size_t prow = (size_t)slot * MT + (wm * RB + rb) * 32 + fcol;
+      const float inv = !row_live || l[rb] == 0.0f ? 0.0f : 1.0f / l[rb];
+      char* op = a.out + orow * C::kRow + 4 * fhalf * C::kES;
+      float* pp = a.part + prow * D + 4 * fhalf;
+      // columns d * 32 + 8 r4 + 4 half and up of the row; a dead row's O may hold anything
+      auto emit_out = [&](int d, int r4, f32x4 x) {
         if (!row_live) x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (BF16) {
           bf16x4 y;
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] = (__bf16)(x[j] * inv);
-          *reinterpret_cast<bf16x4*>(a.out + orow * C::kRow + e * 2) = y;
+          *reinterpret_cast<bf16x4*>(op + (d * 32 + 8 * r4) * 2) = y;
         } else {
-          *reinterpret_cast<f32x4*>(a.out + orow * C::kRow + e * 4) = x * inv;
+          *reinterpret_cast<f32x4*>(op + (d * 32 + 8 * r4) * 4) = x * inv;
         }
-      } else if (row_live) {
-        *reinterpret_cast<f32x4*>(a.part + ((size_t)slot * MT + wm * 32 + col) * D + e) = x;
-      }
-    };
-    if constexpr (WK > 1) {
-      const f32x4* box = reinterpret_cast<const f32x4*>(S.pool);
-      for (int d = wk; d < ND; d += WK)
+      };
+      auto emit_part = [&](int d, int r4, f32x4 x) {
+        *reinterpret_cast<f32x4*>(pp + d * 32 + 8 * r4) = x;
+      };
+      auto each = [&](auto emit) {
+        if constexpr (WK > 1) {
+          const f32x4* box = reinterpret_cast<const f32x4*>(S.pool);
+          for (int d = wk; d < ND; d += WK)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          f32x4 x = box[((wm * ND + d) * 4 + r) * 64 + lane];
+            for (int r = 0; r < 4; ++r) {
+              f32x4 x = box[((wm * ND + d) * 4 + r) * 64 + lane];
 #pragma unroll
-          for (int i = 1; i < WK; ++i)
-            x += box[(((i * WM + wm) * ND + d) * 4 + r) * 64 + lane];
-          emit(d, r, x);
+              for (int i = 1; i < WK; ++i)
+                x += box[(((i * WM + wm) * ND + d) * 4 + r) * 64 + lane];
+              emit(d, r, x);
+            }
+        } else {
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              emit(d, r, f32x4{acc[rb][d][4 * r], acc[rb][d][4 * r + 1], acc[rb][d][4 * r + 2],
+                               acc[rb][d][4 * r + 3]});
         }
-    } else {
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          emit(d, r, f32x4{acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2],
-                           acc[d][4 * r + 3]});
-    }
-    if (wk == 0 && half == 0) {
+      };
       if (whole) {
-        if (a.lse && row_out)
-          a.lse[orow] = !row_live || l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+        if (row_out) each(emit_out);
+        if (wk == 0 && fhalf == 0 && a.lse && row_out)
+          a.lse[orow] = !row_live || l[rb] == 0.0f ? -INFINITY : m[rb] * kLn2 + logf(l[rb]);
       } else {
-        a.part_ml[(size_t)slot * MT + wm * 32 + col] = make_float2(m, l);
+        if (row_live) each(emit_part);
+        if (wk == 0 && fhalf == 0) a.part_ml[prow] = make_float2(m[rb], l[rb]);
       }
     }
     if (tid == 0 && t0 == 0 && !whole)
@@ -607,16 +790,35 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   if (node < n) {
     // parts: slot g.z, then slot 0 of each later worker
     auto slot_of = [&](int s) { return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s); };
-    for (int s = 0; s < g.w; ++s) m = fmaxf(m, a.part_ml[slot_of(s) * MT + row].x);
-    const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-    for (int s = 0; s < g.w; ++s) {
-      const float2 ml = a.part_ml[slot_of(s) * MT + row];
-      const float f = __builtin_amdgcn_exp2f(ml.x - mu);
-      const f32x4 y = *reinterpret_cast<const f32x4*>(a.part + (slot_of(s) * MT + row) * D + e);
-      l += ml.y * f;
-      x += y * f;
-    }
+    auto take = [&](int s0, auto count) {  // so many parts, all their loads in flight
+      constexpr int kCount = decltype(count)::value;
+      float2 ml[kCount];
+      f32x4 y[kCount];
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const size_t at = slot_of(s0 + i) * MT + row;
+        ml[i] = a.part_ml[at];
+        y[i] = *reinterpret_cast<const f32x4*>(a.part + at * D + e);
+      }
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) top = fmaxf(top, ml[i].x);
+      const float mu = top == -INFINITY ? 0.0f : top;
+      const float f = __builtin_amdgcn_exp2f(m - mu);
+      x *= f;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const float p = __builtin_amdgcn_exp2f(ml[i].x - mu);
+        l += ml[i].y * p;
+        x += y[i] * p;
+      }
+      m = top;
+    };
+    int s = 0;
+    for (; s + 8 <= g.w; s += 8) take(s, std::integral_constant<int, 8>{});
+    for (; s + 2 <= g.w; s += 2) take(s, std::integral_constant<int, 2>{});
+    if (s < g.w) take(s, std::integral_constant<int, 1>{});
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if constexpr (BF16) {
@@ -630,29 +832,34 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   if (a.lse && e == 0) a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-// Tile shapes: KS blocks of 32 keys a wave; OCC waves per SIMD that the registers must allow.
+// Tile shapes by row bytes and rows.  Rows of up to 256 bytes: two tiles of 64 keys fit beside
+// another workgroup's; longer ones: one tile, and the other workgroup computes while it loads.
 struct Shape {
-  int wm, wk, ks;
+  int wm, wk, ks, rb, nst, occ;
 };
-constexpr int kRowBytes1 = 256;  // rows up to this many bytes leave room for two workgroups
 
 template <bool BF16, int D>
 constexpr Shape shape_for(int row_tile) {
   constexpr int row = D * (BF16 ? 2 : 4);
-  if (row > 512) return Shape{2, 2, 1};
-  if (row_tile == 32) return Shape{1, 4, 1};
-  if (row_tile == 64) return Shape{2, 2, row > kRowBytes1 ? 1 : 2};
-  return Shape{4, 1, 2};
+  if (row > 512) return Shape{2, 2, 1, 1, 1, 1};
+  if (row > 256) {
+    if (row_tile == 32) return Shape{1, 2, 1, 1, 1, 1};
+    if (row_tile == 64) return D > 128 ? Shape{2, 1, 2, 1, 1, 1} : Shape{2, 2, 1, 1, 1, 2};
+    return Shape{4, 1, 2, 1, 1, 2};
+  }
+  if (row_tile == 32) return Shape{1, 4, 1, 1, 2, 1};
+  if (row_tile == 64) return Shape{2, 2, 1, 1, 2, 2};
+  if (row_tile == 128) return Shape{4, 1, 2, 1, 2, 2};
+  return Shape{4, 1, 2, 2, 2, 2};
 }
 
 template <bool BF16, int D, int RT>
 hipError_t launch_shape(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   constexpr Shape sh = shape_for<BF16, D>(RT);
-  constexpr int occ = D * (BF16 ? 2 : 4) > kRowBytes1 ? 1 : 2;
-  using C = Attn<BF16, D, sh.wm, sh.wk, sh.ks>;
+  using C = Attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.rb, sh.nst>;
   if (p.row_tile != C::kMT || p.key_tile != C::kBN) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_tree_attn<BF16, D, sh.wm, sh.wk, sh.ks, occ>), dim3(p.workers),
-                     dim3(C::kNT), 0, stream, a);
+  hipLaunchKernelGGL((k_tree_attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.rb, sh.nst, sh.occ>),
+                     dim3(p.workers), dim3(C::kNT), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.workers > 1)
@@ -667,6 +874,8 @@ hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
   else {
     if (p.row_tile == 32) return launch_shape<BF16, D, 32>(a, p, stream);
     if (p.row_tile == 64) return launch_shape<BF16, D, 64>(a, p, stream);
+    if constexpr (D * (BF16 ? 2 : 4) <= 256)
+      if (p.row_tile == 256) return launch_shape<BF16, D, 256>(a, p, stream);
     return launch_shape<BF16, D, 128>(a, p, stream);
   }
 }
@@ -698,14 +907,16 @@ AttnPlan plan_tree_attention(const CacheView& c, sv_dtype dt, int N, int G) {
   AttnPlan p{};
   const bool bf16 = dt == SV_DTYPE_BF16;
   const long long rows = (long long)N * G;
+  const int row_bytes = c.head_dim * c.esize;
   const int want = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const Shape sh = bf16 ? shape_of<true>(c.head_dim, want) : shape_of<false>(c.head_dim, want);
-  p.row_tile = 32 * sh.wm;
+  p.row_tile = 32 * sh.wm * sh.rb;
   p.key_tile = 32 * sh.wk * sh.ks;
   p.mts = (int)((rows + p.row_tile - 1) / p.row_tile);
-  // two workgroups fit a compute unit where a row has at most 256 bytes; no more workers than
-  // pieces of work the table has room for
-  const int per_cu = c.head_dim * c.esize > kRowBytes1 ? 1 : 2;
+  // workgroups that fit a compute unit's LDS; no more workers than pieces of work the table has
+  // room for
+  const int tile_bytes = 2 * p.key_tile * row_bytes * sh.nst;
+  const int per_cu = tile_bytes > 65536 ? 1 : 2;
   const long long most = (long long)c.seqs * c.kv_heads * p.mts *
                          (((long long)c.cap + p.key_tile - 1) / p.key_tile);
   p.workers = (int)(most < (long long)kAttnCus * per_cu ? most : (long long)kAttnCus * per_cu);
