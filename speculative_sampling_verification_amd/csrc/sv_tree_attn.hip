@@ -120,6 +120,7 @@ struct Attn {
   static constexpr int kRow = D * kES;        // bytes of a row, in memory and in LDS
   static constexpr int kVecs = kRow / 16;     // 16-byte vectors of a row
   static constexpr int kND = D / 32;
+  static constexpr int kRing = NST == 4 ? 8 : 4;  // tiles whose rows are known
   static constexpr int kLoads = kBN * kVecs / kNT;  // vectors a thread loads per tensor
   static constexpr int kTileBytes = 2 * kBN * kRow;
   static constexpr int kJoinBytes = WK > 1 ? kNW * kND * 16 * 64 * 4 : 0;
@@ -147,10 +148,11 @@ struct Attn {
 
   struct Lds {
     alignas(1024) char pool[kPool];        // NST times (K tile, V tile); the parts when waves join
-    long long rowoff[4][kBN];              // byte offset of a key's row (that of page 0: none)
-    uint32_t valid[4][kBN / 32];           // keys that exist
-    uint32_t badv[4][kBN / 32];            // drafted nodes with non-finite values
+    long long rowoff[kRing][kBN];          // byte offset of a key's row (that of page 0: none)
+    uint32_t valid[kRing][kBN / 32];       // keys that exist
+    uint32_t badv[kRing][kBN / 32];        // drafted nodes with non-finite values
     uint32_t sees[kMT][kBN / 32];          // keys of a rough tile that a node sees
+    int32_t entry[NST == 4 ? 4 : 1][kBN];  // table entries of a tile's keys
     float m[kNW][32], l[kNW][32];
     long long scan[kNW + 1];
     long long start_off;
@@ -165,13 +167,31 @@ __device__ __forceinline__ int fresh(int x) {
   return x;
 }
 
-// 16 bytes a lane from global memory to LDS at `to` (uniform) + 16 * lane.  In assembly because
-// the compiler would wait for it before every LDS read it cannot tell apart; the kernel waits
-// where it has to (tile_barrier).  No register is written.
-__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+// A value that all lanes hold alike, in scalar registers.
+__device__ __forceinline__ long long uniform(long long x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((unsigned long long)x >> 32));
+  return (long long)((unsigned long long)hi << 32 | lo);
+}
+
+// 16 bytes a lane from global memory to LDS at `to` (uniform) + 16 * lane, for the lanes of a mask
+// (0 or all: a condition without a branch; every lane is active where this is called).  In
+// assembly because the compiler would wait for it before every LDS read it cannot tell apart; the
+// kernel waits where it has to (tile_barrier).  No register is written.
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to,
+                                            unsigned long long lanes) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 exec, %2\n\t"
+               "global_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1"
                :
-               : "v"(from), "s"(to)
+               : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to)), "s"(uniform(lanes))
+               : "memory");
+}
+
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load_word_to_lds(const int32_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to))
                : "memory");
 }
 
@@ -226,7 +246,8 @@ void k_tree_attn(AttnArgs a) {
       before += i < wave ? S.scan[i] : 0;
       total += S.scan[i];
     }
-    per = (total + a.workers - 1) / a.workers;
+    total = uniform(total);
+    per = uniform((total + a.workers - 1) / a.workers);
     pos = w * per;
     end = pos + per < total ? pos + per : total;
     long long p = before + incl - mine;
@@ -245,7 +266,7 @@ void k_tree_attn(AttnArgs a) {
   }
   if (pos >= end) return;
   int b = __builtin_amdgcn_readfirstlane(S.start_b);
-  long long off = S.start_off;
+  long long off = uniform(S.start_off);
   const long long begin = pos;
 
   while (pos < end) {
@@ -315,21 +336,21 @@ void k_tree_attn(AttnArgs a) {
       if (tid >= BN || key >= sw.keys) return -1;
       return table[fast_div(a.c.page_div, (uint32_t)key)];
     };
-    auto put_rows = [&](int t, int page) {
-      if (tid < BN) {
-        const int key = t * BN + fresh(tid);
+    auto put_rows = [&](int t, int page, int first = 0) {  // by threads first .. first + BN - 1
+      if (tid >= first && tid < first + BN) {
+        const int at = fresh(tid) - first, key = t * BN + at;
         const bool ok = page >= 0 && page < a.c.pages;
         const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
         const int slot = key - (int)(pi * a.c.page_div.d);
-        S.rowoff[t & 3][tid] = ok ? (long long)page * a.c.page_stride +
-                                        (long long)slot * a.c.token_stride
-                                  : 0ll;
+        S.rowoff[t & (C::kRing - 1)][at] = ok ? (long long)page * a.c.page_stride +
+                                       (long long)slot * a.c.token_stride
+                                 : 0ll;
         const unsigned long long bits = __ballot(ok);
         if (lane == 0) {
-          S.valid[t & 3][(tid >> 5)] = (uint32_t)bits;
-          S.valid[t & 3][(tid >> 5) + 1] = (uint32_t)(bits >> 32);
-          S.badv[t & 3][(tid >> 5)] = 0u;
-          S.badv[t & 3][(tid >> 5) + 1] = 0u;
+          S.valid[t & (C::kRing - 1)][(at >> 5)] = (uint32_t)bits;
+          S.valid[t & (C::kRing - 1)][(at >> 5) + 1] = (uint32_t)(bits >> 32);
+          S.badv[t & (C::kRing - 1)][(at >> 5)] = 0u;
+          S.badv[t & (C::kRing - 1)][(at >> 5) + 1] = 0u;
         }
       }
     };
@@ -338,32 +359,32 @@ void k_tree_attn(AttnArgs a) {
     long long at_row[C::kLoads];
     auto find_rows = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) at_row[i] = S.rowoff[t & 3][row_of(i)];
+      for (int i = 0; i < C::kLoads; ++i) at_row[i] = S.rowoff[t & (C::kRing - 1)][row_of(i)];
     };
-    auto issue = [&](int t, int i) {
+    auto issue = [&](int t, int i, unsigned long long lanes = ~0ull) {
       const uint32_t to =
-          pool_at + (NST > 1 ? (t & 1) * C::kTileBytes : 0) + wave * 1024 + i * (NT * 16);
+          pool_at + (t & (NST - 1)) * C::kTileBytes + wave * 1024 + i * (NT * 16);
       const int r = row_of(i), p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
-      load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to);
-      load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow);
+      load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to, lanes);
+      load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow, lanes);
     };
     // A tile that ends behind the committed tokens or holds keys that do not exist: their values
     // are cleared, and non-finite values of drafted nodes, which may be hidden from some rows
     // (0 * inf must not reach them), are set aside.
     auto mend = [&](int t) {
-      char* vt = S.pool + (NST > 1 ? (t & 1) * C::kTileBytes : 0) + BN * C::kRow;
+      char* vt = S.pool + (t & (NST - 1)) * C::kTileBytes + BN * C::kRow;
       const int x0 = fresh(tid);
 #pragma unroll 1
       for (int i = 0; i < C::kLoads; ++i) {
         const int x = x0 + i * NT, r = x / C::kVecs;
         u32x4* p = reinterpret_cast<u32x4*>(vt + x * 16);
-        if (!(S.valid[t & 3][r >> 5] >> (r & 31) & 1u)) {
+        if (!(S.valid[t & (C::kRing - 1)][r >> 5] >> (r & 31) & 1u)) {
           *p = u32x4{0, 0, 0, 0};
         } else if (t * BN + r >= sw.len) {
           u32x4 y = *p;
           if (clear_non_finite<BF16>(y)) {
             *p = y;
-            atomicOr(&S.badv[t & 3][r >> 5], 1u << (r & 31));
+            atomicOr(&S.badv[t & (C::kRing - 1)][r >> 5], 1u << (r & 31));
           }
         }
       }
@@ -374,7 +395,7 @@ void k_tree_attn(AttnArgs a) {
         const int node = t * BN + k0 + fresh(lane) - sw.len;
         const int near = node < 0 ? 0 : node < a.N ? node : a.N - 1;
         const unsigned long long there =
-            S.valid[t & 3][k0 / 32] | (unsigned long long)S.valid[t & 3][k0 / 32 + 1] << 32;
+            S.valid[t & (C::kRing - 1)][k0 / 32] | (unsigned long long)S.valid[t & (C::kRing - 1)][k0 / 32 + 1] << 32;
 #pragma unroll 1
         for (int r0 = wave; first_node + r0 <= last_node; r0 += 8 * C::kNW) {
           uint8_t shown[8];
@@ -398,6 +419,8 @@ void k_tree_attn(AttnArgs a) {
       }
     };
 
+    const int kr = wk * KS * 32 + col;  // this lane's key row in its first block of 32
+    const int sw_k = C::swz_k(kr);      // the same for every block of 32 keys
     float m[RB], l[RB];
     f32x16 acc[RB][ND];
 #pragma unroll
@@ -410,21 +433,39 @@ void k_tree_attn(AttnArgs a) {
         for (int r = 0; r < 16; ++r) acc[rb][d][r] = 0.0f;
     }
 
+    // The shift m of a row's weights 2^(z - m), in units of log2 (so that weights and rescalings
+    // use the same rounded number): a key's maximum that was the row's running one, or lies less
+    // than kSlack below it.  Weights of up to 2^kSlack cost nothing (fp32 sums, and bf16 rounds
+    // relative to size), and O and l are rescaled a few times a row instead of every time some
+    // row of the wave meets a new maximum.  Returns what is subtracted (0 while nothing is seen).
+    constexpr float kSlack = 8.0f;
+    auto raise = [&](int rb, float top) -> float {
+      const float m_new = fmaxf(m[rb], half_max(top) * sl2);
+      if (__any(m_new > m[rb] + kSlack)) {
+        const float f = __builtin_amdgcn_exp2f(m[rb] - (m_new == -INFINITY ? 0.0f : m_new));
+        l[rb] *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[rb][d][r] *= f;
+        m[rb] = m_new;
+      }
+      return m[rb] == -INFINITY ? 0.0f : m[rb];
+    };
+
     // One tile: scores of this wave's keys, softmax, product with the values.  `Rough` tiles hold
     // keys that do not exist or drafted nodes; the others need no masks.
     auto step = [&](int t, auto rough) {
       constexpr bool Rough = decltype(rough)::value;
-      const char* tile = S.pool + (NST > 1 ? (t & 1) * C::kTileBytes : 0);
+      const char* tile = S.pool + (t & (NST - 1)) * C::kTileBytes;
       // scores: lane = row, register r = key 8 (r / 4) + 4 half + r % 4.  LDS reads run kAhead
       // fragments ahead of the matrix instructions (the order is pinned: left alone, the
       // compiler waits for each read)
       constexpr int kAhead = 4, kKeyFrags = KS * QF;
       constexpr int kPace = kKeyFrags / C::kLoads > 0 ? kKeyFrags / C::kLoads : 1;
-      static_assert(NST == 1 || kKeyFrags >= C::kLoads, "a pass per fragment at most");
+      static_assert(NST != 2 || kKeyFrags >= C::kLoads, "a pass per fragment at most");
       f32x16 s[KS][RB];
-      const int kr = wk * KS * 32 + col;
       const char* kp = tile + kr * C::kRow;
-      const int sw_k = C::swz_k(kr);  // the same for every block of 32 keys
       auto key_frag = [&](int n) {
         return *reinterpret_cast<const u32x4*>(kp + n / QF * (32 * C::kRow) +
                                                (((2 * (n % QF) + half) ^ sw_k) * 16));
@@ -455,7 +496,7 @@ void k_tree_attn(AttnArgs a) {
         }
         if (n + kAhead < kKeyFrags) kf[n % kAhead] = key_frag(n + kAhead);
         // the next tile's loads start in the shadow of these products
-        if (NST > 1 && n % kPace == 0 && n / kPace < C::kLoads && t + 1 < t1)
+        if (NST == 2 && n % kPace == 0 && n / kPace < C::kLoads && t + 1 < t1)
           issue(t + 1, n / kPace);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -476,8 +517,6 @@ void k_tree_attn(AttnArgs a) {
           }
       }
 
-      // running maximum in units of log2 (z log2 e, so that P and every later rescaling use the
-      // same rounded number); P = exp(z - m); O and l rescaled when the maximum grew
       float shift[RB];
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
@@ -486,18 +525,7 @@ void k_tree_attn(AttnArgs a) {
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[ks][rb][r]);
-        const float m_new = fmaxf(m[rb], half_max(mx) * sl2);
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-        if (__any(m_new > m[rb])) {
-          const float f = __builtin_amdgcn_exp2f(m[rb] - m_use);
-          l[rb] *= f;
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[rb][d][r] *= f;
-          m[rb] = m_new;
-        }
-        shift[rb] = m_use;
+        shift[rb] = raise(rb, mx);
       }
       // P of registers [8 j + r0, 8 j + r0 + n) of the wave's 16 KS keys a lane
       auto weigh = [&](int j, int r0, int n) {
@@ -588,7 +616,7 @@ void k_tree_attn(AttnArgs a) {
         const int blk = wk * KS + ks;
         // non-finite values of drafted nodes, for the rows that see them (rare: a rolled loop
         // over a copy of O in scratch memory keeps it out of the registers of the common path)
-        const uint32_t bad = Rough ? S.badv[t & 3][blk] : 0u;
+        const uint32_t bad = Rough ? S.badv[t & (C::kRing - 1)][blk] : 0u;
         if (Rough && __builtin_expect(bad != 0, 0)) {
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb) {
@@ -603,7 +631,7 @@ void k_tree_attn(AttnArgs a) {
               for (int r = 0; r < 16; ++r) p = r == rk ? s[ks][rb][r] : p;
               p = __shfl(p, col + 32 * hk);
               const int sees = __shfl((int)(seen[ks][rb] >> rk & 1u), col + 32 * hk);
-              const char* row = vbase + S.rowoff[t & 3][blk * 32 + kk];
+              const char* row = vbase + S.rowoff[t & (C::kRing - 1)][blk * 32 + kk];
 #pragma unroll 1
               for (int i = 0; i < ND * 16; ++i) {
                 const int e = (i >> 4) * 32 + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
@@ -623,52 +651,241 @@ void k_tree_attn(AttnArgs a) {
       }
     };
 
-    put_rows(t0, load_entry(t0));
-    if (t0 + 1 < t1) put_rows(t0 + 1, load_entry(t0 + 1));
-    int entry = t0 + 2 < t1 ? load_entry(t0 + 2) : -1;
-    __syncthreads();
     auto issue_all = [&](int t) {
       find_rows(t);
 #pragma unroll
       for (int i = 0; i < C::kLoads; ++i) issue(t, i);
     };
-    issue_all(t0);
-
-    // Turns to tile t: waits for it; true if it is rough.
-    auto turn = [&](int t) -> bool {
-      tile_barrier();  // tile t is there; the waves are done with the one before
-      if (NST > 1 && t + 1 < t1) find_rows(t + 1);
-      if (t + 2 < t1) {
-        put_rows(t + 2, entry);
-        entry = t + 3 < t1 ? load_entry(t + 3) : -1;
-      }
+    auto is_rough = [&](int t) -> bool {
       bool rough = (t + 1) * BN > sw.len;
 #pragma unroll
-      for (int i = 0; i < BN / 32; ++i) rough |= S.valid[t & 3][i] != 0xFFFFFFFFu;
+      for (int i = 0; i < BN / 32; ++i) rough |= S.valid[t & (C::kRing - 1)][i] != 0xFFFFFFFFu;
       return __builtin_amdgcn_readfirstlane(rough);
-    };
-    auto leave = [&](int t) {
-      if (NST == 1 && t + 1 < t1) {
-        lds_barrier();
-        issue_all(t + 1);
-      }
     };
     // plain tiles up to the first rough one (usually where the drafted nodes begin), then the
     // rest as rough ones
-    int t = t0;
-    bool rough = turn(t);
-    while (!rough) {
-      step(t, std::false_type{});
-      leave(t);
-      if (++t == t1) break;
-      rough = turn(t);
-    }
-    while (t < t1) {
-      mend(t);
-      lds_barrier();
-      step(t, std::true_type{});
-      leave(t);
-      if (++t < t1) turn(t);
+    if constexpr (NST == 4) {
+      // Four tiles in LDS, one workgroup a compute unit.  The products of one block of 32 keys
+      // run beside the exponentials of the one before, in one instruction stream:
+      //   scores of the next block  |  the first weights of this one
+      //   O += first 16 keys        |  the other weights
+      //   O += other 16 keys        |  maxima of the next block
+      // Tile t + 2 is loaded while t is computed.
+      static_assert(NST != 4 || (BF16 && WK == 1 && KS == 2 && BN == 64 && C::kNW == 8), "shape");
+      const uint32_t entry_at =
+          (uint32_t)reinterpret_cast<uintptr_t>((SV_LDS(char)*)S.entry);
+      {  // rows of the first eight tiles, a wave each
+        const int t = t0 + wave, key = t * BN + lane;
+        const int page = t < t1 && key < sw.keys ? table[fast_div(a.c.page_div, (uint32_t)key)] : -1;
+        if (t < t1) put_rows(t, page, 64 * wave);
+      }
+      __syncthreads();
+      issue_all(t0);
+      if (t0 + 1 < t1) issue_all(t0 + 1);
+      // At every fourth tile (its barrier passed), four waves: rows of tile t + 4 + wave from its
+      // table entries, entries of tile t + 8 + wave on their way.
+      auto keep_books = [&](int t) {
+        if (((t - t0) & 3) != 0 || wave >= 4) return;
+        const int e = t + 4 + wave;
+        if (t > t0 && e < t1) {
+          const int key = e * BN + fresh(lane);
+          put_rows(e, key < sw.keys ? S.entry[wave][lane] : -1, 64 * wave);
+        }
+        if (e + 4 < t1) {
+          const int key = (e + 4) * BN + fresh(lane);
+          if (key < sw.keys)
+            load_word_to_lds(table + fast_div(a.c.page_div, (uint32_t)key),
+                             entry_at + wave * (BN * 4));
+        }
+      };
+      // Waits for tile t: only tile t + 1's loads may still be on their way.
+      auto arrive = [&](int t) {
+        if (t + 1 < t1)
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * C::kLoads)
+                       : "memory");
+        else
+          tile_barrier();
+      };
+
+      constexpr int kAhead = 4, kUnits = 16 * RB, kEarly = 6, kFirst = kUnits * 11 / 16;
+      f32x16 sa[RB], sb[RB];
+      float mx[RB], shift[RB];
+      u32x4 kf[kAhead];
+      typedef short short8v __attribute__((ext_vector_type(8)));
+      short8v vf[kAhead];
+      auto key_frag = [&](const char* tile, int sub, int q) {
+        return *reinterpret_cast<const u32x4*>(tile + (sub * 32 + kr) * C::kRow +
+                                               (((2 * q + half) ^ sw_k) * 16));
+      };
+      const int vr = 4 * half + ((lane & 15) >> 2);
+      const int sw_v = C::swz_v(vr) * 16;
+      auto value_frag = [&](const char* tile, int sub, int n) {
+        const char* at = tile + (BN + sub * 32 + n / ND * 16 + vr) * C::kRow +
+                         ((lane >> 4) & 1) * 32 + (lane & 3) * 8 + ((n % ND * 64) ^ sw_v);
+        const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)at);
+        const short4v hi =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)(at + 8 * C::kRow));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      };
+      // weights u0 .. u1 - 1 of a block, in the order they are used: 16 keys, row block, register
+      auto weigh = [&](f32x16 (&s)[RB], int u0, int u1) {
+#pragma unroll
+        for (int u = u0; u < u1; ++u) {
+          const int rb = u / 8 % RB, r = u / (8 * RB) * 8 + u % 8;
+          s[rb][r] = __builtin_amdgcn_exp2f(s[rb][r] * sl2 - shift[rb]);
+          l[rb] += s[rb][r];
+        }
+      };
+      auto score = [&](f32x16 (&s)[RB], int rb, int q) {
+        if (q == 0)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[rb][r] = 0.0f;
+        s[rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, kf[q % kAhead]), __builtin_bit_cast(bf16x8, qf[rb][q]),
+            s[rb], 0, 0, 0);
+      };
+      auto raise_all = [&]() {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) shift[rb] = raise(rb, mx[rb]);
+      };
+      // Scores of block (next tile, next_sub) into nx beside the first weights of cu, whose first
+      // values (of cur tile, sub) are fetched at the end; `loads`: tile t + 2's loads start too.
+      auto scores_beside = [&](const char* next, int next_sub, f32x16 (&nx)[RB], const char* cur,
+                               int sub, f32x16 (&cu)[RB], int load_tile, auto loads) {
+        constexpr int kSlots = QF * RB;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) kf[q] = key_frag(next, next_sub, q);
+        weigh(cu, 0, kEarly);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < QF; ++q) {
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            const int slot = q * RB + rb;
+            score(nx, rb, q);
+            weigh(cu, kEarly + (kFirst - kEarly) * slot / kSlots,
+                  kEarly + (kFirst - kEarly) * (slot + 1) / kSlots);
+            if (rb + 1 < RB) __builtin_amdgcn_sched_barrier(0);
+          }
+          if (q + kAhead < QF) kf[q % kAhead] = key_frag(next, next_sub, q + kAhead);
+          else vf[q + kAhead - QF] = value_frag(cur, sub, q + kAhead - QF);
+          __builtin_amdgcn_sched_barrier(0);
+          if (decltype(loads)::value && q * C::kLoads % QF < C::kLoads)
+            issue(load_tile, q * C::kLoads / QF, load_tile < t1 ? ~0ull : 0ull);
+        }
+      };
+      // O += block (cur tile, sub) with weights cu beside the maxima of nx
+      auto values_beside = [&](const char* cur, int sub, f32x16 (&cu)[RB], f32x16 (&nx)[RB]) {
+        constexpr int kFrags = 2 * ND, kSlots = ND * RB;
+        bf16x8 pf[RB];
+#pragma unroll
+        for (int n = 0; n < kFrags; ++n) {
+          const int c = n / ND, d = n % ND;
+          if (d == 0)  // P rounded to bf16: half a step of 2^-8 per weight
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) pf[rb][i] = (__bf16)cu[rb][8 * c + i];
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            const int slot = d * RB + rb;
+            acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf[rb], acc[rb][d], 0, 0, 0);
+            if (c == 0) {
+              weigh(cu, kFirst + (kUnits - kFirst) * slot / kSlots,
+                    kFirst + (kUnits - kFirst) * (slot + 1) / kSlots);
+            } else {
+#pragma unroll
+              for (int r = 16 * d / ND; r < 16 * (d + 1) / ND; ++r)
+                mx[rb] = r == 0 ? nx[rb][0] : fmaxf(mx[rb], nx[rb][r]);
+            }
+            if (rb + 1 < RB) __builtin_amdgcn_sched_barrier(0);
+          }
+          if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(cur, sub, n + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) asm volatile("" : "+v"(mx[rb]));  // not moved from here
+      };
+
+      int t = t0;
+      arrive(t);
+      bool plain = !is_rough(t);
+      if (plain) {  // the first block's scores and maxima stand alone
+        const char* tile = S.pool + (t & 3) * C::kTileBytes;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) kf[q] = key_frag(tile, 0, q);
+#pragma unroll
+        for (int q = 0; q < QF; ++q) {
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) score(sa, rb, q);
+          if (q + kAhead < QF) kf[q % kAhead] = key_frag(tile, 0, q + kAhead);
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          mx[rb] = sa[rb][0];
+#pragma unroll
+          for (int r = 1; r < 16; ++r) mx[rb] = fmaxf(mx[rb], sa[rb][r]);
+        }
+      }
+      while (plain) {
+        const char* tile = S.pool + (t & 3) * C::kTileBytes;
+        if (t + 2 < t1) find_rows(t + 2);
+        keep_books(t);
+        raise_all();
+        scores_beside(tile, 1, sb, tile, 0, sa, t + 2, std::true_type{});
+        values_beside(tile, 0, sa, sb);
+        raise_all();
+        if (++t < t1) arrive(t);
+        // the next tile's scores also where it is rough or there is none (LDS holds some tile):
+        // they are dropped then, and the stream of instructions stays one
+        scores_beside(S.pool + (t & 3) * C::kTileBytes, 0, sa, tile, 1, sb, 0, std::false_type{});
+        values_beside(tile, 1, sb, sa);
+        plain = t < t1 && !is_rough(t);
+      }
+      while (t < t1) {
+        if (t + 2 < t1) issue_all(t + 2);
+        keep_books(t);
+        mend(t);
+        lds_barrier();
+        step(t, std::true_type{});
+        if (++t < t1) arrive(t);
+      }
+    } else {
+      put_rows(t0, load_entry(t0));
+      if (t0 + 1 < t1) put_rows(t0 + 1, load_entry(t0 + 1));
+      int entry = t0 + 2 < t1 ? load_entry(t0 + 2) : -1;
+      __syncthreads();
+      issue_all(t0);
+      auto turn = [&](int t) {
+        tile_barrier();  // tile t is there; the waves are done with the one before
+        if (NST > 1 && t + 1 < t1) find_rows(t + 1);
+        if (t + 2 < t1) {
+          put_rows(t + 2, entry);
+          entry = t + 3 < t1 ? load_entry(t + 3) : -1;
+        }
+      };
+      auto leave = [&](int t) {
+        if (NST == 1 && t + 1 < t1) {
+          lds_barrier();
+          issue_all(t + 1);
+        }
+      };
+      int t = t0;
+      turn(t);
+      while (!is_rough(t)) {
+        step(t, std::false_type{});
+        leave(t);
+        if (++t == t1) break;
+        turn(t);
+      }
+      while (t < t1) {
+        mend(t);
+        lds_barrier();
+        step(t, std::true_type{});
+        leave(t);
+        if (++t < t1) turn(t);
+      }
     }
 
     // ------------------------------------------------------------------ the part's result
@@ -769,14 +986,15 @@ void k_tree_attn(AttnArgs a) {
   }
 }
 
-// Joins the parts of the group that begins with worker blockIdx.x's last part and ends with a
-// later worker: every later part is that worker's first.  One thread per four columns of a row.
+// Joins the parts of each group that begins as some worker's last part and ends with a later
+// worker: every later part is that worker's first.  A workgroup looks after kTails neighbouring
+// workers (few of them begin a long group) and 256 pieces of four columns of a row.
+constexpr int kTails = 8;
+
 template <bool BF16, int D, int MT>
-__global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
-  const int4 g = a.tail[blockIdx.x];
-  if (g.w < 2) return;
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const int4 g) {
   const int b = g.x, h = g.y / a.mts, mt = g.y - h * a.mts;
-  const int i = blockIdx.y * 256 + threadIdx.x;
+  const int i = blockIdx.x * 256 + threadIdx.x;
   const int row = i / (D / 4), e = (i - row * (D / 4)) * 4;
   const int r = mt * MT + row;
   const int node = r / a.G, hg = r - node * a.G;
@@ -832,6 +1050,23 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   if (a.lse && e == 0) a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
+template <bool BF16, int D, int MT>
+__global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
+  int4 g[kTails];
+#pragma unroll
+  for (int i = 0; i < kTails; ++i) {
+    const int w = blockIdx.y * kTails + i;
+    g[i] = a.tail[w < a.workers ? w : a.workers - 1];
+    if (w >= a.workers) g[i].w = 0;
+  }
+#pragma unroll 1
+  for (int i = 0; i < kTails; ++i) {
+    if (g[0].w > 1) join_parts<BF16, D, MT>(a, g[0]);
+#pragma unroll
+    for (int j = 0; j + 1 < kTails; ++j) g[j] = g[j + 1];
+  }
+}
+
 // Tile shapes by row bytes and rows.  Rows of up to 256 bytes: two tiles of 64 keys fit beside
 // another workgroup's; longer ones: one tile, and the other workgroup computes while it loads.
 struct Shape {
@@ -850,7 +1085,7 @@ constexpr Shape shape_for(int row_tile) {
   if (row_tile == 32) return Shape{1, 4, 1, 1, 2, 1};
   if (row_tile == 64) return Shape{2, 2, 1, 1, 2, 2};
   if (row_tile == 128) return Shape{4, 1, 2, 1, 2, 2};
-  return Shape{4, 1, 2, 2, 2, 2};
+  return Shape{8, 1, 2, 1, 4, 2};
 }
 
 template <bool BF16, int D, int RT>
@@ -863,8 +1098,9 @@ hipError_t launch_shape(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.workers > 1)
-    hipLaunchKernelGGL((k_tree_join<BF16, D, C::kMT>), dim3(p.workers, C::kMT * D / 4 / 256),
-                       dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((k_tree_join<BF16, D, C::kMT>),
+                       dim3(C::kMT * D / 4 / 256, (p.workers + kTails - 1) / kTails), dim3(256), 0,
+                       stream, a);
   return hipGetLastError();
 }
 
@@ -874,7 +1110,7 @@ hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
   else {
     if (p.row_tile == 32) return launch_shape<BF16, D, 32>(a, p, stream);
     if (p.row_tile == 64) return launch_shape<BF16, D, 64>(a, p, stream);
-    if constexpr (D * (BF16 ? 2 : 4) <= 256)
+    if constexpr (BF16 && 256 % (D * 2) == 0)
       if (p.row_tile == 256) return launch_shape<BF16, D, 256>(a, p, stream);
     return launch_shape<BF16, D, 128>(a, p, stream);
   }
@@ -908,7 +1144,7 @@ AttnPlan plan_tree_attention(const CacheView& c, sv_dtype dt, int N, int G) {
   const bool bf16 = dt == SV_DTYPE_BF16;
   const long long rows = (long long)N * G;
   const int row_bytes = c.head_dim * c.esize;
-  const int want = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int want = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || !bf16 || 256 % row_bytes ? 128 : 256;
   const Shape sh = bf16 ? shape_of<true>(c.head_dim, want) : shape_of<false>(c.head_dim, want);
   p.row_tile = 32 * sh.wm * sh.rb;
   p.key_tile = 32 * sh.wk * sh.ks;
