@@ -37,6 +37,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kKept = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 #define SV_LDS(T) __attribute__((address_space(3))) T
@@ -59,21 +60,19 @@ __device__ __forceinline__ uint32_t of_half(uint32_t x) {
   return (x & 0xFu) | (x >> 4 & 0xF0u) | (x >> 8 & 0xF00u) | (x >> 12 & 0xF000u);
 }
 
-// Work of one sequence: key tiles of its live row tiles, and one piece (zeros to write) for
-// each row tile that holds no node.
+// Work of one sequence, in pieces of a key tile's cost: for each live row tile `fixed` pieces
+// for what a group costs whatever its length, then its key tiles; one piece (zeros to write)
+// for each row tile that holds no node.
 struct SeqWork {
   int len, n, keys;  // committed tokens, nodes, keys behind the table
   int tiles, live;   // key tiles (at least one), row tiles with a node
-  long long units;
 };
 
 template <int MT, int BN>
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b) {
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int len, int n) {
   SeqWork s;
-  int len = a.c.lens[b];
   len = len < 0 ? 0 : len;
   s.len = len > a.c.cap ? a.c.cap : len;
-  int n = a.nodes ? a.nodes[b] : a.N;
   n = n < 0 ? 0 : n;
   s.n = n > a.N ? a.N : n;
   const int keys = s.len + s.n;
@@ -81,8 +80,17 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b) {
   const int tiles = (s.keys + BN - 1) / BN;
   s.tiles = tiles < 1 ? 1 : tiles;
   s.live = (s.n * a.G + MT - 1) / MT;
-  s.units = (long long)a.c.kv_heads * ((long long)s.live * s.tiles + (a.mts - s.live));
   return s;
+}
+
+__device__ __forceinline__ long long seq_pieces(const AttnArgs& a, const SeqWork& s, int fixed) {
+  return (long long)a.c.kv_heads * ((long long)s.live * (s.tiles + fixed) + (a.mts - s.live));
+}
+
+// x / d for 0 <= x, 0 < d < 2^31, in 32 bits where x fits (nearly always).
+__device__ __forceinline__ long long div_pieces(long long x, long long d) {
+  if (x >> 31 == 0) return (uint32_t)x / (uint32_t)d;
+  return x / d;
 }
 
 __device__ __forceinline__ bool non_finite(uint32_t bits32) {
@@ -154,7 +162,8 @@ struct Attn {
     uint32_t sees[kMT][kBN / 32];          // keys of a rough tile that a node sees
     int32_t entry[NST == 4 ? 4 : 1][kBN];  // table entries of a tile's keys
     float m[kNW][32], l[kNW][32];
-    long long scan[kNW + 1];
+    longlong2 scan[kNW];
+    int2 seq[kKept];                       // lengths and node counts of the first sequences
     long long start_off;
     int start_b;
   };
@@ -225,36 +234,53 @@ void k_tree_attn(AttnArgs a) {
   if ((a.workers & 7) == 0) w = (w & 7) * (a.workers >> 3) + (w >> 3);
 
   // where this worker's pieces begin: prefix sums of the sequences' work
+  auto work_of = [&](int b) {
+    return b < kKept ? seq_work<MT, BN>(a, S.seq[b].x, S.seq[b].y)
+                     : seq_work<MT, BN>(a, a.c.lens[b], a.nodes ? a.nodes[b] : a.N);
+  };
   long long total, per, pos, end;
+  int fixed;
   {
     const int chunk = (a.c.seqs + NT - 1) / NT;
     const int b0 = tid * chunk, b1 = b0 + chunk < a.c.seqs ? b0 + chunk : a.c.seqs;
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_work<MT, BN>(a, b).units;
-    long long incl = mine;
+    long long mine = 0, live = 0;  // pieces without the fixed ones, live groups
+    for (int b = b0; b < b1; ++b) {
+      const int len = a.c.lens[b], n = a.nodes ? a.nodes[b] : a.N;
+      if (b < kKept) S.seq[b] = make_int2(len, n);
+      const SeqWork s = seq_work<MT, BN>(a, len, n);
+      mine += seq_pieces(a, s, 0);
+      live += (long long)a.c.kv_heads * s.live;
+    }
+    long long incl = mine, incl_live = live;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const long long y = __shfl_up(incl, d);
+      const long long y = __shfl_up(incl, d), z = __shfl_up(incl_live, d);
       incl += lane >= d ? y : 0;
+      incl_live += lane >= d ? z : 0;
     }
-    if (lane == 63) S.scan[wave] = incl;
+    if (lane == 63) S.scan[wave] = make_longlong2(incl, incl_live);
     __syncthreads();
-    long long before = 0;
+    long long before = 0, before_live = 0, groups = 0;
     total = 0;
 #pragma unroll
     for (int i = 0; i < C::kNW; ++i) {
-      before += i < wave ? S.scan[i] : 0;
-      total += S.scan[i];
+      before += i < wave ? S.scan[i].x : 0;
+      before_live += i < wave ? S.scan[i].y : 0;
+      total += S.scan[i].x;
+      groups += S.scan[i].y;
     }
-    total = uniform(total);
-    per = uniform((total + a.workers - 1) / a.workers);
+    // a group's fixed cost is about three tiles; it is counted where a worker has many
+    const long long tiles_each = div_pieces(uniform(total), a.workers);
+    fixed = tiles_each >= 24 ? 3 : (int)tiles_each / 8;
+    total = uniform(total + groups * fixed);
+    per = div_pieces(total + a.workers - 1, a.workers);
     pos = w * per;
     end = pos + per < total ? pos + per : total;
-    long long p = before + incl - mine;
-    if (pos >= p && pos < p + mine) {
+    long long p = before + incl - mine + (before_live + incl_live - live) * fixed;
+    if (pos >= p && pos < p + mine + live * fixed) {
       int b = b0;
       for (; b < b1; ++b) {
-        const long long u = seq_work<MT, BN>(a, b).units;
+        const long long u = seq_pieces(a, work_of(b), fixed);
         if (pos < p + u) break;
         p += u;
       }
@@ -270,13 +296,18 @@ void k_tree_attn(AttnArgs a) {
   const long long begin = pos;
 
   while (pos < end) {
-    const SeqWork sw = seq_work<MT, BN>(a, b);
-    if (off >= sw.units) {
-      off -= sw.units;
+    SeqWork sw = work_of(b);
+    sw.len = __builtin_amdgcn_readfirstlane(sw.len);
+    sw.n = __builtin_amdgcn_readfirstlane(sw.n);
+    sw.keys = __builtin_amdgcn_readfirstlane(sw.keys);
+    sw.tiles = __builtin_amdgcn_readfirstlane(sw.tiles);
+    sw.live = __builtin_amdgcn_readfirstlane(sw.live);
+    if (const long long u = seq_pieces(a, sw, fixed); off >= u) {
+      off -= u;
       ++b;
       continue;
     }
-    const long long live_units = (long long)a.c.kv_heads * sw.live * sw.tiles;
+    const long long live_units = (long long)a.c.kv_heads * sw.live * (sw.tiles + fixed);
     if (off >= live_units) {  // a row tile without a node: zeros
       const long long u = off - live_units;
       const int dead = a.mts - sw.live;
@@ -297,11 +328,18 @@ void k_tree_attn(AttnArgs a) {
     }
 
     // ------------------------------------------------------------------ one part of a group
-    const long long grp = off / sw.tiles;
-    const int t0 = (int)(off - grp * sw.tiles);
-    const int h = (int)(grp / sw.live), mt = (int)(grp - (long long)h * sw.live);
+    const int group_pieces = sw.tiles + fixed;
+    const long long grp = div_pieces(off, group_pieces);
+    const int r0 = (int)(off - grp * group_pieces);  // first piece in the group
     const long long left = end - pos;
-    const int t1 = (long long)(sw.tiles - t0) < left ? sw.tiles : t0 + (int)left;
+    const int r1 = (long long)(group_pieces - r0) < left ? group_pieces : r0 + (int)left;
+    const int t0 = r0 > fixed ? r0 - fixed : 0, t1 = r1 - fixed;
+    if (t0 >= t1) {  // fixed pieces alone
+      pos += r1 - r0;
+      off += r1 - r0;
+      continue;
+    }
+    const int h = (int)((uint32_t)grp / (uint32_t)sw.live), mt = (int)grp - h * sw.live;
     const int rows = sw.n * a.G;             // live rows of the (sequence, kv head)
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     const char* kbase = a.c.k + (long long)h * a.c.head_stride;
@@ -917,7 +955,7 @@ void k_tree_attn(AttnArgs a) {
       l[0] = lt;
     }
 
-    const long long first = pos - t0;  // the group's first piece
+    const long long first = pos - r0;  // the group's first piece
     const bool whole = t0 == 0 && t1 == sw.tiles;
     const int slot = 2 * w + (pos == begin ? 0 : 1);
     const int hq = a.c.kv_heads * a.G;
@@ -979,10 +1017,10 @@ void k_tree_attn(AttnArgs a) {
       }
     }
     if (tid == 0 && t0 == 0 && !whole)
-      a.tail[w] = make_int4(b, h * a.mts + mt, slot, (int)((first + sw.tiles - 1) / per - w + 1));
+      a.tail[w] = make_int4(b, h * a.mts + mt, slot, (int)(div_pieces(first + group_pieces - 1, per) - w + 1));
     __syncthreads();
-    pos += t1 - t0;
-    off += t1 - t0;
+    pos += r1 - r0;
+    off += r1 - r0;
   }
 }
 
