@@ -37,9 +37,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kLdsBytes = 160 * 1024;  // of a compute unit
 constexpr int kKept = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// Every lambda of the kernels is part of its kernel's loop: one that the compiler calls instead, or
+// whose captures it keeps in memory, is reached through private memory by flat instructions.
+#define SV_INLINE __attribute__((always_inline))
 #define SV_LDS(T) __attribute__((address_space(3))) T
 #define SV_GLOBAL(T) __attribute__((address_space(1))) T
 
@@ -234,7 +238,7 @@ void k_tree_attn(AttnArgs a) {
   if ((a.workers & 7) == 0) w = (w & 7) * (a.workers >> 3) + (w >> 3);
 
   // where this worker's pieces begin: prefix sums of the sequences' work
-  auto work_of = [&](int b) {
+  auto work_of = [&](int b) SV_INLINE {
     return b < kKept ? seq_work<MT, BN>(a, S.seq[b].x, S.seq[b].y)
                      : seq_work<MT, BN>(a, a.c.lens[b], a.nodes ? a.nodes[b] : a.N);
   };
@@ -365,16 +369,16 @@ void k_tree_attn(AttnArgs a) {
     }
 
     // row that this thread's vector of pass i belongs to (a pass covers whole rows, or not)
-    auto row_of = [&](int i) {
+    auto row_of = [&](int i) SV_INLINE {
       return NT % C::kVecs == 0 ? tid / C::kVecs + i * (NT / C::kVecs)
                                 : (tid + i * NT) / C::kVecs;
     };
-    auto load_entry = [&](int t) -> int {  // page of key t * BN + tid, -1: none
+    auto load_entry = [&](int t) SV_INLINE -> int {  // page of key t * BN + tid, -1: none
       const int key = t * BN + fresh(tid);
       if (tid >= BN || key >= sw.keys) return -1;
       return table[fast_div(a.c.page_div, (uint32_t)key)];
     };
-    auto put_rows = [&](int t, int page, int first = 0) {  // by threads first .. first + BN - 1
+    auto put_rows = [&](int t, int page, int first = 0) SV_INLINE {  // by threads first .. first + BN - 1
       if (tid >= first && tid < first + BN) {
         const int at = fresh(tid) - first, key = t * BN + at;
         const bool ok = page >= 0 && page < a.c.pages;
@@ -395,11 +399,11 @@ void k_tree_attn(AttnArgs a) {
     // Loads of tile t into LDS, 1 KB per wave, instruction and tensor: the row offsets of its
     // kLoads passes, then pass i.
     long long at_row[C::kLoads];
-    auto find_rows = [&](int t) {
+    auto find_rows = [&](int t) SV_INLINE {
 #pragma unroll
       for (int i = 0; i < C::kLoads; ++i) at_row[i] = S.rowoff[t & (C::kRing - 1)][row_of(i)];
     };
-    auto issue = [&](int t, int i, unsigned long long lanes = ~0ull) {
+    auto issue = [&](int t, int i, unsigned long long lanes = ~0ull) SV_INLINE {
       const uint32_t to =
           pool_at + (t & (NST - 1)) * C::kTileBytes + wave * 1024 + i * (NT * 16);
       const int r = row_of(i), p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
@@ -409,7 +413,7 @@ void k_tree_attn(AttnArgs a) {
     // A tile that ends behind the committed tokens or holds keys that do not exist: their values
     // are cleared, and non-finite values of drafted nodes, which may be hidden from some rows
     // (0 * inf must not reach them), are set aside.
-    auto mend = [&](int t) {
+    auto mend = [&](int t) SV_INLINE {
       char* vt = S.pool + (t & (NST - 1)) * C::kTileBytes + BN * C::kRow;
       const int x0 = fresh(tid);
 #pragma unroll 1
@@ -477,7 +481,7 @@ void k_tree_attn(AttnArgs a) {
     // relative to size), and O and l are rescaled a few times a row instead of every time some
     // row of the wave meets a new maximum.  Returns what is subtracted (0 while nothing is seen).
     constexpr float kSlack = 8.0f;
-    auto raise = [&](int rb, float top) -> float {
+    auto raise = [&](int rb, float top) SV_INLINE -> float {
       const float m_new = fmaxf(m[rb], half_max(top) * sl2);
       if (__any(m_new > m[rb] + kSlack)) {
         const float f = __builtin_amdgcn_exp2f(m[rb] - (m_new == -INFINITY ? 0.0f : m_new));
@@ -493,7 +497,7 @@ void k_tree_attn(AttnArgs a) {
 
     // One tile: scores of this wave's keys, softmax, product with the values.  `Rough` tiles hold
     // keys that do not exist or drafted nodes; the others need no masks.
-    auto step = [&](int t, auto rough) {
+    auto step = [&](int t, auto rough) SV_INLINE {
       constexpr bool Rough = decltype(rough)::value;
       const char* tile = S.pool + (t & (NST - 1)) * C::kTileBytes;
       // scores: lane = row, register r = key 8 (r / 4) + 4 half + r % 4.  LDS reads run kAhead
@@ -504,7 +508,7 @@ void k_tree_attn(AttnArgs a) {
       static_assert(NST != 2 || kKeyFrags >= C::kLoads, "a pass per fragment at most");
       f32x16 s[KS][RB];
       const char* kp = tile + kr * C::kRow;
-      auto key_frag = [&](int n) {
+      auto key_frag = [&](int n) SV_INLINE {
         return *reinterpret_cast<const u32x4*>(kp + n / QF * (32 * C::kRow) +
                                                (((2 * (n % QF) + half) ^ sw_k) * 16));
       };
@@ -566,7 +570,7 @@ void k_tree_attn(AttnArgs a) {
         shift[rb] = raise(rb, mx);
       }
       // P of registers [8 j + r0, 8 j + r0 + n) of the wave's 16 KS keys a lane
-      auto weigh = [&](int j, int r0, int n) {
+      auto weigh = [&](int j, int r0, int n) SV_INLINE {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -586,7 +590,7 @@ void k_tree_attn(AttnArgs a) {
         const char* vt = vp + vr * C::kRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
         const int sw_v = C::swz_v(vr) * 16;
         typedef short short8v __attribute__((ext_vector_type(8)));
-        auto value_frag = [&](int n) {  // 16 keys n / ND, columns 32 (n % ND) and up
+        auto value_frag = [&](int n) SV_INLINE {  // 16 keys n / ND, columns 32 (n % ND) and up
           const char* at = vt + n / ND * (16 * C::kRow) + ((n % ND * 64) ^ sw_v);
           const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)at);
           const short4v hi =
@@ -626,7 +630,7 @@ void k_tree_attn(AttnArgs a) {
       } else {
 #pragma unroll
         for (int j = 0; j < 2 * KS; ++j) weigh(j, 0, 8);
-        auto value_frag = [&](int n) {  // key register n / ND, columns 32 (n % ND) and up
+        auto value_frag = [&](int n) SV_INLINE {  // key register n / ND, columns 32 (n % ND) and up
           const int r = n / ND;
           return *reinterpret_cast<const float*>(
               vp + (8 * (r >> 2) + 4 * half + (r & 3)) * C::kRow + col * 4 + n % ND * 128);
@@ -661,6 +665,7 @@ void k_tree_attn(AttnArgs a) {
             float o[ND * 16];
 #pragma unroll
             for (int i = 0; i < ND * 16; ++i) o[i] = acc[rb][i >> 4][i & 15];
+            asm volatile("" : : "v"(o) : "memory");  // stays in scratch memory
             for (uint32_t left = bad; left; left &= left - 1) {
               const int kk = __builtin_amdgcn_readfirstlane(__ffs(left) - 1);
               const int hk = (kk >> 2) & 1, rk = ((kk >> 3) << 2) | (kk & 3);
@@ -689,12 +694,12 @@ void k_tree_attn(AttnArgs a) {
       }
     };
 
-    auto issue_all = [&](int t) {
+    auto issue_all = [&](int t) SV_INLINE {
       find_rows(t);
 #pragma unroll
       for (int i = 0; i < C::kLoads; ++i) issue(t, i);
     };
-    auto is_rough = [&](int t) -> bool {
+    auto is_rough = [&](int t) SV_INLINE -> bool {
       bool rough = (t + 1) * BN > sw.len;
 #pragma unroll
       for (int i = 0; i < BN / 32; ++i) rough |= S.valid[t & (C::kRing - 1)][i] != 0xFFFFFFFFu;
@@ -722,7 +727,7 @@ void k_tree_attn(AttnArgs a) {
       if (t0 + 1 < t1) issue_all(t0 + 1);
       // At every fourth tile (its barrier passed), four waves: rows of tile t + 4 + wave from its
       // table entries, entries of tile t + 8 + wave on their way.
-      auto keep_books = [&](int t) {
+      auto keep_books = [&](int t) SV_INLINE {
         if (((t - t0) & 3) != 0 || wave >= 4) return;
         const int e = t + 4 + wave;
         if (t > t0 && e < t1) {
@@ -737,7 +742,7 @@ void k_tree_attn(AttnArgs a) {
         }
       };
       // Waits for tile t: only tile t + 1's loads may still be on their way.
-      auto arrive = [&](int t) {
+      auto arrive = [&](int t) SV_INLINE {
         if (t + 1 < t1)
           asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * C::kLoads)
                        : "memory");
@@ -751,13 +756,13 @@ void k_tree_attn(AttnArgs a) {
       u32x4 kf[kAhead];
       typedef short short8v __attribute__((ext_vector_type(8)));
       short8v vf[kAhead];
-      auto key_frag = [&](const char* tile, int sub, int q) {
+      auto key_frag = [&](const char* tile, int sub, int q) SV_INLINE {
         return *reinterpret_cast<const u32x4*>(tile + (sub * 32 + kr) * C::kRow +
                                                (((2 * q + half) ^ sw_k) * 16));
       };
       const int vr = 4 * half + ((lane & 15) >> 2);
       const int sw_v = C::swz_v(vr) * 16;
-      auto value_frag = [&](const char* tile, int sub, int n) {
+      auto value_frag = [&](const char* tile, int sub, int n) SV_INLINE {
         const char* at = tile + (BN + sub * 32 + n / ND * 16 + vr) * C::kRow +
                          ((lane >> 4) & 1) * 32 + (lane & 3) * 8 + ((n % ND * 64) ^ sw_v);
         const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)at);
@@ -766,7 +771,7 @@ void k_tree_attn(AttnArgs a) {
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       };
       // weights u0 .. u1 - 1 of a block, in the order they are used: 16 keys, row block, register
-      auto weigh = [&](f32x16 (&s)[RB], int u0, int u1) {
+      auto weigh = [&](f32x16 (&s)[RB], int u0, int u1) SV_INLINE {
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
           const int rb = u / 8 % RB, r = u / (8 * RB) * 8 + u % 8;
@@ -774,7 +779,7 @@ void k_tree_attn(AttnArgs a) {
           l[rb] += s[rb][r];
         }
       };
-      auto score = [&](f32x16 (&s)[RB], int rb, int q) {
+      auto score = [&](f32x16 (&s)[RB], int rb, int q) SV_INLINE {
         if (q == 0)
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[rb][r] = 0.0f;
@@ -782,14 +787,14 @@ void k_tree_attn(AttnArgs a) {
             __builtin_bit_cast(bf16x8, kf[q % kAhead]), __builtin_bit_cast(bf16x8, qf[rb][q]),
             s[rb], 0, 0, 0);
       };
-      auto raise_all = [&]() {
+      auto raise_all = [&]() SV_INLINE {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) shift[rb] = raise(rb, mx[rb]);
       };
       // Scores of block (next tile, next_sub) into nx beside the first weights of cu, whose first
       // values (of cur tile, sub) are fetched at the end; `loads`: tile t + 2's loads start too.
       auto scores_beside = [&](const char* next, int next_sub, f32x16 (&nx)[RB], const char* cur,
-                               int sub, f32x16 (&cu)[RB], int load_tile, auto loads) {
+                               int sub, f32x16 (&cu)[RB], int load_tile, auto loads) SV_INLINE {
         constexpr int kSlots = QF * RB;
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) kf[q] = key_frag(next, next_sub, q);
@@ -813,7 +818,7 @@ void k_tree_attn(AttnArgs a) {
         }
       };
       // O += block (cur tile, sub) with weights cu beside the maxima of nx
-      auto values_beside = [&](const char* cur, int sub, f32x16 (&cu)[RB], f32x16 (&nx)[RB]) {
+      auto values_beside = [&](const char* cur, int sub, f32x16 (&cu)[RB], f32x16 (&nx)[RB]) SV_INLINE {
         constexpr int kFrags = 2 * ND, kSlots = ND * RB;
         bf16x8 pf[RB];
 #pragma unroll
@@ -895,7 +900,7 @@ void k_tree_attn(AttnArgs a) {
       int entry = t0 + 2 < t1 ? load_entry(t0 + 2) : -1;
       __syncthreads();
       issue_all(t0);
-      auto turn = [&](int t) {
+      auto turn = [&](int t) SV_INLINE {
         tile_barrier();  // tile t is there; the waves are done with the one before
         if (NST > 1 && t + 1 < t1) find_rows(t + 1);
         if (t + 2 < t1) {
@@ -903,7 +908,7 @@ void k_tree_attn(AttnArgs a) {
           entry = t + 3 < t1 ? load_entry(t + 3) : -1;
         }
       };
-      auto leave = [&](int t) {
+      auto leave = [&](int t) SV_INLINE {
         if (NST == 1 && t + 1 < t1) {
           lds_barrier();
           issue_all(t + 1);
@@ -972,7 +977,7 @@ void k_tree_attn(AttnArgs a) {
       char* op = a.out + orow * C::kRow + 4 * fhalf * C::kES;
       float* pp = a.part + prow * D + 4 * fhalf;
       // columns d * 32 + 8 r4 + 4 half and up of the row; a dead row's O may hold anything
-      auto emit_out = [&](int d, int r4, f32x4 x) {
+      auto emit_out = [&](int d, int r4, f32x4 x) SV_INLINE {
         if (!row_live) x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (BF16) {
           bf16x4 y;
@@ -983,10 +988,10 @@ void k_tree_attn(AttnArgs a) {
           *reinterpret_cast<f32x4*>(op + (d * 32 + 8 * r4) * 4) = x * inv;
         }
       };
-      auto emit_part = [&](int d, int r4, f32x4 x) {
+      auto emit_part = [&](int d, int r4, f32x4 x) SV_INLINE {
         *reinterpret_cast<f32x4*>(pp + d * 32 + 8 * r4) = x;
       };
-      auto each = [&](auto emit) {
+      auto each = [&](auto emit) SV_INLINE {
         if constexpr (WK > 1) {
           const f32x4* box = reinterpret_cast<const f32x4*>(S.pool);
           for (int d = wk; d < ND; d += WK)
@@ -1045,8 +1050,8 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const int4 g) {
   float m = -INFINITY, l = 0.0f;
   if (node < n) {
     // parts: slot g.z, then slot 0 of each later worker
-    auto slot_of = [&](int s) { return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s); };
-    auto take = [&](int s0, auto count) {  // so many parts, all their loads in flight
+    auto slot_of = [&](int s) SV_INLINE { return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s); };
+    auto take = [&](int s0, auto count) SV_INLINE {  // so many parts, all their loads in flight
       constexpr int kCount = decltype(count)::value;
       float2 ml[kCount];
       f32x4 y[kCount];
@@ -1109,6 +1114,7 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
 // another workgroup's; longer ones: one tile, and the other workgroup computes while it loads.
 struct Shape {
   int wm, wk, ks, rb, nst, occ;
+  int per_cu = 0;  // workgroups that a compute unit holds
 };
 
 template <bool BF16, int D>
@@ -1120,7 +1126,7 @@ constexpr Shape shape_for(int row_tile) {
     if (row_tile == 64) return D > 128 ? Shape{2, 1, 2, 1, 1, 1} : Shape{2, 2, 1, 1, 1, 2};
     return Shape{4, 1, 2, 1, 1, 2};
   }
-  if (row_tile == 32) return Shape{1, 4, 1, 1, 2, 1};
+  if (row_tile == 32) return Shape{1, 2, 1, 1, 2, 2};
   if (row_tile == 64) return Shape{2, 2, 1, 1, 2, 2};
   if (row_tile == 128) return Shape{4, 1, 2, 1, 2, 2};
   return Shape{8, 1, 2, 1, 4, 2};
@@ -1150,7 +1156,8 @@ hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
     if (p.row_tile == 64) return launch_shape<BF16, D, 64>(a, p, stream);
     if constexpr (BF16 && 256 % (D * 2) == 0)
       if (p.row_tile == 256) return launch_shape<BF16, D, 256>(a, p, stream);
-    return launch_shape<BF16, D, 128>(a, p, stream);
+    if constexpr (!BF16 || D <= 128) return launch_shape<BF16, D, 128>(a, p, stream);
+    return hipErrorInvalidValue;
   }
 }
 
@@ -1165,13 +1172,37 @@ hipError_t launch_type(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
   }
 }
 
+// The shape of a row tile, with the workgroups that LDS and the waves' registers leave room for.
+template <bool BF16, int D, int RT>
+Shape filled_shape() {
+  Shape sh = shape_for<BF16, D>(RT);
+  constexpr Shape c = shape_for<BF16, D>(RT);
+  using C = Attn<BF16, D, c.wm, c.wk, c.ks, c.rb, c.nst>;
+  const int by_lds = kLdsBytes / (int)sizeof(typename C::Lds), by_waves = 4 * c.occ / C::kNW;
+  sh.per_cu = by_lds < by_waves ? by_lds : by_waves;
+  return sh;
+}
+
+template <bool BF16, int D>
+Shape shape_of_dim(int row_tile) {
+  if constexpr (D * (BF16 ? 2 : 4) > 512) return filled_shape<BF16, D, 64>();
+  else {
+    if (row_tile == 32) return filled_shape<BF16, D, 32>();
+    if constexpr (BF16 && 256 % (D * 2) == 0)
+      if (row_tile == 256) return filled_shape<BF16, D, 256>();
+    if constexpr (!BF16 || D <= 128)
+      if (row_tile == 128) return filled_shape<BF16, D, 128>();
+    return filled_shape<BF16, D, 64>();
+  }
+}
+
 template <bool BF16>
 Shape shape_of(int D, int row_tile) {
   switch (D) {
-    case 64: return shape_for<BF16, 64>(row_tile);
-    case 96: return shape_for<BF16, 96>(row_tile);
-    case 128: return shape_for<BF16, 128>(row_tile);
-    default: return shape_for<BF16, 256>(row_tile);
+    case 64: return shape_of_dim<BF16, 64>(row_tile);
+    case 96: return shape_of_dim<BF16, 96>(row_tile);
+    case 128: return shape_of_dim<BF16, 128>(row_tile);
+    default: return shape_of_dim<BF16, 256>(row_tile);
   }
 }
 
@@ -1182,15 +1213,16 @@ AttnPlan plan_tree_attention(const CacheView& c, sv_dtype dt, int N, int G) {
   const bool bf16 = dt == SV_DTYPE_BF16;
   const long long rows = (long long)N * G;
   const int row_bytes = c.head_dim * c.esize;
-  const int want = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || !bf16 || 256 % row_bytes ? 128 : 256;
+  const int want = rows <= 32 ? 32 : rows <= 64 || (bf16 && row_bytes > 256)       ? 64
+                   : rows <= 128 || !bf16 || 256 % row_bytes ? 128
+                                                             : 256;
   const Shape sh = bf16 ? shape_of<true>(c.head_dim, want) : shape_of<false>(c.head_dim, want);
   p.row_tile = 32 * sh.wm * sh.rb;
   p.key_tile = 32 * sh.wk * sh.ks;
   p.mts = (int)((rows + p.row_tile - 1) / p.row_tile);
-  // workgroups that fit a compute unit's LDS; no more workers than pieces of work the table has
-  // room for
-  const int tile_bytes = 2 * p.key_tile * row_bytes * sh.nst;
-  const int per_cu = tile_bytes > 65536 ? 1 : 2;
+  // as many workers as the GPU holds at once, and no more than pieces of work the table has room
+  // for
+  const int per_cu = sh.per_cu;
   const long long most = (long long)c.seqs * c.kv_heads * p.mts *
                          (((long long)c.cap + p.key_tile - 1) / p.key_tile);
   p.workers = (int)(most < (long long)kAttnCus * per_cu ? most : (long long)kAttnCus * per_cu);

@@ -153,7 +153,8 @@ def test_many_sequences(svm):
     check(svm, c, None, rng.integers(0, 3, 700).astype(np.int32))
 
 
-@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 64), ("bf16", 96), ("bf16", 128),
+                                     ("f32", 96), ("f32", 128), ("f32", 256), ("bf16", 256)])
 def test_long_and_ragged(svm, dtype, D):
     announce(f"tree attention {dtype} D={D}: one long sequence and a ragged batch (parts joined)")
     for lens, N, G in (([9000], 3, 2), ([5000, 0, 1, 700, 64], 12, 4), ([2500, 2501], 40, 4)):
