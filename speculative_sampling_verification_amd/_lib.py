@@ -528,6 +528,7 @@ class PagedCache:
         self._c = SVCache(ptr(k), ptr(v), _dtype_code(k), *k.shape, *strides[:4], seqs, width,
                           ptr(page_table), ptr(seq_lens), ptr(seq_pages), ptr(refcount))
         self._ref = ctypes.byref(self._c)
+        self._index = dev.index
         self._workspace_bytes = {}
 
     def _attention_workspace(self, N, q_heads):
@@ -548,21 +549,42 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _cache_call(cache, stream, fn, name, *args):
-    """Calls fn(*args, stream) with the cache's device current (a null stream is that device's)."""
-    dev = cache.device
-    if dev.index == torch.cuda.current_device():
-        _check(name, fn(*args, _stream(dev, stream)))
+def _arg(t, name, cache, dtype, shape):
+    """The address of an optional contiguous tensor argument on the cache's device."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == cache.device and t.is_contiguous()):
+        _need(t, name, cache.device, dtype, shape)  # says what is wrong
+    return t.data_ptr()
+
+
+def _raw_stream(cache, stream):
+    """The handle of the stream to launch on.  The lookup behind torch.cuda.current_stream, as
+    these calls are short enough for a Stream object to show."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(cache._index)
+
+
+def _cache_call(cache, name, fn, *args):
+    """Calls fn with the cache's device current (a null stream is that device's)."""
+    if torch._C._cuda_getDevice() == cache._index:
+        code = fn(*args)
     else:
-        with torch.cuda.device(dev):
-            _check(name, fn(*args, _stream(dev, stream)))
+        with torch.cuda.device(cache._index):
+            code = fn(*args)
+    if code != SV_OK:
+        raise SpecVerifyError(name, code)
 
 
 def _row_strides(t, name, cache, heads):
     """The element strides of a [seqs, N, heads, head_dim] tensor, None where it is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
-    if t.dtype != cache.dtype:
+    if t.dtype is not cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
     shape = t.shape
     if len(shape) != 4 or shape[0] != cache.seqs or shape[3] != cache.head_dim or (
@@ -590,29 +612,26 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     ``out`` may hold preallocated tensors under the same keys.
     """
     strides = _row_strides(q, "q", cache, None)
-    B, N, H, D = q.shape
+    shape = q.shape
+    B, N, H, D = shape
     dev = cache.device
-    if mask is not None:
-        _need(mask, "mask", dev, torch.uint8, (B, N, N))
-    if num_nodes is not None:
-        _need(num_nodes, "num_nodes", dev, torch.int32, (B,))
+    mask_at = _arg(mask, "mask", cache, torch.uint8, (B, N, N))
+    nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (B,))
     out = dict(out) if out else {}
-    o = out.get("out")
-    if o is None:
-        o = out["out"] = _new((B, N, H, D), q.dtype, dev, stream)
-    else:
-        _need(o, "out out", dev, q.dtype, (B, N, H, D))
-    lse = out.get("lse")
-    if lse is not None:
-        _need(lse, "out lse", dev, torch.float32, (B, N, H))
-    elif want_lse:
-        lse = out["lse"] = _new((B, N, H), torch.float32, dev, stream)
+    if "out" not in out:
+        out["out"] = _new(shape, q.dtype, dev, stream)
+    if want_lse and "lse" not in out:
+        out["lse"] = _new((B, N, H), torch.float32, dev, stream)
+    out_at = _arg(out["out"], "out out", cache, q.dtype, shape)
+    lse_at = _arg(out.get("lse"), "out lse", cache, torch.float32, (B, N, H))
     need = cache._attention_workspace(N, H)
-    ws = workspace(dev, need, stream)
-    _cache_call(cache, stream, _lib.spec_tree_attention, "spec_tree_attention", q.data_ptr(),
-                strides, N, H, cache._ref, layer, _ptr(mask), _ptr(num_nodes),
-                D ** -0.5 if scale is None else scale, o.data_ptr(), _ptr(lse), ws.data_ptr(),
-                ws.numel())
+    raw = _raw_stream(cache, stream)
+    ws = _workspaces.get((dev.type, cache._index, raw))
+    if ws is None or ws.numel() < need:
+        ws = workspace(dev, need, stream)
+    _cache_call(cache, "spec_tree_attention", _lib.spec_tree_attention, q.data_ptr(), strides, N,
+                H, cache._ref, layer, mask_at, nodes_at, D ** -0.5 if scale is None else scale,
+                out_at, lse_at, ws.data_ptr(), ws.numel(), raw)
     return out
 
 
@@ -624,13 +643,13 @@ def spec_cache_append(k_new, v_new, cache, *, layer=0, num_nodes=None, stream=No
     v_strides = _row_strides(v_new, "v_new", cache, cache.kv_heads)
     if k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new must have the same shape")
-    if (strides is None) != (v_strides is None) or (
-            strides is not None and list(strides) != list(v_strides)):
+    if strides is not v_strides and (strides is None or v_strides is None
+                                     or list(strides) != list(v_strides)):
         raise ValueError("k_new and v_new must have the same strides")
-    if num_nodes is not None:
-        _need(num_nodes, "num_nodes", cache.device, torch.int32, (cache.seqs,))
-    _cache_call(cache, stream, _lib.spec_cache_append, "spec_cache_append", k_new.data_ptr(),
-                v_new.data_ptr(), strides, k_new.shape[1], cache._ref, layer, _ptr(num_nodes))
+    nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (cache.seqs,))
+    _cache_call(cache, "spec_cache_append", _lib.spec_cache_append, k_new.data_ptr(),
+                v_new.data_ptr(), strides, k_new.shape[1], cache._ref, layer, nodes_at,
+                _raw_stream(cache, stream))
 
 
 def spec_cache_commit(cache, last_node, *, parent=None, num_nodes=None, out=None, stream=None):
@@ -640,21 +659,21 @@ def spec_cache_commit(cache, last_node, *, parent=None, num_nodes=None, out=None
 
     last_node [seqs] int32: spec_verify_tree's last_node with its parent [seqs, N]; without
     parent (a chain of num_nodes nodes, default 2048) spec_verify's num_accepted."""
-    dev = cache.device
-    _need(last_node, "last_node", dev, torch.int32, (cache.seqs,))
+    seqs = (cache.seqs,)
+    last_at = _arg(last_node, "last_node", cache, torch.int32, seqs)
+    if last_at is None:
+        raise TypeError("last_node must be a torch.Tensor")
     if parent is not None:
-        _need(parent, "parent", dev, torch.int32)
-        if parent.dim() != 2 or parent.shape[0] != cache.seqs:
-            raise ValueError("parent must be [seqs, N]")
-        N = parent.shape[1]
+        N = parent.shape[-1]
+        parent_at = _arg(parent, "parent", cache, torch.int32, (cache.seqs, N))
     else:
         N = 2048 if num_nodes is None else int(num_nodes)
+        parent_at = None
     if out is None:
-        out = _new((cache.seqs,), torch.int32, dev, stream)
-    else:
-        _need(out, "out", dev, torch.int32, (cache.seqs,))
-    _cache_call(cache, stream, _lib.spec_cache_commit, "spec_cache_commit", cache._ref,
-                last_node.data_ptr(), _ptr(parent), N, out.data_ptr())
+        out = _new(seqs, torch.int32, cache.device, stream)
+    _cache_call(cache, "spec_cache_commit", _lib.spec_cache_commit, cache._ref, last_at,
+                parent_at, N, _arg(out, "out", cache, torch.int32, seqs),
+                _raw_stream(cache, stream))
     return out
 
 
@@ -662,34 +681,28 @@ def spec_cache_resize(cache, want, *, new_lens=None, out=None, stream=None):
     """Gives back and takes pages so that each sequence holds those of want [seqs] int32 tokens
     (< 0: left alone, 0: freed); new_lens [seqs] int32 is stored to seq_lens first.  Returns ok
     [seqs] int32 (see include/spec_verify.h)."""
-    dev = cache.device
-    _need(want, "want", dev, torch.int32, (cache.seqs,))
-    if new_lens is not None:
-        _need(new_lens, "new_lens", dev, torch.int32, (cache.seqs,))
+    seqs = (cache.seqs,)
+    want_at = _arg(want, "want", cache, torch.int32, seqs)
+    lens_at = _arg(new_lens, "new_lens", cache, torch.int32, seqs)
     if out is None:
-        out = _new((cache.seqs,), torch.int32, dev, stream)
-    else:
-        _need(out, "out", dev, torch.int32, (cache.seqs,))
-    _cache_call(cache, stream, _lib.spec_cache_resize, "spec_cache_resize", cache._ref,
-                want.data_ptr(), _ptr(new_lens), out.data_ptr())
+        out = _new(seqs, torch.int32, cache.device, stream)
+    _cache_call(cache, "spec_cache_resize", _lib.spec_cache_resize, cache._ref, want_at, lens_at,
+                _arg(out, "out", cache, torch.int32, seqs), _raw_stream(cache, stream))
     return out
 
 
 def spec_cache_fork(cache, src, dst, *, out=None, stream=None):
     """Continues sequences src [F] int32 as the empty sequences dst [F] int32: full pages shared,
     a begun page copied in every layer.  Returns ok [F] int32 (see include/spec_verify.h)."""
-    dev = cache.device
-    _need(src, "src", dev, torch.int32)
     if src.dim() != 1:
         raise ValueError("src must be [F]")
-    F = src.shape[0]
-    _need(dst, "dst", dev, torch.int32, (F,))
+    F = src.shape
+    src_at = _arg(src, "src", cache, torch.int32, F)
+    dst_at = _arg(dst, "dst", cache, torch.int32, F)
     if out is None:
-        out = _new((F,), torch.int32, dev, stream)
-    else:
-        _need(out, "out", dev, torch.int32, (F,))
-    _cache_call(cache, stream, _lib.spec_cache_fork, "spec_cache_fork", cache._ref,
-                src.data_ptr(), dst.data_ptr(), F, out.data_ptr())
+        out = _new(F, torch.int32, cache.device, stream)
+    _cache_call(cache, "spec_cache_fork", _lib.spec_cache_fork, cache._ref, src_at, dst_at, F[0],
+                _arg(out, "out", cache, torch.int32, F), _raw_stream(cache, stream))
     return out
 
 

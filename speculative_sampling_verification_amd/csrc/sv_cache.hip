@@ -60,6 +60,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_append(CacheView c, const char
   *reinterpret_cast<u32x4*>(c.v + to) = vx;
 }
 
+size_t commit_lds_bytes(int N) { return (size_t)N * (2 * sizeof(int64_t) + 4 + 2) + 8; }
+
 // Accepted path of a breadth-first tree: node path[d] at depth d has path[d] >= d, so row
 // len + path[d] moves down to len + d and, taken in increasing d, no move overwrites a row that
 // a later one reads.  A thread owns 16 bytes of a row in one layer's keys or values and moves
@@ -68,9 +70,11 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
                                                          const int32_t* last, int N,
                                                          int32_t* out_lens, FastDiv row_div,
                                                          FastDiv head_div) {
-  __shared__ int32_t up[kCacheMaxNodes];    // parents, then the path from its end
-  __shared__ int16_t walk[kCacheMaxNodes];
-  __shared__ int64_t from[kCacheMaxNodes], to[kCacheMaxNodes];
+  extern __shared__ int64_t commit_lds[];   // commit_lds_bytes(N)
+  int64_t* from = commit_lds;               // row offsets along the path
+  int64_t* to = from + N;
+  int32_t* up = reinterpret_cast<int32_t*>(to + N);     // parents
+  int16_t* walk = reinterpret_cast<int16_t*>(up + N);   // the path from its end
   __shared__ int depth_sh, bad_sh;
   const int b = blockIdx.y, tid = threadIdx.x;
   const int len = clamp_len(c, c.lens[b]);
@@ -188,10 +192,12 @@ __device__ __forceinline__ int owner_of(const int* prefix, int n, int r) {
   return lo;
 }
 
-// Calls take(rank, page) for the free pages of lowest index, rank < want; returns how many
-// there were (at most want).  16 pages a thread and round.
+// Calls take(rank, page, b) for the free pages of lowest index, rank < want, b being the owner of
+// the rank in `prefix` (a thread's ranks follow each other: one search, then steps); returns how
+// many there were (at most want).  16 pages a thread and round.
 template <class F>
-__device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, int want, F take) {
+__device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, int want,
+                                              const int* prefix, int n, F take) {
   constexpr int kPer = 16;
   const bool vec = (reinterpret_cast<uintptr_t>(c.refcount) & 15u) == 0;
   int base = 0;
@@ -213,10 +219,14 @@ __device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, i
     }
     int all;
     int rank = base + block_prefix(s, __popc(free), &all);
-    while (free && rank < want) {
-      const int i = __ffs(free) - 1;
-      free &= free - 1;
-      take(rank++, (int)p + i);
+    if (free && rank < want) {
+      int b = owner_of(prefix, n, rank);
+      for (; free && rank < want; ++rank) {
+        const int i = __ffs(free) - 1;
+        free &= free - 1;
+        while (b + 1 < n && prefix[b + 1] <= rank) ++b;
+        take(rank, (int)p + i, b);
+      }
     }
     base += all;
   }
@@ -228,7 +238,7 @@ __device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, i
 __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const int32_t* want,
                                                               const int32_t* new_lens,
                                                               int32_t* out_ok) {
-  __shared__ int drop[kCacheMaxSeqs], grow[kCacheMaxSeqs];
+  __shared__ int drop[kCacheMaxSeqs], grow[kCacheMaxSeqs], kept[kCacheMaxSeqs];
   __shared__ PoolScan s;
   const int n = c.seqs;
   // what each sequence gives back and takes; out_ok: 2 = leave alone and report 0
@@ -249,24 +259,35 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
     const int need = ok ? need_of(b, held) : held;
     drop[b] = need < held ? held - need : 0;
     grow[b] = need > held ? need - held : 0;
+    kept[b] = need > held ? held : need;  // entries that stay: what is dropped or taken follows
     out_ok[b] = ok ? 1 : 2;
   }
   __syncthreads();
   const int dropped = prefix_counts(s, drop, n);
   const int wanted = prefix_counts(s, grow, n);
 
-  for (int r = threadIdx.x; r < dropped; r += kPoolThreads) {
-    const int b = owner_of(drop, n, r);
-    const int j = need_of(b, c.held[b]) + r - drop[b];
-    const int page = c.table[(size_t)b * c.width + j];
-    if (page >= 0 && page < c.pages) atomicSub(&c.refcount[page], 1);
+  // four dropped pages a thread and round, one after the other
+  constexpr int kRun = 4;
+  for (int r0 = threadIdx.x * kRun; r0 < dropped; r0 += kPoolThreads * kRun) {
+    int page[kRun], b = owner_of(drop, n, r0);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int r = r0 + i;
+      page[i] = -1;
+      if (r < dropped) {
+        while (b + 1 < n && drop[b + 1] <= r) ++b;
+        page[i] = c.table[(size_t)b * c.width + kept[b] + r - drop[b]];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (page[i] >= 0 && page[i] < c.pages) atomicSub(&c.refcount[page[i]], 1);
   }
   __threadfence();
   __syncthreads();
 
-  const int got = for_free_pages(s, c, wanted, [&](int r, int page) {
-    const int b = owner_of(grow, n, r);
-    c.table[(size_t)b * c.width + c.held[b] + r - grow[b]] = page;
+  const int got = for_free_pages(s, c, wanted, grow, n, [&](int r, int page, int b) {
+    c.table[(size_t)b * c.width + kept[b] + r - grow[b]] = page;
     c.refcount[page] = 1;
   });
 
@@ -330,8 +351,7 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const i
   }
   __syncthreads();
   const int wanted = prefix_counts(s, count, F);
-  const int got = for_free_pages(s, c, wanted, [&](int r, int page) {
-    const int f = owner_of(count, F, r);
+  const int got = for_free_pages(s, c, wanted, count, F, [&](int, int page, int f) {
     c.table[(size_t)dst[f] * c.width + fast_div(c.page_div, (uint32_t)c.lens[src[f]])] = page;
     c.refcount[page] = 1;
   });
@@ -411,8 +431,8 @@ hipError_t launch_cache_commit(const CacheView& c, const int32_t* parent, const 
   const int hv = head_vecs(c), rv = hv * c.kv_heads;
   const int64_t cols = parent ? (int64_t)c.layers * 2 * rv : 1;
   const unsigned blocks = (unsigned)((cols + kMoveThreads - 1) / kMoveThreads);
-  hipLaunchKernelGGL(k_commit, dim3(blocks, c.seqs), dim3(kMoveThreads), 0, stream, c, parent,
-                     last, N, out_lens, make_fast_div(rv), make_fast_div(hv));
+  hipLaunchKernelGGL(k_commit, dim3(blocks, c.seqs), dim3(kMoveThreads),
+                     commit_lds_bytes(N), stream, c, parent, last, N, out_lens, make_fast_div(rv), make_fast_div(hv));
   return hipGetLastError();
 }
 

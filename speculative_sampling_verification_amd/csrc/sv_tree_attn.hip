@@ -895,9 +895,10 @@ void k_tree_attn(AttnArgs a) {
         if (++t < t1) arrive(t);
       }
     } else {
-      put_rows(t0, load_entry(t0));
-      if (t0 + 1 < t1) put_rows(t0 + 1, load_entry(t0 + 1));
+      const int entry0 = load_entry(t0), entry1 = t0 + 1 < t1 ? load_entry(t0 + 1) : -1;
       int entry = t0 + 2 < t1 ? load_entry(t0 + 2) : -1;
+      put_rows(t0, entry0);
+      if (t0 + 1 < t1) put_rows(t0 + 1, entry1);
       __syncthreads();
       issue_all(t0);
       auto turn = [&](int t) SV_INLINE {
