@@ -141,41 +141,51 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
 // depends on the one before.
 
 struct PoolScan {
-  int wave[kPoolWaves];
+  int2 wave[2][kPoolWaves];
 };
 
-// Exclusive prefix of one value a thread over the workgroup; total in *all.
-__device__ __forceinline__ int block_prefix(PoolScan& s, int x, int* all) {
+// Exclusive prefix of a pair a thread over the workgroup; totals in *all.  `side` alternates
+// between calls: one barrier each.
+__device__ __forceinline__ int2 block_prefix(PoolScan& s, int side, int2 x, int2* all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int incl = x;
+  int2 incl = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(incl, d);
-    incl += lane >= d ? y : 0;
+    const int y = __shfl_up(incl.x, d), z = __shfl_up(incl.y, d);
+    incl.x += lane >= d ? y : 0;
+    incl.y += lane >= d ? z : 0;
   }
+  if (lane == 63) s.wave[side][wave] = incl;
   __syncthreads();
-  if (lane == 63) s.wave[wave] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
+  int2 before = make_int2(0, 0), total = make_int2(0, 0);
 #pragma unroll
   for (int i = 0; i < kPoolWaves; ++i) {
-    before += i < wave ? s.wave[i] : 0;
-    total += s.wave[i];
+    const int2 w = s.wave[side][i];
+    before.x += i < wave ? w.x : 0;
+    before.y += i < wave ? w.y : 0;
+    total.x += w.x;
+    total.y += w.y;
   }
   *all = total;
-  return before + incl - x;
+  return make_int2(before.x + incl.x - x.x, before.y + incl.y - x.y);
 }
 
-// Replaces the counts count[0..n) in LDS by their exclusive prefix sums;
-// returns the total.
-__device__ __forceinline__ int prefix_counts(PoolScan& s, int* count, int n) {
-  int base = 0;
-  for (int i0 = 0; i0 < n; i0 += kPoolThreads) {
+// Replaces two rows of counts in LDS (each thread's own entries i = thread mod kPoolThreads) by
+// their exclusive prefix sums; returns the totals.
+__device__ __forceinline__ int2 prefix_counts(PoolScan& s, int* u, int* v, int n) {
+  int2 base = make_int2(0, 0);
+  int side = 0;
+  for (int i0 = 0; i0 < n; i0 += kPoolThreads, side ^= 1) {
     const int i = i0 + threadIdx.x;
-    int all;
-    const int p = block_prefix(s, i < n ? count[i] : 0, &all);
-    if (i < n) count[i] = base + p;
-    base += all;
+    int2 all;
+    const int2 p =
+        block_prefix(s, side, i < n ? make_int2(u[i], v[i]) : make_int2(0, 0), &all);
+    if (i < n) {
+      u[i] = base.x + p.x;
+      v[i] = base.y + p.y;
+    }
+    base.x += all.x;
+    base.y += all.y;
   }
   __syncthreads();
   return base;
@@ -192,79 +202,76 @@ __device__ __forceinline__ int owner_of(const int* prefix, int n, int r) {
   return lo;
 }
 
-// Calls take(rank, page, b) for the free pages of lowest index, rank < want, b being the owner of
-// the rank in `prefix` (a thread's ranks follow each other: one search, then steps); returns how
-// many there were (at most want).  16 pages a thread and round.
+// Calls take(owner, rank in owner, page) for the free pages of lowest index, the owners' shares
+// given by `prefix` (a thread's ranks follow each other: one search, then steps), until `want`
+// are taken; returns how many there were.  Four pages a thread and round (few, so that the pages
+// found are spread over many threads), the next round's counts on their way meanwhile.
 template <class F>
 __device__ __forceinline__ int for_free_pages(PoolScan& s, const CacheView& c, int want,
                                               const int* prefix, int n, F take) {
-  constexpr int kPer = 16;
+  constexpr int kPer = 4, kRound = kPoolThreads * kPer;
   const bool vec = (reinterpret_cast<uintptr_t>(c.refcount) & 15u) == 0;
-  int base = 0;
-  for (int64_t p0 = 0; p0 < c.pages && base < want; p0 += kPoolThreads * kPer) {
-    const int64_t p = p0 + (int64_t)threadIdx.x * kPer;
-    uint32_t free = 0;
+  auto load = [&](int64_t p) {  // a page behind the last counts as held
+    int4 x = make_int4(1, 1, 1, 1);
     if (vec && p + kPer <= c.pages) {
-      int4 x[kPer / 4];
-#pragma unroll
-      for (int i = 0; i < kPer / 4; ++i)
-        x[i] = reinterpret_cast<const int4*>(c.refcount + p)[i];
-#pragma unroll
-      for (int i = 0; i < kPer / 4; ++i)
-        free |= ((x[i].x == 0) | (x[i].y == 0) << 1 | (x[i].z == 0) << 2 | (x[i].w == 0) << 3)
-                << (4 * i);
+      x = *reinterpret_cast<const int4*>(c.refcount + p);
     } else {
-      for (int i = 0; i < kPer; ++i)
-        if (p + i < c.pages) free |= (c.refcount[p + i] == 0 ? 1u : 0u) << i;
+      if (p < c.pages) x.x = c.refcount[p];
+      if (p + 1 < c.pages) x.y = c.refcount[p + 1];
+      if (p + 2 < c.pages) x.z = c.refcount[p + 2];
+      if (p + 3 < c.pages) x.w = c.refcount[p + 3];
     }
-    int all;
-    int rank = base + block_prefix(s, __popc(free), &all);
+    return x;
+  };
+  int base = 0, side = 0;
+  int4 next = load((int64_t)threadIdx.x * kPer);
+  for (int64_t p0 = 0; p0 < c.pages && base < want; p0 += kRound, side ^= 1) {
+    const int64_t p = p0 + (int64_t)threadIdx.x * kPer;
+    const int4 x = next;
+    next = load(p + kRound);
+    uint32_t free = (x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3;
+    int2 all;
+    int rank = base + block_prefix(s, side, make_int2(__popc(free), 0), &all).x;
     if (free && rank < want) {
       int b = owner_of(prefix, n, rank);
       for (; free && rank < want; ++rank) {
         const int i = __ffs(free) - 1;
         free &= free - 1;
         while (b + 1 < n && prefix[b + 1] <= rank) ++b;
-        take(rank, (int)p + i, b);
+        take(b, rank - prefix[b], (int)p + i);
       }
     }
-    base += all;
+    base += all.x;
   }
-  __threadfence_block();
-  __syncthreads();
   return base < want ? base : want;
 }
 
 __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const int32_t* want,
                                                               const int32_t* new_lens,
                                                               int32_t* out_ok) {
+  // prefix sums of the entries each sequence gives back and takes; kept: the entries that stay
+  // (what is dropped or taken follows them), complemented where a value is out of range
   __shared__ int drop[kCacheMaxSeqs], grow[kCacheMaxSeqs], kept[kCacheMaxSeqs];
   __shared__ PoolScan s;
   const int n = c.seqs;
-  // what each sequence gives back and takes; out_ok: 2 = leave alone and report 0
-  auto need_of = [&](int b, int held) {
-    const int w = want[b];
-    return w < 0 ? held : (int)fast_div(c.page_div, (uint32_t)w + c.page_div.d - 1);
-  };
   for (int b = threadIdx.x; b < n; b += kPoolThreads) {
-    const int held = c.held[b], w = want[b];
-    bool ok = held >= 0 && held <= c.width;
+    const int held = c.held[b], w = want[b], nl = new_lens ? new_lens[b] : 0;
     int len = c.lens[b];
+    bool ok = held >= 0 && held <= c.width;
     if (ok && new_lens) {
-      const int nl = new_lens[b];
       ok = nl >= 0 && nl <= (int64_t)held * c.page_size;
       if (ok) c.lens[b] = len = nl;
     }
     ok = ok && (w <= 0 || (w >= len && w <= c.cap));
-    const int need = ok ? need_of(b, held) : held;
+    if (ok && w == 0) c.lens[b] = 0;
+    const int need =
+        !ok || w < 0 ? held : (int)fast_div(c.page_div, (uint32_t)w + c.page_div.d - 1);
     drop[b] = need < held ? held - need : 0;
     grow[b] = need > held ? need - held : 0;
-    kept[b] = need > held ? held : need;  // entries that stay: what is dropped or taken follows
-    out_ok[b] = ok ? 1 : 2;
+    kept[b] = ok ? min(held, need) : ~0;
   }
-  __syncthreads();
-  const int dropped = prefix_counts(s, drop, n);
-  const int wanted = prefix_counts(s, grow, n);
+  const int2 totals = prefix_counts(s, drop, grow, n);
+  const int dropped = totals.x, wanted = totals.y;
 
   // four dropped pages a thread and round, one after the other
   constexpr int kRun = 4;
@@ -283,28 +290,30 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
     for (int i = 0; i < kRun; ++i)
       if (page[i] >= 0 && page[i] < c.pages) atomicSub(&c.refcount[page[i]], 1);
   }
-  __threadfence();
-  __syncthreads();
-
-  const int got = for_free_pages(s, c, wanted, grow, n, [&](int r, int page, int b) {
-    c.table[(size_t)b * c.width + kept[b] + r - grow[b]] = page;
-    c.refcount[page] = 1;
-  });
+  int got = 0;
+  if (wanted) {
+    // the counts are read by this workgroup alone, and were not read before the atomics (which
+    // act in the L2 behind its loads)
+    __threadfence_block();
+    __syncthreads();
+    got = for_free_pages(s, c, wanted, grow, n, [&](int b, int i, int page) {
+      c.table[(size_t)b * c.width + kept[b] + i] = page;
+      c.refcount[page] = 1;
+    });
+    __threadfence_block();
+    __syncthreads();
+  }
 
   // sequences are served in order until one does not fit; what that one was given goes back
   for (int b = threadIdx.x; b < n; b += kPoolThreads) {
-    const int g = (b + 1 < n ? grow[b + 1] : wanted) - grow[b];
-    const int held = c.held[b];
-    int ok = out_ok[b] == 1;
-    if (ok && g > 0 && grow[b] + g > got) {
+    const int first = grow[b], g = (b + 1 < n ? grow[b + 1] : wanted) - first;
+    int ok = kept[b] >= 0;
+    if (ok && g > 0 && first + g > got) {
       ok = 0;
-      for (int r = grow[b]; r < got; ++r)
-        c.refcount[c.table[(size_t)b * c.width + held + r - grow[b]]] = 0;
+      for (int r = first; r < got; ++r)
+        c.refcount[c.table[(size_t)b * c.width + kept[b] + r - first]] = 0;
     }
-    if (ok) {
-      c.held[b] = need_of(b, held);
-      if (want[b] == 0) c.lens[b] = 0;
-    }
+    if (ok) c.held[b] = kept[b] + g;
     out_ok[b] = ok;
   }
 }
@@ -314,7 +323,8 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const i
                                                             int32_t* out_ok) {
   // first[s]: the first fork into slot s, F if none; bit 31: s is some fork's source
   __shared__ uint32_t first[kCacheMaxSeqs];
-  __shared__ int count[kCacheMaxSeqs];
+  // prefix sums of the pages each fork needs (0 or 1) and of the full pages it shares
+  __shared__ int part[kCacheMaxSeqs], full[kCacheMaxSeqs];
   __shared__ PoolScan s;
   for (int i = threadIdx.x; i < c.seqs; i += kPoolThreads) first[i] = (uint32_t)F;
   __syncthreads();
@@ -332,54 +342,44 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const i
   for (int f = threadIdx.x; f < F; f += kPoolThreads) {
     const int x = src[f], d = dst[f];
     bool ok = x >= 0 && x < c.seqs && d >= 0 && d < c.seqs;
+    const int len = ok ? c.lens[x] : 0, held = ok ? c.held[x] : 0, there = ok ? c.held[d] : 0;
     // into an empty slot that is no fork's source, and by its first fork
-    ok = ok && first[d] == (uint32_t)f && c.held[d] == 0;
-    bool part = false;
-    if (ok) {
-      const int len = c.lens[x], held = c.held[x];
-      ok = len >= 0 && held >= 0 && held <= c.width && len <= (int64_t)held * c.page_size;
-      const int full = ok ? (int)fast_div(c.page_div, (uint32_t)len) : 0;
-      part = ok && len != full * c.page_size;
-      if (part) {
-        const int page = c.table[(size_t)x * c.width + full];
-        ok = page >= 0 && page < c.pages;
-        part = ok;
-      }
+    ok = ok && first[d] == (uint32_t)f && there == 0;
+    ok = ok && len >= 0 && held >= 0 && held <= c.width && len <= (int64_t)held * c.page_size;
+    const int whole = ok ? (int)fast_div(c.page_div, (uint32_t)len) : 0;
+    bool begun = ok && len != whole * c.page_size;
+    if (begun) {
+      const int page = c.table[(size_t)x * c.width + whole];
+      ok = begun = page >= 0 && page < c.pages;
     }
-    count[f] = part ? 1 : 0;
+    part[f] = begun ? 1 : 0;
+    full[f] = ok ? whole : 0;
     out_ok[f] = ok ? 1 : 0;
   }
-  __syncthreads();
-  const int wanted = prefix_counts(s, count, F);
-  const int got = for_free_pages(s, c, wanted, count, F, [&](int, int page, int f) {
-    c.table[(size_t)dst[f] * c.width + fast_div(c.page_div, (uint32_t)c.lens[src[f]])] = page;
+  const int2 totals = prefix_counts(s, part, full, F);
+  const int wanted = totals.x, shared = totals.y;
+  auto count = [&](const int* prefix, int f, int all) {
+    return (f + 1 < F ? prefix[f + 1] : all) - prefix[f];
+  };
+  const int got = for_free_pages(s, c, wanted, part, F, [&](int f, int, int page) {
+    c.table[(size_t)dst[f] * c.width + count(full, f, shared)] = page;
     c.refcount[page] = 1;
   });
-  // forks without a page fail; the others share the full pages
-  for (int f0 = 0; f0 < F; f0 += kPoolThreads) {
-    const int f = f0 + threadIdx.x;
-    int full = 0;
-    bool ok = f < F && out_ok[f] == 1;
-    int part = 0;
-    if (ok) {
-      part = (f + 1 < F ? count[f + 1] : wanted) - count[f];
-      ok = part == 0 || count[f] < got;
-      full = ok ? (int)fast_div(c.page_div, (uint32_t)c.lens[src[f]]) : 0;
+  // a fork without the page it needs fails; the others take their length and the full pages
+  auto served = [&](int f) { return count(part, f, wanted) == 0 || part[f] < got; };
+  for (int f = threadIdx.x; f < F; f += kPoolThreads) {
+    if (out_ok[f] != 1) continue;
+    if (served(f)) {
+      const int d = dst[f];
+      c.held[d] = count(full, f, shared) + count(part, f, wanted);
+      c.lens[d] = c.lens[src[f]];
+    } else {
+      out_ok[f] = 0;
     }
-    __syncthreads();  // count[f + 1] of the last thread is read before it is replaced
-    if (f < F) {
-      out_ok[f] = ok ? 1 : 0;
-      if (ok) {
-        c.held[dst[f]] = full + part;
-        c.lens[dst[f]] = c.lens[src[f]];
-      }
-      count[f] = full;
-    }
-    __syncthreads();
   }
-  const int shared = prefix_counts(s, count, F);
   for (int r = threadIdx.x; r < shared; r += kPoolThreads) {
-    const int f = owner_of(count, F, r), j = r - count[f];
+    const int f = owner_of(full, F, r), j = r - full[f];
+    if (!served(f)) continue;
     const int page = c.table[(size_t)src[f] * c.width + j];
     c.table[(size_t)dst[f] * c.width + j] = page;
     if (page >= 0 && page < c.pages) atomicAdd(&c.refcount[page], 1);
