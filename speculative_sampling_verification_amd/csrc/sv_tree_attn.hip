@@ -21,7 +21,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -45,7 +44,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // whose captures it keeps in memory, is reached through private memory by flat instructions.
 #define SV_INLINE __attribute__((always_inline))
 #define SV_LDS(T) __attribute__((address_space(3))) T
-#define SV_GLOBAL(T) __attribute__((address_space(1))) T
 
 // max / sum with the lane 32 away
 __device__ __forceinline__ float half_max(float x) {
@@ -120,14 +118,14 @@ __device__ __forceinline__ bool clear_non_finite(u32x4& x) {
   return any;
 }
 
-// WM waves share the rows (RB blocks of 32 each), WK the keys of a tile (KS blocks of 32 each);
+// WM waves share the rows (32 each), WK the keys of a tile (KS blocks of 32 each);
 // NST tiles are kept in LDS, loaded there directly from global memory.
-template <bool BF16, int D, int WM, int WK, int KS, int RB, int NST>
+template <bool BF16, int D, int WM, int WK, int KS, int NST>
 struct Attn {
   static constexpr int kES = BF16 ? 2 : 4;
   static constexpr int kNW = WM * WK;
   static constexpr int kNT = 64 * kNW;
-  static constexpr int kMT = 32 * WM * RB;
+  static constexpr int kMT = 32 * WM;
   static constexpr int kBN = 32 * WK * KS;
   static constexpr int kRow = D * kES;        // bytes of a row, in memory and in LDS
   static constexpr int kVecs = kRow / 16;     // 16-byte vectors of a row
@@ -138,7 +136,6 @@ struct Attn {
   static constexpr int kJoinBytes = WK > 1 ? kNW * kND * 16 * 64 * 4 : 0;
   static constexpr int kPool = NST * kTileBytes > kJoinBytes ? NST * kTileBytes : kJoinBytes;
   static_assert(D % 32 == 0 && (kBN * kVecs) % kNT == 0 && kBN % 64 == 0 && kBN <= kNT, "tile");
-  static_assert(RB == 1 || WK == 1, "waves join one block of rows");
 
   // Direct loads fill LDS in lane order, so rows are not padded; instead vector c of row r lies
   // at place c ^ swz(r) of its row, which a lane gets by loading that vector.
@@ -218,10 +215,10 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <bool BF16, int D, int WM, int WK, int KS, int RB, int NST, int OCC>
+template <bool BF16, int D, int WM, int WK, int KS, int NST, int OCC>
 __global__ __launch_bounds__(64 * WM * WK) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void k_tree_attn(AttnArgs a) {
-  using C = Attn<BF16, D, WM, WK, KS, RB, NST>;
+  using C = Attn<BF16, D, WM, WK, KS, NST>;
   constexpr int MT = C::kMT, BN = C::kBN, NT = C::kNT, ND = C::kND;
   constexpr int QF = BF16 ? D / 16 : D / 8;  // 16-byte pieces of a Q row a lane holds
   __shared__ typename C::Lds S;
@@ -299,7 +296,7 @@ void k_tree_attn(AttnArgs a) {
   long long off = uniform(S.start_off);
   const long long begin = pos;
 
-  while (pos < end) {
+  while (pos < end && (uint32_t)b < (uint32_t)a.c.seqs) {
     SeqWork sw = work_of(b);
     sw.len = __builtin_amdgcn_readfirstlane(sw.len);
     sw.n = __builtin_amdgcn_readfirstlane(sw.n);
@@ -348,25 +345,18 @@ void k_tree_attn(AttnArgs a) {
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     const char* kbase = a.c.k + (long long)h * a.c.head_stride;
     const char* vbase = a.c.v + (long long)h * a.c.head_stride;
-    // live nodes of the row tile, and the node of each row of this lane (dead rows: the last one;
-    // what they compute is dropped)
+    // live nodes of the row tile, and the node of this lane's row (a dead row: the last one; what
+    // it computes is dropped)
     const int first_node = mt * MT / a.G;
     const int last_node = (rows < (mt + 1) * MT ? sw.n : ((mt + 1) * MT - 1) / a.G + 1) - 1;
-    int my_node[RB];
-    u32x4 qf[RB][QF];
+    const int my_row = mt * MT + wm * 32 + col;
+    const int my_node = my_row < rows ? my_row / a.G : last_node;
+    const char* qp = a.q + (long long)b * a.q_seq + (long long)my_node * a.q_node +
+                     (long long)(h * a.G + my_row - my_node * a.G) * a.q_head + half * 16;
+    u32x4 qf[QF];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int row = mt * MT + (wm * RB + rb) * 32 + col;
-      const bool row_live = row < rows;
-      const int node = row_live ? row / a.G : last_node, g = row - node * a.G;
-      my_node[rb] = node;
-      const char* qp = a.q + (long long)b * a.q_seq + (long long)node * a.q_node +
-                       (long long)(h * a.G + g) * a.q_head + half * 16;
-#pragma unroll
-      for (int s = 0; s < QF; ++s)
-        qf[rb][s] = row_live ? *reinterpret_cast<const u32x4*>(qp + s * 32)
-                                      : u32x4{0, 0, 0, 0};
-    }
+    for (int s = 0; s < QF; ++s)
+      qf[s] = my_row < rows ? *reinterpret_cast<const u32x4*>(qp + s * 32) : u32x4{0, 0, 0, 0};
 
     // row that this thread's vector of pass i belongs to (a pass covers whole rows, or not)
     auto row_of = [&](int i) SV_INLINE {
@@ -378,15 +368,15 @@ void k_tree_attn(AttnArgs a) {
       if (tid >= BN || key >= sw.keys) return -1;
       return table[fast_div(a.c.page_div, (uint32_t)key)];
     };
-    auto put_rows = [&](int t, int page, int first = 0) SV_INLINE {  // by threads first .. first + BN - 1
+    // by threads first .. first + BN - 1
+    auto put_rows = [&](int t, int page, int first = 0) SV_INLINE {
       if (tid >= first && tid < first + BN) {
         const int at = fresh(tid) - first, key = t * BN + at;
         const bool ok = page >= 0 && page < a.c.pages;
         const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
         const int slot = key - (int)(pi * a.c.page_div.d);
-        S.rowoff[t & (C::kRing - 1)][at] = ok ? (long long)page * a.c.page_stride +
-                                       (long long)slot * a.c.token_stride
-                                 : 0ll;
+        S.rowoff[t & (C::kRing - 1)][at] =
+            ok ? (long long)page * a.c.page_stride + (long long)slot * a.c.token_stride : 0ll;
         const unsigned long long bits = __ballot(ok);
         if (lane == 0) {
           S.valid[t & (C::kRing - 1)][(at >> 5)] = (uint32_t)bits;
@@ -406,7 +396,8 @@ void k_tree_attn(AttnArgs a) {
     auto issue = [&](int t, int i, unsigned long long lanes = ~0ull) SV_INLINE {
       const uint32_t to =
           pool_at + (t & (NST - 1)) * C::kTileBytes + wave * 1024 + i * (NT * 16);
-      const int r = row_of(i), p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
+      const int r = row_of(i);
+      const int p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
       load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to, lanes);
       load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow, lanes);
     };
@@ -436,8 +427,8 @@ void k_tree_attn(AttnArgs a) {
       for (int k0 = 0; k0 < BN; k0 += 64) {
         const int node = t * BN + k0 + fresh(lane) - sw.len;
         const int near = node < 0 ? 0 : node < a.N ? node : a.N - 1;
-        const unsigned long long there =
-            S.valid[t & (C::kRing - 1)][k0 / 32] | (unsigned long long)S.valid[t & (C::kRing - 1)][k0 / 32 + 1] << 32;
+        const uint32_t* there32 = &S.valid[t & (C::kRing - 1)][k0 / 32];
+        const unsigned long long there = there32[0] | (unsigned long long)there32[1] << 32;
 #pragma unroll 1
         for (int r0 = wave; first_node + r0 <= last_node; r0 += 8 * C::kNW) {
           uint8_t shown[8];
@@ -463,17 +454,12 @@ void k_tree_attn(AttnArgs a) {
 
     const int kr = wk * KS * 32 + col;  // this lane's key row in its first block of 32
     const int sw_k = C::swz_k(kr);      // the same for every block of 32 keys
-    float m[RB], l[RB];
-    f32x16 acc[RB][ND];
+    float m = -INFINITY, l = 0.0f;
+    f32x16 acc[ND];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      m[rb] = -INFINITY;
-      l[rb] = 0.0f;
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[rb][d][r] = 0.0f;
-    }
+      for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
     // The shift m of a row's weights 2^(z - m), in units of log2 (so that weights and rescalings
     // use the same rounded number): a key's maximum that was the row's running one, or lies less
@@ -481,18 +467,18 @@ void k_tree_attn(AttnArgs a) {
     // relative to size), and O and l are rescaled a few times a row instead of every time some
     // row of the wave meets a new maximum.  Returns what is subtracted (0 while nothing is seen).
     constexpr float kSlack = 8.0f;
-    auto raise = [&](int rb, float top) SV_INLINE -> float {
-      const float m_new = fmaxf(m[rb], half_max(top) * sl2);
-      if (__any(m_new > m[rb] + kSlack)) {
-        const float f = __builtin_amdgcn_exp2f(m[rb] - (m_new == -INFINITY ? 0.0f : m_new));
-        l[rb] *= f;
+    auto raise = [&](float top) SV_INLINE -> float {
+      const float m_new = fmaxf(m, half_max(top) * sl2);
+      if (__any(m_new > m + kSlack)) {
+        const float f = __builtin_amdgcn_exp2f(m - (m_new == -INFINITY ? 0.0f : m_new));
+        l *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[rb][d][r] *= f;
-        m[rb] = m_new;
+          for (int r = 0; r < 16; ++r) acc[d][r] *= f;
+        m = m_new;
       }
-      return m[rb] == -INFINITY ? 0.0f : m[rb];
+      return m == -INFINITY ? 0.0f : m;
     };
 
     // One tile: scores of this wave's keys, softmax, product with the values.  `Rough` tiles hold
@@ -506,7 +492,7 @@ void k_tree_attn(AttnArgs a) {
       constexpr int kAhead = 4, kKeyFrags = KS * QF;
       constexpr int kPace = kKeyFrags / C::kLoads > 0 ? kKeyFrags / C::kLoads : 1;
       static_assert(NST != 2 || kKeyFrags >= C::kLoads, "a pass per fragment at most");
-      f32x16 s[KS][RB];
+      f32x16 s[KS];
       const char* kp = tile + kr * C::kRow;
       auto key_frag = [&](int n) SV_INLINE {
         return *reinterpret_cast<const u32x4*>(kp + n / QF * (32 * C::kRow) +
@@ -519,22 +505,18 @@ void k_tree_attn(AttnArgs a) {
 #pragma unroll
       for (int n = 0; n < kKeyFrags; ++n) {
         const int ks = n / QF, q = n % QF;
+        if (q == 0)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          if (q == 0)
+          for (int r = 0; r < 16; ++r) s[ks][r] = 0.0f;
+        if constexpr (BF16) {
+          s[ks] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, kf[n % kAhead]), __builtin_bit_cast(bf16x8, qf[q]), s[ks],
+              0, 0, 0);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[ks][rb][r] = 0.0f;
-          if constexpr (BF16) {
-            s[ks][rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, kf[n % kAhead]), __builtin_bit_cast(bf16x8, qf[rb][q]),
-                s[ks][rb], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[ks][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                  __uint_as_float(kf[n % kAhead][e]), __uint_as_float(qf[rb][q][e]), s[ks][rb],
-                  0, 0, 0);
-          }
+          for (int e = 0; e < 4; ++e)
+            s[ks] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kf[n % kAhead][e]),
+                                                         __uint_as_float(qf[q][e]), s[ks], 0, 0, 0);
         }
         if (n + kAhead < kKeyFrags) kf[n % kAhead] = key_frag(n + kAhead);
         // the next tile's loads start in the shadow of these products
@@ -544,41 +526,32 @@ void k_tree_attn(AttnArgs a) {
       }
 
       // hide keys that the row does not see
-      uint32_t seen[KS][RB];
+      uint32_t seen[KS];
       if constexpr (Rough) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t bits =
+              of_half(S.sees[my_node - first_node][wk * KS + ks] >> (4 * half));
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            const uint32_t bits = of_half(
-                S.sees[my_node[rb] - first_node][wk * KS + ks] >> (4 * half));
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              s[ks][rb][r] = bits & (1u << r) ? s[ks][rb][r] : -INFINITY;
-            seen[ks][rb] = bits;
-          }
+          for (int r = 0; r < 16; ++r) s[ks][r] = bits & (1u << r) ? s[ks][r] : -INFINITY;
+          seen[ks] = bits;
+        }
       }
 
-      float shift[RB];
+      float mx = s[0][0];
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        float mx = s[0][rb][0];
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[ks][rb][r]);
-        shift[rb] = raise(rb, mx);
-      }
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[ks][r]);
+      const float shift = raise(mx);
       // P of registers [8 j + r0, 8 j + r0 + n) of the wave's 16 KS keys a lane
       auto weigh = [&](int j, int r0, int n) SV_INLINE {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-          for (int r = r0; r < r0 + n; ++r) {
-            const int i = 8 * (j & 1) + r;
-            s[j >> 1][rb][i] = __builtin_amdgcn_exp2f(s[j >> 1][rb][i] * sl2 - shift[rb]);
-            l[rb] += s[j >> 1][rb][i];
-          }
+        for (int r = r0; r < r0 + n; ++r) {
+          const int i = 8 * (j & 1) + r;
+          s[j >> 1][i] = __builtin_amdgcn_exp2f(s[j >> 1][i] * sl2 - shift);
+          l += s[j >> 1][i];
+        }
       };
 
       // O^T += V^T P^T
@@ -607,20 +580,16 @@ void k_tree_attn(AttnArgs a) {
         for (int j = 0; j < kChunks; ++j) {
           // P rounded to bf16 for the matrix instruction: half a step of 2^-8 per weight, the
           // rounding the inputs carry; the sum l keeps the unrounded weights
-          bf16x8 pf[RB];
+          bf16x8 pf;
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pf[rb][i] = (__bf16)s[j >> 1][rb][8 * (j & 1) + i];
+          for (int i = 0; i < 8; ++i) pf[i] = (__bf16)s[j >> 1][8 * (j & 1) + i];
           // the next keys' weights are computed in the shadow of these products
           constexpr int kShare = (8 + ND - 1) / ND;
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
             const int n = j * ND + d;
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-              acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf[rb], acc[rb][d], 0, 0, 0);
+            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf, acc[d], 0, 0, 0);
             if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(n + kAhead);
             if (j + 1 < kChunks && d * kShare < 8)
               weigh(j + 1, d * kShare, 8 - d * kShare < kShare ? 8 - d * kShare : kShare);
@@ -643,11 +612,8 @@ void k_tree_attn(AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < kFrags; ++n) {
           const int r = n / ND, d = n % ND;
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
-            acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf[n % kAhead],
-                                                              s[r >> 4][rb][r & 15], acc[rb][d],
-                                                              0, 0, 0);
+          acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf[n % kAhead], s[r >> 4][r & 15], acc[d],
+                                                        0, 0, 0);
           if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(n + kAhead);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -660,35 +626,32 @@ void k_tree_attn(AttnArgs a) {
         // over a copy of O in scratch memory keeps it out of the registers of the common path)
         const uint32_t bad = Rough ? S.badv[t & (C::kRing - 1)][blk] : 0u;
         if (Rough && __builtin_expect(bad != 0, 0)) {
+          float o[ND * 16];
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            float o[ND * 16];
+          for (int i = 0; i < ND * 16; ++i) o[i] = acc[i >> 4][i & 15];
+          asm volatile("" : : "v"(o) : "memory");  // stays in scratch memory
+          for (uint32_t left = bad; left; left &= left - 1) {
+            const int kk = __builtin_amdgcn_readfirstlane(__ffs(left) - 1);
+            const int hk = (kk >> 2) & 1, rk = ((kk >> 3) << 2) | (kk & 3);
+            float p = 0.0f;
 #pragma unroll
-            for (int i = 0; i < ND * 16; ++i) o[i] = acc[rb][i >> 4][i & 15];
-            asm volatile("" : : "v"(o) : "memory");  // stays in scratch memory
-            for (uint32_t left = bad; left; left &= left - 1) {
-              const int kk = __builtin_amdgcn_readfirstlane(__ffs(left) - 1);
-              const int hk = (kk >> 2) & 1, rk = ((kk >> 3) << 2) | (kk & 3);
-              float p = 0.0f;
-#pragma unroll
-              for (int r = 0; r < 16; ++r) p = r == rk ? s[ks][rb][r] : p;
-              p = __shfl(p, col + 32 * hk);
-              const int sees = __shfl((int)(seen[ks][rb] >> rk & 1u), col + 32 * hk);
-              const char* row = vbase + S.rowoff[t & (C::kRing - 1)][blk * 32 + kk];
+            for (int r = 0; r < 16; ++r) p = r == rk ? s[ks][r] : p;
+            p = __shfl(p, col + 32 * hk);
+            const int sees = __shfl((int)(seen[ks] >> rk & 1u), col + 32 * hk);
+            const char* row = vbase + S.rowoff[t & (C::kRing - 1)][blk * 32 + kk];
 #pragma unroll 1
-              for (int i = 0; i < ND * 16; ++i) {
-                const int e = (i >> 4) * 32 + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
-                float x;
-                if constexpr (BF16)
-                  x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
-                else
-                  x = reinterpret_cast<const float*>(row)[e];
-                if (sees && non_finite(__float_as_uint(x))) o[i] += p * x;
-              }
+            for (int i = 0; i < ND * 16; ++i) {
+              const int e = (i >> 4) * 32 + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
+              float x;
+              if constexpr (BF16)
+                x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
+              else
+                x = reinterpret_cast<const float*>(row)[e];
+              if (sees && non_finite(__float_as_uint(x))) o[i] += p * x;
             }
-#pragma unroll
-            for (int i = 0; i < ND * 16; ++i) acc[rb][i >> 4][i & 15] = o[i];
           }
+#pragma unroll
+          for (int i = 0; i < ND * 16; ++i) acc[i >> 4][i & 15] = o[i];
           __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0) here: not in the common path's tiles
         }
       }
@@ -719,7 +682,8 @@ void k_tree_attn(AttnArgs a) {
           (uint32_t)reinterpret_cast<uintptr_t>((SV_LDS(char)*)S.entry);
       {  // rows of the first eight tiles, a wave each
         const int t = t0 + wave, key = t * BN + lane;
-        const int page = t < t1 && key < sw.keys ? table[fast_div(a.c.page_div, (uint32_t)key)] : -1;
+        const int page =
+            t < t1 && key < sw.keys ? table[fast_div(a.c.page_div, (uint32_t)key)] : -1;
         if (t < t1) put_rows(t, page, 64 * wave);
       }
       __syncthreads();
@@ -750,9 +714,9 @@ void k_tree_attn(AttnArgs a) {
           tile_barrier();
       };
 
-      constexpr int kAhead = 4, kUnits = 16 * RB, kEarly = 6, kFirst = kUnits * 11 / 16;
-      f32x16 sa[RB], sb[RB];
-      float mx[RB], shift[RB];
+      constexpr int kAhead = 4, kEarly = 6, kFirst = 11;
+      f32x16 sa, sb;
+      float mx, shift;
       u32x4 kf[kAhead];
       typedef short short8v __attribute__((ext_vector_type(8)));
       short8v vf[kAhead];
@@ -770,46 +734,34 @@ void k_tree_attn(AttnArgs a) {
             __builtin_amdgcn_ds_read_tr16_b64_v4i16((SV_LDS(short4v)*)(at + 8 * C::kRow));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       };
-      // weights u0 .. u1 - 1 of a block, in the order they are used: 16 keys, row block, register
-      auto weigh = [&](f32x16 (&s)[RB], int u0, int u1) SV_INLINE {
+      // weights of registers u0 .. u1 - 1 of a block
+      auto weigh = [&](f32x16& s, int u0, int u1) SV_INLINE {
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
-          const int rb = u / 8 % RB, r = u / (8 * RB) * 8 + u % 8;
-          s[rb][r] = __builtin_amdgcn_exp2f(s[rb][r] * sl2 - shift[rb]);
-          l[rb] += s[rb][r];
+          s[u] = __builtin_amdgcn_exp2f(s[u] * sl2 - shift);
+          l += s[u];
         }
       };
-      auto score = [&](f32x16 (&s)[RB], int rb, int q) SV_INLINE {
+      auto score = [&](f32x16& s, int q) SV_INLINE {
         if (q == 0)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[rb][r] = 0.0f;
-        s[rb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, kf[q % kAhead]), __builtin_bit_cast(bf16x8, qf[rb][q]),
-            s[rb], 0, 0, 0);
-      };
-      auto raise_all = [&]() SV_INLINE {
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) shift[rb] = raise(rb, mx[rb]);
+          for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, kf[q % kAhead]), __builtin_bit_cast(bf16x8, qf[q]),
+            s, 0, 0, 0);
       };
       // Scores of block (next tile, next_sub) into nx beside the first weights of cu, whose first
       // values (of cur tile, sub) are fetched at the end; `loads`: tile t + 2's loads start too.
-      auto scores_beside = [&](const char* next, int next_sub, f32x16 (&nx)[RB], const char* cur,
-                               int sub, f32x16 (&cu)[RB], int load_tile, auto loads) SV_INLINE {
-        constexpr int kSlots = QF * RB;
+      auto scores_beside = [&](const char* next, int next_sub, f32x16& nx, const char* cur,
+                               int sub, f32x16& cu, int load_tile, auto loads) SV_INLINE {
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) kf[q] = key_frag(next, next_sub, q);
         weigh(cu, 0, kEarly);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < QF; ++q) {
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            const int slot = q * RB + rb;
-            score(nx, rb, q);
-            weigh(cu, kEarly + (kFirst - kEarly) * slot / kSlots,
-                  kEarly + (kFirst - kEarly) * (slot + 1) / kSlots);
-            if (rb + 1 < RB) __builtin_amdgcn_sched_barrier(0);
-          }
+          score(nx, q);
+          weigh(cu, kEarly + (kFirst - kEarly) * q / QF, kEarly + (kFirst - kEarly) * (q + 1) / QF);
           if (q + kAhead < QF) kf[q % kAhead] = key_frag(next, next_sub, q + kAhead);
           else vf[q + kAhead - QF] = value_frag(cur, sub, q + kAhead - QF);
           __builtin_amdgcn_sched_barrier(0);
@@ -818,37 +770,28 @@ void k_tree_attn(AttnArgs a) {
         }
       };
       // O += block (cur tile, sub) with weights cu beside the maxima of nx
-      auto values_beside = [&](const char* cur, int sub, f32x16 (&cu)[RB], f32x16 (&nx)[RB]) SV_INLINE {
-        constexpr int kFrags = 2 * ND, kSlots = ND * RB;
-        bf16x8 pf[RB];
+      auto values_beside = [&](const char* cur, int sub, f32x16& cu, f32x16& nx) SV_INLINE {
+        constexpr int kFrags = 2 * ND;
+        bf16x8 pf;
 #pragma unroll
         for (int n = 0; n < kFrags; ++n) {
           const int c = n / ND, d = n % ND;
           if (d == 0)  // P rounded to bf16: half a step of 2^-8 per weight
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
+            for (int i = 0; i < 8; ++i) pf[i] = (__bf16)cu[8 * c + i];
+          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf, acc[d], 0, 0, 0);
+          if (c == 0) {
+            weigh(cu, kFirst + (16 - kFirst) * d / ND, kFirst + (16 - kFirst) * (d + 1) / ND);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) pf[rb][i] = (__bf16)cu[rb][8 * c + i];
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            const int slot = d * RB + rb;
-            acc[rb][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, vf[n % kAhead]), pf[rb], acc[rb][d], 0, 0, 0);
-            if (c == 0) {
-              weigh(cu, kFirst + (kUnits - kFirst) * slot / kSlots,
-                    kFirst + (kUnits - kFirst) * (slot + 1) / kSlots);
-            } else {
-#pragma unroll
-              for (int r = 16 * d / ND; r < 16 * (d + 1) / ND; ++r)
-                mx[rb] = r == 0 ? nx[rb][0] : fmaxf(mx[rb], nx[rb][r]);
-            }
-            if (rb + 1 < RB) __builtin_amdgcn_sched_barrier(0);
+            for (int r = 16 * d / ND; r < 16 * (d + 1) / ND; ++r)
+              mx = r == 0 ? nx[0] : fmaxf(mx, nx[r]);
           }
           if (n + kAhead < kFrags) vf[n % kAhead] = value_frag(cur, sub, n + kAhead);
           __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) asm volatile("" : "+v"(mx[rb]));  // not moved from here
+        asm volatile("" : "+v"(mx));  // not moved from here
       };
 
       int t = t0;
@@ -860,25 +803,21 @@ void k_tree_attn(AttnArgs a) {
         for (int q = 0; q < kAhead; ++q) kf[q] = key_frag(tile, 0, q);
 #pragma unroll
         for (int q = 0; q < QF; ++q) {
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) score(sa, rb, q);
+          score(sa, q);
           if (q + kAhead < QF) kf[q % kAhead] = key_frag(tile, 0, q + kAhead);
         }
+        mx = sa[0];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          mx[rb] = sa[rb][0];
-#pragma unroll
-          for (int r = 1; r < 16; ++r) mx[rb] = fmaxf(mx[rb], sa[rb][r]);
-        }
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sa[r]);
       }
       while (plain) {
         const char* tile = S.pool + (t & 3) * C::kTileBytes;
         if (t + 2 < t1) find_rows(t + 2);
         keep_books(t);
-        raise_all();
+        shift = raise(mx);
         scores_beside(tile, 1, sb, tile, 0, sa, t + 2, std::true_type{});
         values_beside(tile, 0, sa, sb);
-        raise_all();
+        shift = raise(mx);
         if (++t < t1) arrive(t);
         // the next tile's scores also where it is rough or there is none (LDS holds some tile):
         // they are dropped then, and the stream of instructions stays one
@@ -933,11 +872,10 @@ void k_tree_attn(AttnArgs a) {
     }
 
     // ------------------------------------------------------------------ the part's result
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) l[rb] = half_sum(l[rb]);
+    l = half_sum(l);
     if constexpr (WK > 1) {  // join the waves that share rows
-      if (half == 0) S.m[wave][col] = m[0];
-      if (half == 0) S.l[wave][col] = l[0];
+      if (half == 0) S.m[wave][col] = m;
+      if (half == 0) S.l[wave][col] = l;
       __syncthreads();
       float mt_all = -INFINITY;
 #pragma unroll
@@ -947,83 +885,81 @@ void k_tree_attn(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < WK; ++i)
         lt += S.l[i * WM + wm][col] * __builtin_amdgcn_exp2f(S.m[i * WM + wm][col] - mu);
-      const float f = __builtin_amdgcn_exp2f(m[0] - mu);
+      const float f = __builtin_amdgcn_exp2f(m - mu);
       f32x4* box = reinterpret_cast<f32x4*>(S.pool);
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           box[((wave * ND + d) * 4 + r) * 64 + lane] =
-              f32x4{acc[0][d][4 * r] * f, acc[0][d][4 * r + 1] * f, acc[0][d][4 * r + 2] * f,
-                    acc[0][d][4 * r + 3] * f};
+              f32x4{acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f,
+                    acc[d][4 * r + 3] * f};
       __syncthreads();
-      m[0] = mt_all;
-      l[0] = lt;
+      m = mt_all;
+      l = lt;
     }
 
     const long long first = pos - r0;  // the group's first piece
     const bool whole = t0 == 0 && t1 == sw.tiles;
     const int slot = 2 * w + (pos == begin ? 0 : 1);
     const int hq = a.c.kv_heads * a.G;
+    const int fcol = fresh(col), fhalf = fresh(half);
+    const int row = mt * MT + wm * 32 + fcol;
+    const int node = row / a.G, g = row - node * a.G;
+    const bool row_live = row < rows;
+    const bool row_out = node < a.N;  // padding nodes get zeros
+    const size_t orow = ((size_t)b * a.N + node) * hq + h * a.G + g;
+    const size_t prow = (size_t)slot * MT + wm * 32 + fcol;
+    const float inv = !row_live || l == 0.0f ? 0.0f : 1.0f / l;
+    char* op = a.out + orow * C::kRow + 4 * fhalf * C::kES;
+    float* pp = a.part + prow * D + 4 * fhalf;
+    // columns d * 32 + 8 r4 + 4 half and up of the row; a dead row's O may hold anything
+    auto emit_out = [&](int d, int r4, f32x4 x) SV_INLINE {
+      if (!row_live) x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (BF16) {
+        bf16x4 y;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int fcol = fresh(col), fhalf = fresh(half);
-      const int row = mt * MT + (wm * RB + rb) * 32 + fcol;
-      const int node = row / a.G, g = row - node * a.G;
-      const bool row_live = row < rows;
-      const bool row_out = node < a.N;  // padding nodes get zeros
-      const size_t orow = ((size_t)b * a.N + node) * hq + h * a.G + g;
-      const size_t prow = (size_t)slot * MT + (wm * RB + rb) * 32 + fcol;
-      const float inv = !row_live || l[rb] == 0.0f ? 0.0f : 1.0f / l[rb];
-      char* op = a.out + orow * C::kRow + 4 * fhalf * C::kES;
-      float* pp = a.part + prow * D + 4 * fhalf;
-      // columns d * 32 + 8 r4 + 4 half and up of the row; a dead row's O may hold anything
-      auto emit_out = [&](int d, int r4, f32x4 x) SV_INLINE {
-        if (!row_live) x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (BF16) {
-          bf16x4 y;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = (__bf16)(x[j] * inv);
-          *reinterpret_cast<bf16x4*>(op + (d * 32 + 8 * r4) * 2) = y;
-        } else {
-          *reinterpret_cast<f32x4*>(op + (d * 32 + 8 * r4) * 4) = x * inv;
-        }
-      };
-      auto emit_part = [&](int d, int r4, f32x4 x) SV_INLINE {
-        *reinterpret_cast<f32x4*>(pp + d * 32 + 8 * r4) = x;
-      };
-      auto each = [&](auto emit) SV_INLINE {
-        if constexpr (WK > 1) {
-          const f32x4* box = reinterpret_cast<const f32x4*>(S.pool);
-          for (int d = wk; d < ND; d += WK)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              f32x4 x = box[((wm * ND + d) * 4 + r) * 64 + lane];
-#pragma unroll
-              for (int i = 1; i < WK; ++i)
-                x += box[(((i * WM + wm) * ND + d) * 4 + r) * 64 + lane];
-              emit(d, r, x);
-            }
-        } else {
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              emit(d, r, f32x4{acc[rb][d][4 * r], acc[rb][d][4 * r + 1], acc[rb][d][4 * r + 2],
-                               acc[rb][d][4 * r + 3]});
-        }
-      };
-      if (whole) {
-        if (row_out) each(emit_out);
-        if (wk == 0 && fhalf == 0 && a.lse && row_out)
-          a.lse[orow] = !row_live || l[rb] == 0.0f ? -INFINITY : m[rb] * kLn2 + logf(l[rb]);
+        for (int j = 0; j < 4; ++j) y[j] = (__bf16)(x[j] * inv);
+        *reinterpret_cast<bf16x4*>(op + (d * 32 + 8 * r4) * 2) = y;
       } else {
-        if (row_live) each(emit_part);
-        if (wk == 0 && fhalf == 0) a.part_ml[prow] = make_float2(m[rb], l[rb]);
+        *reinterpret_cast<f32x4*>(op + (d * 32 + 8 * r4) * 4) = x * inv;
       }
+    };
+    auto emit_part = [&](int d, int r4, f32x4 x) SV_INLINE {
+      *reinterpret_cast<f32x4*>(pp + d * 32 + 8 * r4) = x;
+    };
+    auto each = [&](auto emit) SV_INLINE {
+      if constexpr (WK > 1) {
+        const f32x4* box = reinterpret_cast<const f32x4*>(S.pool);
+        for (int d = wk; d < ND; d += WK)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            f32x4 x = box[((wm * ND + d) * 4 + r) * 64 + lane];
+#pragma unroll
+            for (int i = 1; i < WK; ++i)
+              x += box[(((i * WM + wm) * ND + d) * 4 + r) * 64 + lane];
+            emit(d, r, x);
+          }
+      } else {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            emit(d, r, f32x4{acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2],
+                             acc[d][4 * r + 3]});
+      }
+    };
+    if (whole) {
+      if (row_out) each(emit_out);
+      if (wk == 0 && fhalf == 0 && a.lse && row_out)
+        a.lse[orow] = !row_live || l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    } else {
+      if (row_live) each(emit_part);
+      if (wk == 0 && fhalf == 0) a.part_ml[prow] = make_float2(m, l);
     }
     if (tid == 0 && t0 == 0 && !whole)
-      a.tail[w] = make_int4(b, h * a.mts + mt, slot, (int)(div_pieces(first + group_pieces - 1, per) - w + 1));
+      a.tail[w] = make_int4(b, h * a.mts + mt, slot,
+                            (int)(div_pieces(first + group_pieces - 1, per) - w + 1));
     __syncthreads();
     pos += r1 - r0;
     off += r1 - r0;
@@ -1051,7 +987,9 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const int4 g) {
   float m = -INFINITY, l = 0.0f;
   if (node < n) {
     // parts: slot g.z, then slot 0 of each later worker
-    auto slot_of = [&](int s) SV_INLINE { return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s); };
+    auto slot_of = [&](int s) SV_INLINE {
+      return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s);
+    };
     auto take = [&](int s0, auto count) SV_INLINE {  // so many parts, all their loads in flight
       constexpr int kCount = decltype(count)::value;
       float2 ml[kCount];
@@ -1111,34 +1049,36 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   }
 }
 
-// Tile shapes by row bytes and rows.  Rows of up to 256 bytes: two tiles of 64 keys fit beside
-// another workgroup's; longer ones: one tile, and the other workgroup computes while it loads.
+// Tile shapes: rows of the (sequence, kv head) decide between 32, 64, 128 and 256 (row_tile_for),
+// bytes of a row what fits into LDS.  Rows of up to 256 bytes: two tiles of 64 keys, the next one
+// loaded while one is computed, beside a second workgroup's two; longer ones: one tile, and the
+// other workgroups compute while it is loaded.
 struct Shape {
-  int wm, wk, ks, rb, nst, occ;
+  int wm, wk, ks, nst, occ;
   int per_cu = 0;  // workgroups that a compute unit holds
 };
 
 template <bool BF16, int D>
 constexpr Shape shape_for(int row_tile) {
   constexpr int row = D * (BF16 ? 2 : 4);
-  if (row > 512) return Shape{2, 2, 1, 1, 1, 1};
+  if (row > 512) return Shape{2, 2, 1, 1, 1};
   if (row > 256) {
-    if (row_tile == 32) return Shape{1, 2, 1, 1, 1, 1};
-    if (row_tile == 64) return D > 128 ? Shape{2, 1, 2, 1, 1, 1} : Shape{2, 2, 1, 1, 1, 2};
-    return Shape{4, 1, 2, 1, 1, 2};
+    if (row_tile == 32) return Shape{1, 2, 1, 1, 1};
+    if (row_tile == 64) return D > 128 ? Shape{2, 1, 2, 1, 1} : Shape{2, 2, 1, 1, 2};
+    return Shape{4, 1, 2, 1, 2};
   }
-  if (row_tile == 32) return Shape{1, 2, 1, 1, 2, 2};
-  if (row_tile == 64) return Shape{2, 2, 1, 1, 2, 2};
-  if (row_tile == 128) return Shape{4, 1, 2, 1, 2, 2};
-  return Shape{8, 1, 2, 1, 4, 2};
+  if (row_tile == 32) return Shape{1, 2, 1, 2, 2};
+  if (row_tile == 64) return Shape{2, 2, 1, 2, 2};
+  if (row_tile == 128) return Shape{4, 1, 2, 2, 2};
+  return Shape{8, 1, 2, 4, 2};
 }
 
 template <bool BF16, int D, int RT>
 hipError_t launch_shape(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   constexpr Shape sh = shape_for<BF16, D>(RT);
-  using C = Attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.rb, sh.nst>;
+  using C = Attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.nst>;
   if (p.row_tile != C::kMT || p.key_tile != C::kBN) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_tree_attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.rb, sh.nst, sh.occ>),
+  hipLaunchKernelGGL((k_tree_attn<BF16, D, sh.wm, sh.wk, sh.ks, sh.nst, sh.occ>),
                      dim3(p.workers), dim3(C::kNT), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -1153,7 +1093,8 @@ template <bool BF16, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if constexpr (D * (BF16 ? 2 : 4) > 512) return launch_shape<BF16, D, 64>(a, p, stream);
   else {
-    if (p.row_tile == 32) return launch_shape<BF16, D, 32>(a, p, stream);
+    if constexpr (!BF16 || D == 64 || D == 256)
+      if (p.row_tile == 32) return launch_shape<BF16, D, 32>(a, p, stream);
     if (p.row_tile == 64) return launch_shape<BF16, D, 64>(a, p, stream);
     if constexpr (BF16 && 256 % (D * 2) == 0)
       if (p.row_tile == 256) return launch_shape<BF16, D, 256>(a, p, stream);
@@ -1178,7 +1119,7 @@ template <bool BF16, int D, int RT>
 Shape filled_shape() {
   Shape sh = shape_for<BF16, D>(RT);
   constexpr Shape c = shape_for<BF16, D>(RT);
-  using C = Attn<BF16, D, c.wm, c.wk, c.ks, c.rb, c.nst>;
+  using C = Attn<BF16, D, c.wm, c.wk, c.ks, c.nst>;
   const int by_lds = kLdsBytes / (int)sizeof(typename C::Lds), by_waves = 4 * c.occ / C::kNW;
   sh.per_cu = by_lds < by_waves ? by_lds : by_waves;
   return sh;
@@ -1188,7 +1129,8 @@ template <bool BF16, int D>
 Shape shape_of_dim(int row_tile) {
   if constexpr (D * (BF16 ? 2 : 4) > 512) return filled_shape<BF16, D, 64>();
   else {
-    if (row_tile == 32) return filled_shape<BF16, D, 32>();
+    if constexpr (!BF16 || D == 64 || D == 256)
+      if (row_tile == 32) return filled_shape<BF16, D, 32>();
     if constexpr (BF16 && 256 % (D * 2) == 0)
       if (row_tile == 256) return filled_shape<BF16, D, 256>();
     if constexpr (!BF16 || D <= 128)
@@ -1207,6 +1149,26 @@ Shape shape_of(int D, int row_tile) {
   }
 }
 
+// Rows of a tile.  A tile too small reads the keys again for each further one, a tile too large
+// computes rows that do not exist and leaves larger parts; the smallest that holds all rows, but:
+// - bf16 rows of 192 and 256 bytes take 64 instead of 32: LDS holds two workgroups either way and
+//   four waves load better than two (32 sequences of 4096 tokens, 8 kv heads of 128: 4 rows 112
+//   against 117 us, 32 rows 118 against 121; 64 ragged ones of up to 8191: 232 both).  With 128
+//   bytes LDS holds more workgroups of two waves (ragged, 64 columns: 122 us with 32 rows, 139
+//   with 64), with 512 one tile each (232 and 237), and fp32 products of rows that do not exist
+//   cost 16 times as much (64 columns: 146 and 198).
+// - beyond 128 rows bf16 rows of 128 and 256 bytes take 256 rows a workgroup and the kernel's
+//   pipelined loop (256 rows of 128 columns: 169 us against 188 with tiles of 128; 128 rows: 153
+//   against 133).  Rows of 192 bytes do not spread evenly over eight waves' loads; fp32 is bound
+//   by its products (128 and 64 rows a tile: 178 and 183 us at 128 rows).
+// - bf16 rows of 512 bytes stay at 64: O of a row takes 128 registers, Q 64.
+int row_tile_for(bool bf16, int row_bytes, long long rows) {
+  if (rows <= 32 && !(bf16 && row_bytes > 128 && row_bytes <= 256)) return 32;
+  if (rows <= 64 || (bf16 && row_bytes > 256)) return 64;
+  if (rows <= 128 || !bf16 || 256 % row_bytes) return 128;
+  return 256;
+}
+
 }  // namespace
 
 AttnPlan plan_tree_attention(const CacheView& c, sv_dtype dt, int N, int G) {
@@ -1214,11 +1176,9 @@ AttnPlan plan_tree_attention(const CacheView& c, sv_dtype dt, int N, int G) {
   const bool bf16 = dt == SV_DTYPE_BF16;
   const long long rows = (long long)N * G;
   const int row_bytes = c.head_dim * c.esize;
-  const int want = rows <= 32 ? 32 : rows <= 64 || (bf16 && row_bytes > 256)       ? 64
-                   : rows <= 128 || !bf16 || 256 % row_bytes ? 128
-                                                             : 256;
+  const int want = row_tile_for(bf16, row_bytes, rows);
   const Shape sh = bf16 ? shape_of<true>(c.head_dim, want) : shape_of<false>(c.head_dim, want);
-  p.row_tile = 32 * sh.wm * sh.rb;
+  p.row_tile = 32 * sh.wm;
   p.key_tile = 32 * sh.wk * sh.ks;
   p.mts = (int)((rows + p.row_tile - 1) / p.row_tile);
   // as many workers as the GPU holds at once, and no more than pieces of work the table has room
