@@ -322,8 +322,9 @@ int spec_philox_uniform(uint64_t key0, uint64_t key1, uint64_t counter, int64_t 
  * (spec_verify_tree or spec_verify) and moves the accepted path's rows together
  * (spec_cache_commit).  spec_cache_resize and spec_cache_fork manage the pages.
  *
- * Keys and values do not overlap (calls that write them refuse k == v).  A cache's arrays are
- * changed by one call at a time.
+ * Keys and values share no row (two tensors, or two parts of one: k and v differ by a stride that
+ * clears, or is cleared by, the others; calls that write them refuse what does not).  A cache's
+ * arrays are changed by one call at a time, and not while another call reads them.
  *
  * Rules for device values: a length below 0 counts as 0 and one beyond the table as the table's
  * end; a page outside [0, pages) holds nothing (its keys are seen by no row, writes to it are
@@ -335,7 +336,7 @@ typedef struct {
   void* v;             /*   layer * layer_stride + page * page_stride + slot *             */
                        /*   token_stride + head * head_stride + d; the values likewise     */
   sv_dtype dtype;      /* of keys, values and queries                                      */
-  int32_t layers;      /* >= 1                                                             */
+  int32_t layers;      /* 1..8192                                                          */
   int32_t pages;       /* >= 1                                                             */
   int32_t page_size;   /* tokens a page, >= 1 (any size)                                   */
   int32_t kv_heads;    /* 1..1024                                                          */
@@ -362,7 +363,7 @@ typedef struct {
  *               token is seen by every node
  *   num_nodes   [seqs] or NULL (N each): rows past it get zeros (lse -inf), and nobody sees them
  *   scale       > 0, of the products q.k
- *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype
+ *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype; apart from q
  *   out_lse     [seqs, N, q_heads] float or NULL: natural logarithm of the sum of exponentials
  * A row that sees nothing gives zeros and -inf.  Keys and values that a row does not see do not
  * reach it, whatever they hold (NaN and infinities too).  Sums and softmax statistics are kept
@@ -397,7 +398,7 @@ int spec_cache_append(const void* k_new, const void* v_new, const int64_t* new_s
  *   out_lens   [seqs]: seq_lens + depth of last_node + 1 (the root is committed too).  A
  *              sequence whose last_node is outside [0, N), whose path meets an invalid parent or
  *              whose path lies on a missing page is left alone: its out_lens is seq_lens.
- *              Must not overlap seq_lens (spec_cache_resize stores it there)
+ *              Must overlap neither seq_lens (spec_cache_resize stores it there) nor the inputs
  */
 int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int32_t* parent,
                       int N, int32_t* out_lens, hipStream_t stream);
@@ -411,11 +412,14 @@ int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int
  *             otherwise seq_lens <= want <= table_width * page_size (committed tokens are not
  *             cut)
  *   new_lens  [seqs] or NULL: stored to seq_lens first (0 <= new_lens <= the pages held), as
- *             after spec_cache_commit
+ *             after spec_cache_commit.  Below seq_lens it takes committed tokens back, and is out
+ *             of range where a page that stays and would be written again belongs to another
+ *             sequence too
  *   out_ok    [seqs]: 1, or 0 where a value is out of range or the free pages did not suffice
  *             (sequences are served in order until one does not fit; it and the later ones that
  *             need pages keep what they hold).  A failing sequence's pages are untouched
- * The arrays of one call must not overlap.
+ * The arrays of one call must not overlap, but want (trimming to the committed tokens) and
+ * new_lens may be seq_lens itself.
  */
 int spec_cache_resize(const sv_cache* cache, const int32_t* want, const int32_t* new_lens,
                       int32_t* out_ok, hipStream_t stream);
@@ -429,6 +433,7 @@ int spec_cache_resize(const sv_cache* cache, const int32_t* want, const int32_t*
  *   out_ok    [F]: 1, or 0 where that does not hold, an index or the source's state is out of
  *             range, its begun page is missing, or no page is free (forks are served in order).
  *             A failing fork changes nothing
+ * The arrays of one call must not overlap.
  */
 int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* dst, int F,
                     int32_t* out_ok, hipStream_t stream);

@@ -118,14 +118,21 @@ def commit(k, v, table, lens, last, parent=None, N=None):
 
 
 def resize(table, lens, held, refcount, want, page_size, new_lens=None):
-    """Pages given back, then taken, lowest index first; returns ok."""
+    """Pages given back, then taken, lowest index first; returns ok.  New lengths that cut into
+    pages which stay and are shared are out of range."""
     S, width = table.shape
     ok = np.zeros(S, dtype=np.int32)
     need = np.zeros(S, dtype=np.int64)
+    before = refcount.copy()
     for b in range(S):
         good = 0 <= held[b] <= width
         if good and new_lens is not None:
             good = 0 <= new_lens[b] <= int(held[b]) * page_size
+            old = min(max(int(lens[b]), 0), int(held[b]) * page_size)
+            if good and new_lens[b] < old and want[b] != 0:
+                stay = held[b] if want[b] < 0 else -(-int(want[b]) // page_size)
+                for j in range(new_lens[b] // page_size, min(-(-old // page_size), stay)):
+                    good = good and not (0 <= table[b, j] < len(before) and before[table[b, j]] > 1)
             if good:
                 lens[b] = new_lens[b]
         good = good and (want[b] <= 0 or lens[b] <= want[b] <= width * page_size)

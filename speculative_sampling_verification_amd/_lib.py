@@ -626,9 +626,12 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     lse_at = _arg(out.get("lse"), "out lse", cache, torch.float32, (B, N, H))
     need = cache._attention_workspace(N, H)
     raw = _raw_stream(cache, stream)
-    ws = _workspaces.get((dev.type, cache._index, raw))
-    if ws is None or ws.numel() < need:
-        ws = workspace(dev, need, stream)
+    if torch.cuda.is_current_stream_capturing():  # the graph's own: graphs may run side by side
+        ws = _new((need,), torch.uint8, dev, stream)
+    else:
+        ws = _workspaces.get((dev.type, cache._index, raw))
+        if ws is None or ws.numel() < need:
+            ws = workspace(dev, need, stream)
     _cache_call(cache, "spec_tree_attention", _lib.spec_tree_attention, q.data_ptr(), strides, N,
                 H, cache._ref, layer, mask_at, nodes_at, D ** -0.5 if scale is None else scale,
                 out_at, lse_at, ws.data_ptr(), ws.numel(), raw)

@@ -260,6 +260,20 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
     bool ok = held >= 0 && held <= c.width;
     if (ok && new_lens) {
       ok = nl >= 0 && nl <= (int64_t)held * c.page_size;
+      const int old = min(max(len, 0), held * (int)c.page_div.d);
+      if (ok && nl < old && w != 0) {
+        // cut back into committed tokens: their pages are written again, so no other sequence
+        // may hold them.  (Counts before this call's changes; loads that leave none behind in
+        // the L1, as the changes are made in the L2.)
+        const int kept_to = w < 0 ? old : min(old, min(w, c.cap));
+        const int end = (int)fast_div(c.page_div, (uint32_t)kept_to + c.page_div.d - 1);
+        for (int j = (int)fast_div(c.page_div, (uint32_t)nl); j < end; ++j) {
+          const int page = c.table[(size_t)b * c.width + j];
+          if (page >= 0 && page < c.pages &&
+              __hip_atomic_load(&c.refcount[page], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 1)
+            ok = false;
+        }
+      }
       if (ok) c.lens[b] = len = nl;
     }
     ok = ok && (w <= 0 || (w >= len && w <= c.cap));
@@ -275,11 +289,11 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
 
   // four dropped pages a thread and round, one after the other
   constexpr int kRun = 4;
-  for (int r0 = threadIdx.x * kRun; r0 < dropped; r0 += kPoolThreads * kRun) {
-    int page[kRun], b = owner_of(drop, n, r0);
+  for (uint32_t r0 = threadIdx.x * kRun; r0 < (uint32_t)dropped; r0 += kPoolThreads * kRun) {
+    int page[kRun], b = owner_of(drop, n, (int)r0);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const int r = r0 + i;
+      const int r = (int)r0 + i;
       page[i] = -1;
       if (r < dropped) {
         while (b + 1 < n && drop[b + 1] <= r) ++b;
@@ -292,8 +306,8 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
   }
   int got = 0;
   if (wanted) {
-    // the counts are read by this workgroup alone, and were not read before the atomics (which
-    // act in the L2 behind its loads)
+    // the counts are changed and read by this workgroup alone; the atomics act in the L2, whose
+    // lines none of its loads has brought into the L1 yet
     __threadfence_block();
     __syncthreads();
     got = for_free_pages(s, c, wanted, grow, n, [&](int b, int i, int page) {
@@ -377,8 +391,8 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const i
       out_ok[f] = 0;
     }
   }
-  for (int r = threadIdx.x; r < shared; r += kPoolThreads) {
-    const int f = owner_of(full, F, r), j = r - full[f];
+  for (uint32_t r = threadIdx.x; r < (uint32_t)shared; r += kPoolThreads) {
+    const int f = owner_of(full, F, (int)r), j = (int)r - full[f];
     if (!served(f)) continue;
     const int page = c.table[(size_t)src[f] * c.width + j];
     c.table[(size_t)dst[f] * c.width + j] = page;
@@ -386,20 +400,22 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_fork(CacheView c, const i
   }
 }
 
-// Copies the begun page of every fork: workgroup (layer and k or v, fork).
+// Copies the begun page of every fork: workgroup (layer and k or v, fork, `rows` of the page).
 __global__ __launch_bounds__(kMoveThreads) void k_fork_copy(CacheView c, const int32_t* src,
                                                             const int32_t* dst,
-                                                            const int32_t* ok, FastDiv row_div,
-                                                            FastDiv head_div) {
+                                                            const int32_t* ok, int rows,
+                                                            FastDiv row_div, FastDiv head_div) {
   const int f = blockIdx.y;
   if (ok[f] != 1) return;
   const int x = src[f], y = dst[f], len = c.lens[x];
   const int full = (int)fast_div(c.page_div, (uint32_t)len);
-  const int rest = len - full * c.page_size;
-  if (rest == 0) return;
+  const int row0 = blockIdx.z * rows;
+  const int rest = min(len - full * c.page_size - row0, rows);
+  if (rest <= 0) return;
   const int64_t from = (int64_t)c.table[(size_t)x * c.width + full] * c.page_stride;
   const int64_t to = (int64_t)c.table[(size_t)y * c.width + full] * c.page_stride;
-  char* base = (blockIdx.x & 1 ? c.v : c.k) + (int64_t)(blockIdx.x >> 1) * c.layer_stride;
+  char* base = (blockIdx.x & 1 ? c.v : c.k) + (int64_t)(blockIdx.x >> 1) * c.layer_stride +
+               (int64_t)row0 * c.token_stride;
   const uint32_t all = (uint32_t)rest * row_div.d;
 #pragma unroll 4
   for (uint32_t i = threadIdx.x; i < all; i += kMoveThreads) {
@@ -432,7 +448,8 @@ hipError_t launch_cache_commit(const CacheView& c, const int32_t* parent, const 
   const int64_t cols = parent ? (int64_t)c.layers * 2 * rv : 1;
   const unsigned blocks = (unsigned)((cols + kMoveThreads - 1) / kMoveThreads);
   hipLaunchKernelGGL(k_commit, dim3(blocks, c.seqs), dim3(kMoveThreads),
-                     commit_lds_bytes(N), stream, c, parent, last, N, out_lens, make_fast_div(rv), make_fast_div(hv));
+                     commit_lds_bytes(N), stream, c, parent, last, N, out_lens, make_fast_div(rv),
+                     make_fast_div(hv));
   return hipGetLastError();
 }
 
@@ -449,8 +466,12 @@ hipError_t launch_cache_fork(const CacheView& c, const int32_t* src, const int32
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int hv = head_vecs(c), rv = hv * c.kv_heads;
-  hipLaunchKernelGGL(k_fork_copy, dim3(2 * c.layers, F), dim3(kMoveThreads), 0, stream, c, src,
-                     dst, out_ok, make_fast_div(rv), make_fast_div(hv));
+  // 256 KB a workgroup, more where a page has more than 65535 of them (at most 2^30 vectors)
+  int rows = (256 * 1024 / 16 + rv - 1) / rv;
+  rows = rows > (c.page_size + 65534) / 65535 ? rows : (c.page_size + 65534) / 65535;
+  hipLaunchKernelGGL(k_fork_copy, dim3(2 * c.layers, F, (c.page_size + rows - 1) / rows),
+                     dim3(kMoveThreads), 0, stream, c, src, dst, out_ok, rows, make_fast_div(rv),
+                     make_fast_div(hv));
   return hipGetLastError();
 }
 

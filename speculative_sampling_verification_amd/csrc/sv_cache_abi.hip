@@ -14,19 +14,26 @@ namespace {
 
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxHeadBytes = 1024;
-constexpr int kMaxLayers = 16384;
+constexpr int kMaxLayers = 8192;
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// Whether [a, a + n) and [b, b + m) (bytes) share memory; a null pointer shares none.
+bool overlap(const void* a, uint64_t n, const void* b, uint64_t m) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + m && y < x + n;
+}
 
 // Whether the rows of a dense or strided tensor lie apart: with the dimensions in order of
 // stride, each stride clears everything the smaller ones span.  `row` is the innermost extent.
 // Sizes of one do not move anything, so their strides do not matter.
-bool rows_apart(int64_t row, const int64_t (&stride)[4], const int64_t (&size)[4]) {
+template <int Dims>
+bool rows_apart(int64_t row, const int64_t (&stride)[Dims], const int64_t (&size)[Dims]) {
   int64_t span = row;
-  bool used[4] = {};
-  for (int n = 0; n < 4; ++n) {
+  bool used[Dims] = {};
+  for (int n = 0; n < Dims; ++n) {
     int best = -1;
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < Dims; ++i)
       if (!used[i] && size[i] > 1 && (best < 0 || stride[i] < stride[best])) best = i;
     if (best < 0) return true;
     used[best] = true;
@@ -88,6 +95,17 @@ int view_of(const sv_cache* c, int layer, int count, CacheView* v) {
   return SV_OK;
 }
 
+// Whether no row of the keys is one of the values: of two tensors apart, or two parts of one.
+bool values_apart(const sv_cache* c) {
+  const int64_t k = (int64_t)reinterpret_cast<uintptr_t>(c->k);
+  const int64_t v = (int64_t)reinterpret_cast<uintptr_t>(c->v);
+  const int es = c->dtype == SV_DTYPE_BF16 ? 2 : 4;
+  const int64_t stride[5] = {c->layer_stride, c->page_stride, c->token_stride, c->head_stride,
+                             (k < v ? v - k : k - v) / es};
+  const int64_t size[5] = {c->layers, c->pages, c->page_size, c->kv_heads, 2};
+  return rows_apart(c->head_dim, stride, size);
+}
+
 // Strides (elements) of a [B, N, H, D] tensor, dense where `given` is null; false if a row does
 // not start on 16 bytes.
 bool row_strides(const int64_t* given, int N, int H, int D, int es, int64_t (&s)[3]) {
@@ -143,7 +161,7 @@ int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_he
   a.N = N;
   const AttnPlan p = plan_tree_attention(a.c, cache->dtype, N, a.G);
   if (!workspace || workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned_to(workspace, 16)) return SV_ERR_INVALID_ARG;
+  if (!aligned_to(workspace, 16) || out == q) return SV_ERR_INVALID_ARG;
   a.q = static_cast<const char*>(q);
   a.q_seq = s[0];
   a.q_node = s[1];
@@ -168,7 +186,7 @@ int spec_cache_append(const void* k_new, const void* v_new, const int64_t* new_s
   CacheView v{};
   const int st = view_of(cache, layer, 1, &v);
   if (st != SV_OK) return st;
-  if (v.k == v.v || !k_new || !v_new || N < 1 || N > kCacheMaxNodes) return SV_ERR_INVALID_ARG;
+  if (!values_apart(cache) || !k_new || !v_new || N < 1 || N > kCacheMaxNodes) return SV_ERR_INVALID_ARG;
   if (!aligned_to(k_new, 16) || !aligned_to(v_new, 16) || !aligned_to(num_nodes, 4))
     return SV_ERR_INVALID_ARG;
   int64_t s[3];
@@ -183,14 +201,15 @@ int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int
   CacheView v{};
   const int st = view_of(cache, 0, cache ? cache->layers : 0, &v);
   if (st != SV_OK) return st;
-  if (v.k == v.v || !last_node || !out_lens || N < 1 || N > kCacheMaxNodes) return SV_ERR_INVALID_ARG;
+  if (!values_apart(cache) || !last_node || !out_lens || N < 1 || N > kCacheMaxNodes)
+    return SV_ERR_INVALID_ARG;
   if (!aligned_to(last_node, 4) || !aligned_to(parent, 4) || !aligned_to(out_lens, 4))
     return SV_ERR_INVALID_ARG;
-  // every workgroup of a sequence reads its length while one of them stores the new one
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(out_lens);
-  const uintptr_t in = reinterpret_cast<uintptr_t>(cache->seq_lens);
-  const uintptr_t span = (uintptr_t)v.seqs * sizeof(int32_t);
-  if (lo < in + span && in < lo + span) return SV_ERR_INVALID_ARG;
+  // every workgroup of a sequence reads these while one of them stores the new length
+  const uint64_t row = (uint64_t)v.seqs * sizeof(int32_t);
+  if (overlap(out_lens, row, v.lens, row) || overlap(out_lens, row, last_node, row) ||
+      overlap(out_lens, row, parent, row * N) || overlap(out_lens, row, v.table, row * v.width))
+    return SV_ERR_INVALID_ARG;
   return status_of(launch_cache_commit(v, parent, last_node, N, out_lens, stream));
 }
 
@@ -202,6 +221,16 @@ int spec_cache_resize(const sv_cache* cache, const int32_t* want, const int32_t*
   if (!v.held || !v.refcount || !want || !out_ok) return SV_ERR_INVALID_ARG;
   if (!aligned_to(want, 4) || !aligned_to(new_lens, 4) || !aligned_to(out_ok, 4))
     return SV_ERR_INVALID_ARG;
+  // the cache's arrays and the results are written while the others are read; seq_lens itself may
+  // be given (a thread reads a sequence's values before it stores its length)
+  const uint64_t row = (uint64_t)v.seqs * sizeof(int32_t);
+  const uint64_t counts = (uint64_t)v.pages * sizeof(int32_t);
+  for (const int32_t* x : {want, new_lens, static_cast<const int32_t*>(out_ok)})
+    if ((overlap(x, row, v.lens, row) && (x == out_ok || x != v.lens)) || overlap(x, row, v.held, row) ||
+        overlap(x, row, v.refcount, counts) || overlap(x, row, v.table, row * v.width))
+      return SV_ERR_INVALID_ARG;
+  if (overlap(out_ok, row, want, row) || overlap(out_ok, row, new_lens, row))
+    return SV_ERR_INVALID_ARG;
   return status_of(launch_cache_resize(v, want, new_lens, out_ok, stream));
 }
 
@@ -210,10 +239,19 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* ds
   CacheView v{};
   const int st = view_of(cache, 0, cache ? cache->layers : 0, &v);
   if (st != SV_OK) return st;
-  if (v.k == v.v || !v.held || !v.refcount || F < 0 || F > v.seqs) return SV_ERR_INVALID_ARG;
+  if (!values_apart(cache) || !v.held || !v.refcount || F < 0 || F > v.seqs)
+    return SV_ERR_INVALID_ARG;
   if (F == 0) return SV_OK;
   if (!src || !dst || !out_ok) return SV_ERR_INVALID_ARG;
   if (!aligned_to(src, 4) || !aligned_to(dst, 4) || !aligned_to(out_ok, 4))
+    return SV_ERR_INVALID_ARG;
+  const uint64_t row = (uint64_t)v.seqs * sizeof(int32_t), some = (uint64_t)F * sizeof(int32_t);
+  const uint64_t counts = (uint64_t)v.pages * sizeof(int32_t);
+  for (const int32_t* x : {src, dst, static_cast<const int32_t*>(out_ok)})
+    if (overlap(x, some, v.lens, row) || overlap(x, some, v.held, row) ||
+        overlap(x, some, v.refcount, counts) || overlap(x, some, v.table, row * v.width))
+      return SV_ERR_INVALID_ARG;
+  if (overlap(out_ok, some, src, some) || overlap(out_ok, some, dst, some))
     return SV_ERR_INVALID_ARG;
   return status_of(launch_cache_fork(v, src, dst, F, out_ok, stream));
 }

@@ -124,6 +124,52 @@ def test_move_and_pool_arguments(svl):
     assert L.spec_cache_fork(ctypes.byref(same), DUMMY, DUMMY, 2, DUMMY, None) == INVALID
 
 
+def test_arrays_of_a_call_share_no_memory(svl):
+    L, c = svl.lib(), cache(svl, seq_lens=16 * DUMMY, seq_pages=17 * DUMMY, refcount=18 * DUMMY,
+                            page_table=19 * DUMMY)
+    r, a, b, o = ctypes.byref(c), 24 * DUMMY, 25 * DUMMY, 26 * DUMMY
+    for out in (a, a + 8, a - 8, b, b + 44, 16 * DUMMY + 8, 19 * DUMMY + 56):
+        assert L.spec_cache_commit(r, a, b, 4, out, None) == INVALID, out
+    state = (16 * DUMMY + 8, 17 * DUMMY - 8, 18 * DUMMY + 36, 19 * DUMMY + 56)
+    for x in state:
+        for args in ((x, None, o), (a, x, o), (a, b, x)):
+            assert L.spec_cache_resize(r, *args, None) == INVALID, (x, args)
+        for args in ((x, b, o), (a, x, o), (a, b, x)):
+            assert L.spec_cache_fork(r, args[0], args[1], 3, args[2], None) == INVALID, (x, args)
+    # seq_lens itself may be wanted, not returned to
+    assert L.spec_cache_resize(r, 16 * DUMMY, None, 16 * DUMMY, None) == INVALID
+    for x in (a + 8, b - 8):
+        assert L.spec_cache_resize(r, a, b, x, None) == INVALID
+        assert L.spec_cache_fork(r, a, b, 3, x, None) == INVALID
+    assert attend(svl, c, q=a, out=a, ws=o, ws_bytes=1 << 40) == INVALID
+    assert attend(svl, cache(svl, layers=8193), ws_bytes=1 << 40) == INVALID
+
+
+def test_keys_and_values_share_no_row(svl):
+    L = svl.lib()
+    row, page = 128, 16 * 128  # a token's elements, a page's
+    # k and v as neighbouring halves of a row, a token, a page, a layer: taken (the refusal is
+    # that of the new rows' address)
+    for over in (dict(head_stride=128, token_stride=256, page_stride=2 * page, v=DUMMY + 128),
+                 dict(token_stride=2 * row, page_stride=2 * page, v=DUMMY + 2 * row),
+                 dict(page_stride=2 * page, v=DUMMY + 2 * page),
+                 dict(layer_stride=20 * page, v=DUMMY + 2 * 10 * page)):
+        over.setdefault("layer_stride", 20 * page)
+        for c in (cache(svl, **over), cache(svl, **{**over, "k": over["v"], "v": DUMMY})):
+            assert L.spec_cache_append(DUMMY, DUMMY, None, 0, ctypes.byref(c), 0, None, None) \
+                == INVALID
+            assert L.spec_cache_fork(ctypes.byref(c), None, None, 0, None, None) == 0
+    for v in (DUMMY + 16, DUMMY + 2 * row, DUMMY + 2 * page, DUMMY + 2 * 10 * page,
+              DUMMY + 2 * 20 * page - 16):
+        c = cache(svl, v=v)
+        assert L.spec_cache_append(3 * DUMMY, 4 * DUMMY, None, 4, ctypes.byref(c), 0, None,
+                                   None) == INVALID
+        assert L.spec_cache_commit(ctypes.byref(c), DUMMY, DUMMY, 4, 3 * DUMMY, None) == INVALID
+        assert L.spec_cache_fork(ctypes.byref(c), None, None, 0, None, None) == INVALID
+    assert L.spec_cache_fork(ctypes.byref(cache(svl, v=DUMMY + 2 * 20 * page)), None, None, 0, None,
+                             None) == 0
+
+
 def test_binding_names_bad_tensors(svl):
     k = torch.zeros((2, 6, 4, 2, 64))
     table, lens = torch.zeros((3, 5), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)

@@ -272,6 +272,52 @@ def test_unaligned_counts(svm):
     assert table[0].tolist() == [1, 3, 5, 7, 9] and table[2, :2].tolist() == [13, 15]
 
 
+def test_taking_back_committed_tokens(svm):
+    announce("resize: new lengths below the old ones, in own pages and in shared ones")
+    p = Pool(svm, 5, 8, 6, 40, 8, 1)
+    p.resize(i32(40, 40, 30, 0, 0, 0, 0, 0))
+    p.lens[:3] = 37, 35, 30
+    p.upload()
+    assert p.fork(i32(0, 0, 2), i32(3, 4, 5)).all()
+    # 0: into a page that 3 and 4 hold; 1: its own; 2: into its begun page, its own; 3: to a page's
+    # end, the shared pages behind it given back; 4: the same, but kept
+    ok = p.resize(i32(40, 40, 30, 16, 24, -1, -1, -1), i32(20, 3, 27, 16, 16, 30, 0, 0))
+    assert ok.tolist() == [0, 1, 1, 1, 0, 1, 1, 1]
+    assert p.lens.tolist() == [37, 3, 27, 16, 37, 30, 0, 0]
+    # left alone otherwise, or freed whatever is shared; page 2 of 0 is 4's too, page 4 its own
+    ok = p.resize(i32(-1, 0, -1, 0, 0, 2 ** 31 - 1, -1, -1), i32(33, 3, 5, 1, 2, 3, 0, 0))
+    assert ok.tolist() == [1, 1, 0, 1, 1, 0, 1, 1]
+    # the other holders gone: now 0 may
+    assert p.lens.tolist() == [33, 0, 27, 0, 0, 30, 0, 0]
+    assert p.resize(i32(40, 0, -1, 0, 0, 0, 0, 0), i32(20, 0, 30, 0, 0, 30, 0, 0)).all()
+    assert p.lens.tolist() == [20, 0, 30, 0, 0, 0, 0, 0]
+
+
+def test_seq_lens_as_the_wanted_ones(svm):
+    announce("resize: want is seq_lens itself, with and without new lengths")
+    p = Pool(svm, 7, 4, 6, 20, 8, 1)
+    p.resize(i32(40, 17, 8, 0))
+    p.lens = i32(9, 17, 0, 0)
+    p.upload()
+    want = p.lens.copy()
+    ok = svm.spec_cache_resize(p.cache, p.cache.seq_lens)
+    assert ok.tolist() == O.resize(p.table, p.lens, p.held, p.ref, want, 8).tolist() == [1] * 4
+    p.same()
+    want, new = p.lens.copy(), i32(3, 18, 0, 0)
+    ok = svm.spec_cache_resize(p.cache, p.cache.seq_lens, new_lens=ints(new))
+    assert ok.tolist() == O.resize(p.table, p.lens, p.held, p.ref, want, 8, new).tolist()
+    p.same()
+
+
+def test_fork_of_a_page_for_several_workgroups(svm):
+    announce("fork: a begun page of 3000 rows, copied by many workgroups")
+    p = Pool(svm, 6, 4, 2, 6, 3000, 2, 2, 256, "f32")
+    p.resize(i32(2900, 3001, 0, 0))
+    p.lens[:2] = 2899, 3001
+    p.upload()
+    assert p.fork(i32(0, 1), i32(2, 3)).all()
+
+
 def test_graph_replays(svm):
     announce("a reserve, fork, commit and free sequence captured once and replayed")
     p = Pool(svm, 9, 6, 8, 60, 4, 2)

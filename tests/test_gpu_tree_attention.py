@@ -241,6 +241,33 @@ def test_graph_replays(svm):
         check_attention(got, ref, "bf16", 128)
 
 
+def test_two_graphs_at_once(svm):
+    announce("two graphs captured one after the other, replayed side by side on two streams")
+    cs = [Case(s, "bf16", [20000, 9000, 14000], 8, 2, 4, 128, 16) for s in (42, 43)]
+    caches = [c.cache(svm) for c in cs]
+    qs = [c.dev(c.q) for c in cs]
+    want = [svm.spec_tree_attention(q, k)["out"].clone() for q, k in zip(qs, caches)]
+    outs = [dict(out=torch.empty_like(q)) for q in qs]
+    torch.cuda.synchronize()
+    graphs = []
+    for q, k, out in zip(qs, caches, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(8):
+                svm.spec_tree_attention(q, k, out=out)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for rep in range(5):
+        for out in outs:
+            out["out"].zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out["out"], w), rep
+
+
 def test_two_streams_at_once(svm):
     announce("tree attention on two streams at once, and on a stream= argument")
     cs = [Case(s, "bf16", [3000, 100, 900], 8, 2, 4, 128, 16) for s in (40, 41)]
