@@ -18,6 +18,14 @@
 // single long sequences load every compute unit alike, and the host needs no lengths.  A group
 // that spans several workgroups leaves a part (O, m, l) with each, joined by k_tree_join in
 // workgroup order.
+//
+// What bounds it, by the rows r that share a kv head's keys (8 kv heads of 128 columns, bf16,
+// attention and join): few rows, the bytes of the keys and values: r = 4, 64 ragged sequences of
+// up to 8191 tokens, 1.21 GB in 227 us, 5.3 TB/s.  Many rows, the matrix instructions, at the clock
+// that the power limit leaves them: r = 512, 131072 tokens, 275 GFLOP in 307 us, 895 TFLOP/s,
+// matrix units busy for about two thirds of the cycles and LDS reads free of bank conflicts.
+// Between them (r = 256, 32 ragged sequences of up to 4096 tokens, 69 GFLOP in 124 us) the cut
+// itself counts: 256 groups on 256 workgroups leave 64 MB of parts, written and read again.
 
 #include <hip/hip_runtime.h>
 
@@ -118,8 +126,11 @@ __device__ __forceinline__ bool clear_non_finite(u32x4& x) {
   return any;
 }
 
-// WM waves share the rows (32 each), WK the keys of a tile (KS blocks of 32 each);
-// NST tiles are kept in LDS, loaded there directly from global memory.
+// WM waves share the rows (32 each), WK the keys of a tile (KS blocks of 32 each); NST tiles are
+// kept in LDS, loaded there directly from global memory: no registers hold tiles on their way, so
+// the loads of one or two tiles ahead cost none.  32 rows a wave: with 64, its O and scores take
+// 256 registers, which leaves one wave a SIMD and scores in the accumulation registers, and took
+// 2.5 times as long.
 template <bool BF16, int D, int WM, int WK, int KS, int NST>
 struct Attn {
   static constexpr int kES = BF16 ? 2 : 4;
