@@ -21,11 +21,12 @@
 //
 // What bounds it, by the rows r that share a kv head's keys (8 kv heads of 128 columns, bf16,
 // attention and join): few rows, the bytes of the keys and values: r = 4, 64 ragged sequences of
-// up to 8191 tokens, 1.21 GB in 227 us, 5.3 TB/s.  Many rows, the matrix instructions, at the clock
-// that the power limit leaves them: r = 512, 131072 tokens, 275 GFLOP in 307 us, 895 TFLOP/s,
-// matrix units busy for about two thirds of the cycles and LDS reads free of bank conflicts.
-// Between them (r = 256, 32 ragged sequences of up to 4096 tokens, 69 GFLOP in 124 us) the cut
-// itself counts: 256 groups on 256 workgroups leave 64 MB of parts, written and read again.
+// up to 8191 tokens, 1.21 GB in 227 us, 5.3 TB/s.  Many rows, the products and the exponentials
+// beside them (16 a lane and block of 32 keys take as many cycles as the block's 16 matrix
+// instructions): r = 512, 131072 tokens, 275 GFLOP in 310 us, 890 TFLOP/s, three quarters of what
+// a large library product reaches on the same card; LDS reads have no bank conflicts.  Between
+// them (r = 256, 32 ragged sequences of up to 4096 tokens, 69 GFLOP in 127 us) the cut itself
+// counts: 256 groups on 256 workgroups leave 64 MB of parts, written and read again.
 
 #include <hip/hip_runtime.h>
 
