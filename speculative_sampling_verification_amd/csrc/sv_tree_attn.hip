@@ -980,62 +980,83 @@ void k_tree_attn(AttnArgs a) {
 
 // Joins the parts of each group that begins as some worker's last part and ends with a later
 // worker: every later part is that worker's first.  A workgroup looks after kTails neighbouring
-// workers, one after the other, and 256 pieces of four columns of a row; rows that the batch cannot
-// have are not launched.  Bound by the parts it reads (64 MB in 17 us, 4 TB/s, for 32 ragged trees
+// workers, one after the other, and 256 / W pieces of four columns of a row; W threads share a
+// piece's parts, in order, and the first adds up their sums.  Rows that the batch cannot have are
+// not launched.  Bound by the parts it reads (64 MB in 14 us, 4.6 TB/s, for 32 ragged trees
 // of 256 rows) or, with few rows, by the latency of two dependent loads.  One, two, four and eight
 // workers a workgroup: 18.3, 18.1, 18.5 and 20.2 us for attention and join of 4 sequences of up to
 // 2000 tokens, 226, 227, 228 and 232 us for 64 of up to 8191; with 256 rows a group they are alike.
 constexpr int kTails = 2;
 
-template <bool BF16, int D, int MT>
+template <bool BF16, int D, int MT, int W>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, const int4 g) {
+  constexpr int kPieces = 256 / W;
+  __shared__ f32x4 box[W > 1 ? 256 : 1];
+  __shared__ float2 box_ml[W > 1 ? 256 : 1];
   const int b = g.x, h = g.y / a.mts, mt = g.y - h * a.mts;
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int share = W > 1 ? threadIdx.x / kPieces : 0;
+  const int i = blockIdx.x * kPieces + threadIdx.x % kPieces;
   const int row = i / (D / 4), e = (i - row * (D / 4)) * 4;
   const int r = mt * MT + row;
   const int node = r / a.G, hg = r - node * a.G;
-  if (row >= MT || node >= a.N) return;
-  const int hq = a.c.kv_heads * a.G;
-  const size_t orow = ((size_t)b * a.N + node) * hq + h * a.G + hg;
+  const bool out = row < MT && node < a.N;
   int n = a.nodes ? a.nodes[b] : a.N;
   n = n > a.N ? a.N : n;
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;
-  if (node < n) {
+  // adds kCount parts to (m, l, x), their loads in flight together
+  auto add = [&](auto count, auto load) SV_INLINE {
+    constexpr int kCount = decltype(count)::value;
+    float2 ml[kCount];
+    f32x4 y[kCount];
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) load(k, ml[k], y[k]);
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) top = fmaxf(top, ml[k].x);
+    const float mu = top == -INFINITY ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(m - mu);
+    x *= f;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) {
+      const float p = __builtin_amdgcn_exp2f(ml[k].x - mu);
+      l += ml[k].y * p;
+      x += y[k] * p;
+    }
+    m = top;
+  };
+  if (out && node < n) {
     // parts: slot g.z, then slot 0 of each later worker
-    auto slot_of = [&](int s) SV_INLINE {
-      return s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s);
+    auto take = [&](int s0, auto count) SV_INLINE {
+      add(count, [&](int k, float2& ml, f32x4& y) SV_INLINE {
+        const int s = s0 + k;
+        const size_t slot = s == 0 ? (size_t)g.z : (size_t)2 * (g.z / 2 + s);
+        ml = a.part_ml[slot * MT + row];
+        y = *reinterpret_cast<const f32x4*>(a.part + (slot * MT + row) * D + e);
+      });
     };
-    auto take = [&](int s0, auto count) SV_INLINE {  // so many parts, all their loads in flight
-      constexpr int kCount = decltype(count)::value;
-      float2 ml[kCount];
-      f32x4 y[kCount];
-      float top = m;
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) {
-        const size_t at = slot_of(s0 + i) * MT + row;
-        ml[i] = a.part_ml[at];
-        y[i] = *reinterpret_cast<const f32x4*>(a.part + at * D + e);
-      }
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) top = fmaxf(top, ml[i].x);
-      const float mu = top == -INFINITY ? 0.0f : top;
-      const float f = __builtin_amdgcn_exp2f(m - mu);
-      x *= f;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) {
-        const float p = __builtin_amdgcn_exp2f(ml[i].x - mu);
-        l += ml[i].y * p;
-        x += y[i] * p;
-      }
-      m = top;
-    };
-    int s = 0;
-    for (; s + 8 <= g.w; s += 8) take(s, std::integral_constant<int, 8>{});
-    for (; s + 2 <= g.w; s += 2) take(s, std::integral_constant<int, 2>{});
-    if (s < g.w) take(s, std::integral_constant<int, 1>{});
+    const int each = (g.w + W - 1) / W;
+    int s = share * each;
+    const int end = s + each < g.w ? s + each : g.w;
+    for (; s + 8 <= end; s += 8) take(s, std::integral_constant<int, 8>{});
+    for (; s + 2 <= end; s += 2) take(s, std::integral_constant<int, 2>{});
+    if (s < end) take(s, std::integral_constant<int, 1>{});
   }
+  if constexpr (W > 1) {
+    __syncthreads();  // the group before has been read
+    box[threadIdx.x] = x;
+    box_ml[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
+    if (share > 0) return;
+    add(std::integral_constant<int, W - 1>{}, [&](int k, float2& ml, f32x4& y) SV_INLINE {
+      ml = box_ml[threadIdx.x + (k + 1) * kPieces];
+      y = box[threadIdx.x + (k + 1) * kPieces];
+    });
+  }
+  if (!out) return;
+  const int hq = a.c.kv_heads * a.G;
+  const size_t orow = ((size_t)b * a.N + node) * hq + h * a.G + hg;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if constexpr (BF16) {
     bf16x4 y;
@@ -1048,7 +1069,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, const int4 g) {
   if (a.lse && e == 0) a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-template <bool BF16, int D, int MT>
+template <bool BF16, int D, int MT, int W>
 __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   static_assert(kTails == 2, "two tails in registers");
   int4 g[kTails];
@@ -1060,7 +1081,7 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
   }
 #pragma unroll 1
   for (int i = 0; i < kTails; ++i) {
-    if (g[0].w > 1) join_parts<BF16, D, MT>(a, g[0]);
+    if (g[0].w > 1) join_parts<BF16, D, MT, W>(a, g[0]);
     g[0] = g[1];
   }
 }
@@ -1100,9 +1121,19 @@ hipError_t launch_shape(const AttnArgs& a, const AttnPlan& p, hipStream_t stream
   if (e != hipSuccess) return e;
   if (p.workers == 1) return hipSuccess;
   const int rows = p.mts == 1 ? a.N * a.G : C::kMT;  // of a tile, at most
-  hipLaunchKernelGGL((k_tree_join<BF16, D, C::kMT>),
-                     dim3((rows * (D / 4) + 255) / 256, (p.workers + kTails - 1) / kTails),
-                     dim3(256), 0, stream, a);
+  const unsigned pieces = rows * (D / 4), tails = (p.workers + kTails - 1) / kTails;
+  // Few threads and many parts each: sixteen threads share them (attention and join of 2 sequences
+  // of up to 14304 tokens, one kv head, 5 rows: 15.8 against 31.2 us; of one of 8000, 8 kv heads, 4
+  // rows: 16.8 against 20.7).  With 8192 pieces or more the GPU is full either way, and 16 times
+  // the workgroups cost (8 such sequences: 35.2 against 34.4; one tree of 256 rows: 62 against 38),
+  // and with few parts there is nothing to share (4 each: 14.5 and 14.4).
+  const long long groups = (long long)a.c.seqs * a.c.kv_heads * p.mts;
+  if (p.workers >= 8 * groups && groups * pieces <= 4096)
+    hipLaunchKernelGGL((k_tree_join<BF16, D, C::kMT, 16>), dim3((pieces + 15) / 16, tails),
+                       dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_tree_join<BF16, D, C::kMT, 1>), dim3((pieces + 255) / 256, tails),
+                       dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -241,6 +241,21 @@ def test_graph_replays(svm):
         check_attention(got, ref, "bf16", 128)
 
 
+@pytest.mark.parametrize("dtype,N,Hkv,G,D,lens", [
+    ("bf16", 5, 1, 1, 128, [14304, 9]), ("f32", 25, 1, 4, 64, [12775]), ("bf16", 1, 2, 7, 256, [9000]),
+    ("bf16", 3, 3, 5, 96, [17000]), ("f32", 2, 1, 5, 128, [6001, 0, 4000]), ("f32", 9, 2, 1, 256, [5000])])
+def test_groups_of_many_parts(svm, dtype, N, Hkv, G, D, lens):
+    announce(f"few rows over long contexts, {dtype} N={N} Hkv={Hkv} G={G} D={D} lens={lens}")
+    c = Case(N + D, dtype, lens, N, Hkv, G, D, 24)
+    mask = random_tree(c.rng, len(lens), N)[1]
+    nodes = np.full(len(lens), N, dtype=np.int32)
+    nodes[-1] = N - N // 3
+    got = svm.spec_tree_attention(c.dev(c.q), c.cache(svm), mask=ints(mask), num_nodes=ints(nodes),
+                                  want_lse=True)
+    ref = O.tree_attention(c.q, c.k, c.v, c.table, c.lens, mask, nodes)
+    check_attention(got, ref, dtype, D)
+
+
 def test_two_graphs_at_once(svm):
     announce("two graphs captured one after the other, replayed side by side on two streams")
     cs = [Case(s, "bf16", [20000, 9000, 14000], 8, 2, 4, 128, 16) for s in (42, 43)]
