@@ -1089,7 +1089,11 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
 // Tile shapes: rows of the (sequence, kv head) decide between 32, 64, 128 and 256 (row_tile_for),
 // bytes of a row what fits into LDS.  Rows of up to 256 bytes: two tiles of 64 keys, the next one
 // loaded while one is computed, beside a second workgroup's two; longer ones: one tile, and the
-// other workgroups compute while it is loaded.
+// other workgroups compute while it is loaded.  bf16 rows of 512 bytes: O and Q of 32 rows take 192
+// registers a lane, so four waves and one workgroup a compute unit, with two tiles, for more than
+// 64 rows (32 sequences of up to 4096 tokens, 256 rows: 299 us, 477 with the 64-row workgroups);
+// up to 64 two workgroups of two waves with a tile each (64 sequences of 300 tokens, 48 rows: 58
+// us, 84 with four waves and two tiles; 32 of up to 4096, 64 rows: 151 and 148).
 struct Shape {
   int wm, wk, ks, nst, occ;
   int per_cu = 0;  // workgroups that a compute unit holds
@@ -1101,8 +1105,8 @@ constexpr Shape shape_for(int row_tile) {
   if (row > 512) return Shape{2, 2, 1, 1, 1};
   if (row > 256) {
     if (row_tile == 32) return Shape{1, 2, 1, 1, 1};
-    if (row_tile == 64) return D > 128 ? Shape{2, 1, 2, 1, 1} : Shape{2, 2, 1, 1, 2};
-    return Shape{4, 1, 2, 1, 2};
+    if (row_tile == 64) return BF16 ? Shape{2, 1, 2, 1, 1} : Shape{2, 2, 1, 1, 2};
+    return BF16 ? Shape{4, 1, 2, 2, 1} : Shape{4, 1, 2, 1, 2};
   }
   if (row_tile == 32) return Shape{1, 2, 1, 2, 2};
   if (row_tile == 64) return Shape{2, 2, 1, 2, 2};
@@ -1146,8 +1150,7 @@ hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
     if (p.row_tile == 64) return launch_shape<BF16, D, 64>(a, p, stream);
     if constexpr (BF16 && 256 % (D * 2) == 0)
       if (p.row_tile == 256) return launch_shape<BF16, D, 256>(a, p, stream);
-    if constexpr (!BF16 || D <= 128) return launch_shape<BF16, D, 128>(a, p, stream);
-    return hipErrorInvalidValue;
+    return launch_shape<BF16, D, 128>(a, p, stream);
   }
 }
 
@@ -1181,9 +1184,8 @@ Shape shape_of_dim(int row_tile) {
       if (row_tile == 32) return filled_shape<BF16, D, 32>();
     if constexpr (BF16 && 256 % (D * 2) == 0)
       if (row_tile == 256) return filled_shape<BF16, D, 256>();
-    if constexpr (!BF16 || D <= 128)
-      if (row_tile == 128) return filled_shape<BF16, D, 128>();
-    return filled_shape<BF16, D, 64>();
+    if (row_tile == 64) return filled_shape<BF16, D, 64>();
+    return filled_shape<BF16, D, 128>();
   }
 }
 
@@ -1207,12 +1209,13 @@ Shape shape_of(int D, int row_tile) {
 //   cost 16 times as much (64 columns: 146 and 198).
 // - beyond 128 rows bf16 rows of 128 and 256 bytes take 256 rows a workgroup and the kernel's
 //   pipelined loop (256 rows of 128 columns: 169 us against 188 with tiles of 128; 128 rows: 153
-//   against 133).  Rows of 192 bytes do not spread evenly over eight waves' loads; fp32 is bound
-//   by its products (128 and 64 rows a tile: 178 and 183 us at 128 rows).
-// - bf16 rows of 512 bytes stay at 64: O of a row takes 128 registers, Q 64.
+//   against 133).  Rows of 192 bytes do not spread evenly over eight waves' loads, those of 512
+//   leave no room for the loop's four tiles; fp32 is bound by its products (128 and 64 rows a tile:
+//   178 and 183 us at 128 rows).
+// - rows of 1024 bytes (fp32) stay at 64: O of a row takes 128 registers, Q 128.
 int row_tile_for(bool bf16, int row_bytes, long long rows) {
   if (rows <= 32 && !(bf16 && row_bytes > 128 && row_bytes <= 256)) return 32;
-  if (rows <= 64 || (bf16 && row_bytes > 256)) return 64;
+  if (rows <= 64) return 64;
   if (rows <= 128 || !bf16 || 256 % row_bytes) return 128;
   return 256;
 }
