@@ -56,6 +56,19 @@ def test_row_tiles_and_ragged_nodes(svm, dtype, N, G):
     check(svm, c, None, nodes)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [96, 128, 256])
+@pytest.mark.parametrize("N,G", [(33, 3), (70, 4), (9, 7)])
+def test_row_tiles_of_wide_heads(svm, dtype, D, N, G):
+    announce(f"tree attention {dtype} D={D} N={N} G={G}: several row tiles over longer contexts")
+    c = Case(N + D, dtype, [700, 0, 131, 65, 1023], N, 2, G, D, 16)
+    _, mask = random_tree(c.rng, 5, N)
+    mask[2, N // 2:] = 0
+    nodes = np.array([N, N, N // 2 + 3, 1, N - 1], dtype=np.int32)
+    c.v[c.table[0, 702 // 16], 702 % 16, 1, ::5] = np.inf  # node 2 of sequence 0
+    check(svm, c, mask, nodes)
+
+
 @pytest.mark.parametrize("length", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257])
 def test_lengths_at_tile_edges(svm, length):
     announce(f"tree attention at a tile edge: {length} committed tokens")
