@@ -562,7 +562,11 @@ def _arg(t, name, cache, dtype, shape):
 def _raw_stream(cache, stream):
     """The handle of the stream to launch on.  The lookup behind torch.cuda.current_stream, as
     these calls are short enough for a Stream object to show."""
+    if cache._index is None:
+        raise ValueError(f"the cache is on {cache.device}, expected a GPU")
     if stream is not None:
+        if stream.device != cache.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(cache._index)
 
@@ -667,7 +671,7 @@ def spec_cache_commit(cache, last_node, *, parent=None, num_nodes=None, out=None
     if last_at is None:
         raise TypeError("last_node must be a torch.Tensor")
     if parent is not None:
-        N = parent.shape[-1]
+        N = parent.shape[-1] if isinstance(parent, torch.Tensor) else 0
         parent_at = _arg(parent, "parent", cache, torch.int32, (cache.seqs, N))
     else:
         N = 2048 if num_nodes is None else int(num_nodes)
@@ -697,6 +701,8 @@ def spec_cache_resize(cache, want, *, new_lens=None, out=None, stream=None):
 def spec_cache_fork(cache, src, dst, *, out=None, stream=None):
     """Continues sequences src [F] int32 as the empty sequences dst [F] int32: full pages shared,
     a begun page copied in every layer.  Returns ok [F] int32 (see include/spec_verify.h)."""
+    if not isinstance(src, torch.Tensor):
+        raise TypeError("src must be a torch.Tensor")
     if src.dim() != 1:
         raise ValueError("src must be [F]")
     F = src.shape

@@ -2,6 +2,7 @@
 anything touches a GPU, and the binding names what is wrong with a tensor."""
 
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -200,4 +201,25 @@ def test_binding_names_bad_tensors(svl):
                  lambda: svl.spec_cache_resize(c, i[:2]), lambda: svl.spec_cache_resize(c, 5),
                  lambda: svl.spec_cache_fork(c, i, i[:2]), lambda: svl.spec_cache_fork(c, i[None], i)):
         with pytest.raises((TypeError, ValueError)):
+            call()
+
+
+def test_binding_refuses_other_devices(svl):
+    """Every argument agrees, but the cache is in host memory: nothing may be launched on it."""
+    k = torch.zeros((2, 6, 4, 2, 64))
+    table, i = torch.zeros((3, 5), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    c = svl.PagedCache(k, k.clone(), table, i, seq_pages=i.clone(), refcount=torch.zeros(6, dtype=torch.int32))
+    q, new, x, o = torch.zeros((3, 4, 4, 64)), torch.zeros((3, 4, 2, 64)), i.clone(), i.clone()
+    other = SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    same = SimpleNamespace(cuda_stream=0, device=torch.device("cpu"))
+    for stream in (None, other, same):
+        for call in (lambda: svl.spec_tree_attention(q, c, out={"out": torch.empty_like(q)}, stream=stream),
+                     lambda: svl.spec_cache_append(new, new.clone(), c, stream=stream),
+                     lambda: svl.spec_cache_commit(c, x, num_nodes=4, out=o, stream=stream),
+                     lambda: svl.spec_cache_resize(c, x, out=o, stream=stream),
+                     lambda: svl.spec_cache_fork(c, x, x.clone(), out=o, stream=stream)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (lambda: svl.spec_cache_fork(c, [0], x), lambda: svl.spec_cache_commit(c, x, parent=[0])):
+        with pytest.raises(TypeError):
             call()
