@@ -549,6 +549,14 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(t, stream):
+    """The same with a dense tensor's shape and type (less to parse for torch than those)."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _arg(t, name, cache, dtype, shape):
     """The address of an optional contiguous tensor argument on the cache's device."""
     if t is None:
@@ -623,7 +631,7 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (B,))
     out = dict(out) if out else {}
     if "out" not in out:
-        out["out"] = _new(shape, q.dtype, dev, stream)
+        out["out"] = _new_like(q, stream) if strides is None else _new(shape, q.dtype, dev, stream)
     if want_lse and "lse" not in out:
         out["lse"] = _new((B, N, H), torch.float32, dev, stream)
     out_at = _arg(out["out"], "out out", cache, q.dtype, shape)
@@ -677,7 +685,7 @@ def spec_cache_commit(cache, last_node, *, parent=None, num_nodes=None, out=None
         N = 2048 if num_nodes is None else int(num_nodes)
         parent_at = None
     if out is None:
-        out = _new(seqs, torch.int32, cache.device, stream)
+        out = _new_like(last_node, stream)
     _cache_call(cache, "spec_cache_commit", _lib.spec_cache_commit, cache._ref, last_at,
                 parent_at, N, _arg(out, "out", cache, torch.int32, seqs),
                 _raw_stream(cache, stream))
@@ -692,7 +700,7 @@ def spec_cache_resize(cache, want, *, new_lens=None, out=None, stream=None):
     want_at = _arg(want, "want", cache, torch.int32, seqs)
     lens_at = _arg(new_lens, "new_lens", cache, torch.int32, seqs)
     if out is None:
-        out = _new(seqs, torch.int32, cache.device, stream)
+        out = _new_like(want, stream)
     _cache_call(cache, "spec_cache_resize", _lib.spec_cache_resize, cache._ref, want_at, lens_at,
                 _arg(out, "out", cache, torch.int32, seqs), _raw_stream(cache, stream))
     return out
@@ -709,7 +717,7 @@ def spec_cache_fork(cache, src, dst, *, out=None, stream=None):
     src_at = _arg(src, "src", cache, torch.int32, F)
     dst_at = _arg(dst, "dst", cache, torch.int32, F)
     if out is None:
-        out = _new(F, torch.int32, cache.device, stream)
+        out = _new_like(src, stream)
     _cache_call(cache, "spec_cache_fork", _lib.spec_cache_fork, cache._ref, src_at, dst_at, F[0],
                 _arg(out, "out", cache, torch.int32, F), _raw_stream(cache, stream))
     return out
