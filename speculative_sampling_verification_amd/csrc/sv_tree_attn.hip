@@ -1108,7 +1108,7 @@ constexpr Shape shape_for(int row_tile) {
     if (row_tile == 64) return BF16 ? Shape{2, 1, 2, 1, 1} : Shape{2, 2, 1, 1, 2};
     return BF16 ? Shape{4, 1, 2, 2, 1} : Shape{4, 1, 2, 1, 2};
   }
-  if (row_tile == 32) return Shape{1, 2, 1, 2, 2};
+  if (row_tile == 32) return Shape{1, 2, 1, 2, BF16 ? 2 : 1};
   if (row_tile == 64) return Shape{2, 2, 1, 2, 2};
   if (row_tile == 128) return Shape{4, 1, 2, 2, 2};
   return Shape{8, 1, 2, 4, 2};
