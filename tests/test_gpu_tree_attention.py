@@ -69,6 +69,20 @@ def test_row_tiles_of_wide_heads(svm, dtype, D, N, G):
     check(svm, c, mask, nodes)
 
 
+@pytest.mark.parametrize("dtype,D,N,G", [("bf16", 128, 600, 2), ("bf16", 64, 300, 5), ("f32", 64, 500, 1),
+                                         ("bf16", 256, 300, 1), ("f32", 128, 257, 1), ("bf16", 96, 400, 1)])
+def test_long_chains(svm, dtype, D, N, G):
+    announce(f"pieces of prompts as chains, {dtype} D={D} N={N} G={G}: tiles that some rows see")
+    c = Case(N + D, dtype, [0, 100, 700], N, 1, G, D, 16)
+    nodes = np.array([N, N // 2, N - 1], dtype=np.int32)
+    c.v[c.table[0, 130 // 16], 130 % 16, 0, ::7] = -np.inf   # node 130 of sequence 0
+    c.v[c.table[1, 141 // 16], 141 % 16, 0, 3] = np.nan      # node 41 of sequence 1
+    c.k[c.table[2, 900 // 16], 900 % 16, 0, 5] = np.nan      # node 200 of sequence 2
+    check(svm, c, None, nodes)
+    tril = np.tril(np.ones((N, N), dtype=np.uint8))[None].repeat(3, 0)
+    check(svm, c, tril, nodes)  # the same rows, no tile left out
+
+
 @pytest.mark.parametrize("length", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257])
 def test_lengths_at_tile_edges(svm, length):
     announce(f"tree attention at a tile edge: {length} committed tokens")
