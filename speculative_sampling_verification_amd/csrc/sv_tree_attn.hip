@@ -196,26 +196,39 @@ __device__ __forceinline__ long long uniform(long long x) {
   return (long long)((unsigned long long)hi << 32 | lo);
 }
 
-// 16 bytes a lane from global memory to LDS at `to` (uniform) + 16 * lane, for the lanes of a mask
-// (0 or all: a condition without a branch; every lane is active where this is called).  In
-// assembly because the compiler would wait for it before every LDS read it cannot tell apart; the
-// kernel waits where it has to (tile_barrier).  No register is written.
-__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to,
-                                            unsigned long long lanes) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 exec, %2\n\t"
-               "global_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1"
+// Loads from global memory to LDS at `to` (uniform) + 16 (4) * lane, by the active lanes.  In
+// assembly because the compiler would wait for them before every LDS read it cannot tell apart; the
+// kernel waits where it has to (tile_barrier).  No vector register is written; m0, which holds the
+// LDS address, is declared (it is a reserved register, never kept across a statement, hence the
+// compiler's warning), and needs one wait state before the load.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
-               : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to)), "s"(uniform(lanes))
-               : "memory");
+               : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to))
+               : "memory", "m0");
 }
 
-// The same with 4 bytes a lane.
+// The same by those of the active lanes that are in `lanes` (uniform): a condition without a
+// branch.  The execution mask is put back as it was.
+__device__ __forceinline__ void load_to_lds(const char* from, uint32_t to,
+                                            unsigned long long lanes) {
+  unsigned long long active;
+  asm volatile("s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\t"
+               "global_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, %0"
+               : "=&s"(active)
+               : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to)), "s"(uniform(lanes))
+               : "memory", "m0", "scc");
+}
+
 __device__ __forceinline__ void load_word_to_lds(const int32_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                :
                : "v"(from), "s"(__builtin_amdgcn_readfirstlane(to))
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Waits for this wave's loads to LDS, then for the other waves'.
 __device__ __forceinline__ void tile_barrier() {
@@ -411,13 +424,13 @@ void k_tree_attn(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < C::kLoads; ++i) at_row[i] = S.rowoff[t & (C::kRing - 1)][row_of(i)];
     };
-    auto issue = [&](int t, int i, unsigned long long lanes = ~0ull) SV_INLINE {
+    auto issue = [&](int t, int i, auto... lanes) SV_INLINE {
       const uint32_t to =
           pool_at + (t & (NST - 1)) * C::kTileBytes + wave * 1024 + i * (NT * 16);
       const int r = row_of(i);
       const int p = NT % C::kVecs == 0 ? tid % C::kVecs : tid + i * NT - r * C::kVecs;
-      load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to, lanes);
-      load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow, lanes);
+      load_to_lds(kbase + at_row[i] + (p ^ C::swz_k(r)) * 16, to, lanes...);
+      load_to_lds(vbase + at_row[i] + (p ^ C::swz_v(r)) * 16, to + BN * C::kRow, lanes...);
     };
     // A tile that ends behind the committed tokens or holds keys that do not exist: their values
     // are cleared, and non-finite values of drafted nodes, which may be hidden from some rows
