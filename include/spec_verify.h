@@ -328,7 +328,9 @@ int spec_philox_uniform(uint64_t key0, uint64_t key1, uint64_t counter, int64_t 
  *
  * Rules for device values: a length below 0 counts as 0 and one beyond the table as the table's
  * end; a page outside [0, pages) holds nothing (its keys are seen by no row, writes to it are
- * dropped).  Nothing outside the cache's pages is ever read or written.
+ * dropped, and a path over it is not committed).  Where seq_pages and refcount are given, that
+ * goes for an entry at or past the sequence's seq_pages too if its page's count is not 0: the page
+ * is another sequence's by now.  Nothing outside the cache's pages is ever read or written.
  * ---------------------------------------------------------------------------------------------
  */
 typedef struct {
@@ -347,8 +349,8 @@ typedef struct {
   int32_t table_width; /* entries a sequence; table_width * page_size <= 2^30              */
   int32_t* page_table; /* [seqs, table_width] device                                       */
   int32_t* seq_lens;   /* [seqs] device: committed tokens                                  */
-  int32_t* seq_pages;  /* [seqs] device: entries in use (resize and fork; else NULL)       */
-  int32_t* refcount;   /* [pages] device: sequences that hold the page, 0 = free (likewise) */
+  int32_t* seq_pages;  /* [seqs] device: entries in use; resize and fork need it           */
+  int32_t* refcount;   /* [pages] device: sequences that hold the page, 0 = free; likewise */
 } sv_cache;
 
 /*
@@ -382,7 +384,8 @@ int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_he
  * of one layer.  k_new, v_new [seqs, N, kv_heads, head_dim] of the cache's dtype with element
  * strides new_strides[3] (NULL: dense), 16-byte aligned rows; num_nodes [seqs] or NULL (N each).
  * The pages written are the sequence's own (spec_cache_fork shares full pages below seq_lens
- * only).  seq_lens stays: the nodes are not committed yet.
+ * only; what lies behind the pages held is dropped as said above).  seq_lens stays: the nodes are
+ * not committed yet.
  */
 int spec_cache_append(const void* k_new, const void* v_new, const int64_t* new_strides, int N,
                       const sv_cache* cache, int layer, const int32_t* num_nodes,
@@ -406,8 +409,9 @@ int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int
 /*
  * Makes every sequence hold exactly the pages of want[b] tokens: pages past them are given back
  * (their count falls by one), missing ones are taken from the free pages, lowest index first,
- * and entered in page_table; seq_pages follows.  Entries of page_table from seq_pages on are
- * unspecified.  All pages given back in a call are free for it.
+ * and entered in page_table; seq_pages follows.  Entries of page_table from seq_pages on keep
+ * what they named before, unless the sequence is refused.  All pages given back in a call are
+ * free for it.
  *   want      [seqs]: < 0 leaves the sequence alone; 0 frees it and sets seq_lens to 0;
  *             otherwise seq_lens <= want <= table_width * page_size (committed tokens are not
  *             cut)
@@ -417,7 +421,8 @@ int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int
  *             sequence too
  *   out_ok    [seqs]: 1, or 0 where a value is out of range or the free pages did not suffice
  *             (sequences are served in order until one does not fit; it and the later ones that
- *             need pages keep what they hold).  A failing sequence's pages are untouched
+ *             need pages keep what they hold).  A failing sequence's pages are untouched, and the
+ *             entries that it asked for behind them are cleared to -1: nodes there have no page
  * The arrays of one call must not overlap, but want (trimming to the committed tokens) and
  * new_lens may be seq_lens itself.
  */

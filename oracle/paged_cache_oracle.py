@@ -12,22 +12,32 @@ import numpy as np
 __all__ = ["positions", "tree_attention", "append", "commit", "resize", "fork"]
 
 
-def positions(table_row, page_size, pages, first, last):
-    """[(position, page, slot)] of positions first <= x < last that have a page."""
+def positions(table_row, page_size, pages, first, last, books=None):
+    """[(position, page, slot)] of positions first <= x < last that have a page.  `books`: (entries
+    that the sequence holds, counts of all pages); a page named behind those that somebody holds is
+    another sequence's."""
     cap = len(table_row) * page_size
     out = []
     for x in range(first, min(last, cap)):
         page = int(table_row[x // page_size])
-        if 0 <= page < pages:
-            out.append((x, page, x % page_size))
+        if not 0 <= page < pages:
+            continue
+        if books is not None and x // page_size >= books[0] and books[1][page] != 0:
+            continue
+        out.append((x, page, x % page_size))
     return out
+
+
+def _books(held, refcount, b):
+    return None if held is None or refcount is None else (int(held[b]), refcount)
 
 
 def _length(lens, b, cap):
     return min(max(int(lens[b]), 0), cap)
 
 
-def tree_attention(q, k, v, table, lens, mask=None, nodes=None, scale=None):
+def tree_attention(q, k, v, table, lens, mask=None, nodes=None, scale=None, held=None,
+                   refcount=None):
     """q [B, N, Hq, D], k, v [pages, page_size, Hkv, D] (one layer) in float64.
 
     Returns out [B, N, Hq, D], lse [B, N, Hq] and what error bounds are made of: absolute
@@ -46,9 +56,9 @@ def tree_attention(q, k, v, table, lens, mask=None, nodes=None, scale=None):
     for b in range(B):
         length = _length(lens, b, cap)
         n = N if nodes is None else min(max(int(nodes[b]), 0), N)
-        held = positions(table[b], page_size, pages, 0, length + n)
+        rows = positions(table[b], page_size, pages, 0, length + n, _books(held, refcount, b))
         for i in range(n):
-            seen = [(p, s) for x, p, s in held
+            seen = [(p, s) for x, p, s in rows
                     if x < length or (x - length <= i if mask is None
                                       else mask[b, i, x - length] != 0)]
             count[b, i] = len(seen)
@@ -70,19 +80,20 @@ def tree_attention(q, k, v, table, lens, mask=None, nodes=None, scale=None):
     return dict(out=out, lse=lse, absolute=absolute, reach=reach, count=count)
 
 
-def append(k, v, k_new, v_new, table, lens, nodes=None):
+def append(k, v, k_new, v_new, table, lens, nodes=None, held=None, refcount=None):
     """Writes k_new, v_new [B, N, Hkv, D] behind the committed tokens of one layer's k, v."""
     pages, page_size = k.shape[:2]
     B, N = k_new.shape[:2]
     for b in range(B):
         length = _length(lens, b, table.shape[1] * page_size)
         n = N if nodes is None else min(max(int(nodes[b]), 0), N)
-        for x, page, slot in positions(table[b], page_size, pages, length, length + n):
+        for x, page, slot in positions(table[b], page_size, pages, length, length + n,
+                                       _books(held, refcount, b)):
             k[page, slot] = k_new[b, x - length]
             v[page, slot] = v_new[b, x - length]
 
 
-def commit(k, v, table, lens, last, parent=None, N=None):
+def commit(k, v, table, lens, last, parent=None, N=None, held=None, refcount=None):
     """Moves the accepted path's rows of k, v [layers, pages, page_size, Hkv, D] together;
     returns the new lengths."""
     pages, page_size = k.shape[1:3]
@@ -104,7 +115,8 @@ def commit(k, v, table, lens, last, parent=None, N=None):
             path.insert(0, up)
         if path is None:
             continue
-        where = [positions(table[b], page_size, pages, length + x, length + x + 1)
+        where = [positions(table[b], page_size, pages, length + x, length + x + 1,
+                           _books(held, refcount, b))
                  for x in path + list(range(len(path)))]
         if not all(where):
             continue
@@ -119,7 +131,8 @@ def commit(k, v, table, lens, last, parent=None, N=None):
 
 def resize(table, lens, held, refcount, want, page_size, new_lens=None):
     """Pages given back, then taken, lowest index first; returns ok.  New lengths that cut into
-    pages which stay and are shared are out of range."""
+    pages which stay and are shared are out of range.  The entries that a refused sequence asked
+    for are cleared."""
     S, width = table.shape
     ok = np.zeros(S, dtype=np.int32)
     need = np.zeros(S, dtype=np.int64)
@@ -137,6 +150,8 @@ def resize(table, lens, held, refcount, want, page_size, new_lens=None):
                 lens[b] = new_lens[b]
         good = good and (want[b] <= 0 or lens[b] <= want[b] <= width * page_size)
         ok[b] = good
+        if not good and held[b] >= 0 and want[b] > 0:
+            table[b, held[b]:-(-min(int(want[b]), width * page_size) // page_size)] = -1
         need[b] = held[b] if not good or want[b] < 0 else -(-int(want[b]) // page_size)
         for j in range(need[b], held[b]):
             if 0 <= table[b, j] < len(refcount):
@@ -151,6 +166,7 @@ def resize(table, lens, held, refcount, want, page_size, new_lens=None):
             full = full or grow > len(free)
             if full:
                 ok[b] = 0
+                table[b, held[b]:need[b]] = -1
                 continue
             for j in range(held[b], need[b]):
                 table[b, j] = free.pop(0)

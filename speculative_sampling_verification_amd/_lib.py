@@ -494,7 +494,8 @@ class PagedCache:
                 fp32, any strides with rows on 16 bytes and apart (both tensors alike)
     page_table  [seqs, width] int32
     seq_lens    [seqs] int32, committed tokens
-    seq_pages, refcount   [seqs], [pages] int32: needed by spec_cache_resize and spec_cache_fork
+    seq_pages, refcount   [seqs], [pages] int32: needed by spec_cache_resize and spec_cache_fork;
+                with them the other calls leave alone what another sequence holds by now
     """
 
     def __init__(self, k, v, page_table, seq_lens, *, seq_pages=None, refcount=None):

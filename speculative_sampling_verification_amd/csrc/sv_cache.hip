@@ -23,12 +23,13 @@ constexpr int kMoveThreads = 256;
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWaves = kPoolThreads / 64;
 
-// Byte offset of a position's row in the pages of sequence b; -1 where the table has no page.
-__device__ __forceinline__ int64_t row_offset(const CacheView& c, int b, int pos) {
+// Byte offset of a position's row in the pages of sequence b, which holds `held` of them; -1 where
+// it has no page.
+__device__ __forceinline__ int64_t row_offset(const CacheView& c, int b, int held, int pos) {
   if (pos < 0 || pos >= c.cap) return -1;
   const uint32_t pi = fast_div(c.page_div, (uint32_t)pos);
   const int page = c.table[(size_t)b * c.width + pi];
-  if (page < 0 || page >= c.pages) return -1;
+  if (!names_page(c, held, pos, page)) return -1;
   return (int64_t)page * c.page_stride + (int64_t)(pos - (int)(pi * c.page_div.d)) * c.token_stride;
 }
 
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_append(CacheView c, const char
   const int at = (int)(y - (uint32_t)h * head_div.d) * 16;
   const int n = nodes ? nodes[b] : N;
   if (i >= n || i >= N) return;
-  const int64_t row = row_offset(c, b, clamp_len(c, c.lens[b]) + i);
+  const int64_t row = row_offset(c, b, positions_held(c, b), clamp_len(c, c.lens[b]) + i);
   if (row < 0) return;
   const int64_t from = (int64_t)b * new_seq + (int64_t)i * new_node + (int64_t)h * new_head + at;
   const int64_t to = row + (int64_t)h * c.head_stride + at;
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
   int16_t* walk = reinterpret_cast<int16_t*>(up + N);   // the path from its end
   __shared__ int depth_sh, bad_sh;
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int len = clamp_len(c, c.lens[b]);
+  const int len = clamp_len(c, c.lens[b]), held = positions_held(c, b);
   const int end = last[b];
   bool ok = end >= 0 && end < N;
   if (tid == 0) bad_sh = 0;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
   const int depth = depth_sh;
   for (int d = tid; d <= depth; d += kMoveThreads) {
     const int node = !parent ? d : d == 0 ? 0 : walk[depth - d];
-    const int64_t src = row_offset(c, b, len + node), dst = row_offset(c, b, len + d);
+    const int64_t src = row_offset(c, b, held, len + node), dst = row_offset(c, b, held, len + d);
     if (src < 0 || dst < 0) bad_sh = 1;
     from[d] = src;
     to[d] = dst;
@@ -290,6 +291,12 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
     if (ok && w == 0) c.lens[b] = 0;
     const int need =
         !ok || w < 0 ? held : (int)fast_div(c.page_div, (uint32_t)w + c.page_div.d - 1);
+    // a sequence that is refused reaches no page by the entries it asked for (here those whose
+    // values are out of range, below those that do not fit), whatever they named before
+    if (!ok && held >= 0 && w > 0) {
+      const int asked = (int)fast_div(c.page_div, (uint32_t)min(w, c.cap) + c.page_div.d - 1);
+      for (int j = held; j < asked; ++j) c.table[(size_t)b * c.width + j] = -1;
+    }
     drop[b] = need < held ? held - need : 0;
     grow[b] = need > held ? need - held : 0;
     kept[b] = ok ? min(held, need) : ~0;
@@ -336,6 +343,7 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
       ok = 0;
       for (int r = first; r < got; ++r)
         c.refcount[c.table[(size_t)b * c.width + kept[b] + r - first]] = 0;
+      for (int i = 0; i < g; ++i) c.table[(size_t)b * c.width + kept[b] + i] = -1;
     }
     if (ok) c.held[b] = kept[b] + g;
     out_ok[b] = ok;

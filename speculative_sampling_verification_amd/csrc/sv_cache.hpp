@@ -49,6 +49,21 @@ struct CacheView {
   int32_t* refcount;
 };
 
+// Positions of sequence b in the pages that it holds; all there can be for a cache without books.
+__device__ __forceinline__ int positions_held(const CacheView& c, int b) {
+  if (!c.held || !c.refcount) return INT32_MAX;
+  const int n = c.held[b];
+  return (n < 0 ? 0 : n > c.width ? c.width : n) * c.page_size;
+}
+
+// Whether a page that the table names for position `pos` is its sequence's, which holds `held`
+// positions.  Entries behind those keep what they named before pages were given back, and such a
+// page may have gone to another sequence: its count says so (one load, and only there).
+__device__ __forceinline__ bool names_page(const CacheView& c, int held, int pos, int page) {
+  if (page < 0 || page >= c.pages) return false;
+  return pos < held || c.refcount[page] == 0;
+}
+
 struct AttnArgs {
   CacheView c;
   const char* q;

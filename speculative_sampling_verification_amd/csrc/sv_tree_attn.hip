@@ -367,6 +367,7 @@ void k_tree_attn(AttnArgs a) {
     }
     const int h = (int)((uint32_t)grp / (uint32_t)sw.live), mt = (int)grp - h * sw.live;
     const int rows = sw.n * a.G;             // live rows of the (sequence, kv head)
+    const int held = positions_held(a.c, b);
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     const char* kbase = a.c.k + (long long)h * a.c.head_stride;
     const char* vbase = a.c.v + (long long)h * a.c.head_stride;
@@ -403,8 +404,9 @@ void k_tree_attn(AttnArgs a) {
     auto put_rows = [&](int t, int page, int first = 0) SV_INLINE {
       if (tid >= first && tid < first + BN) {
         const int at = fresh(tid) - first, key = t * BN + at;
-        const bool ok = page >= 0 && page < a.c.pages;
         const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
+        bool ok = page >= 0 && page < a.c.pages;
+        if ((t + 1) * BN > held) ok = names_page(a.c, held, key, page);
         const int slot = key - (int)(pi * a.c.page_div.d);
         S.rowoff[t & (C::kRing - 1)][at] =
             ok ? (long long)page * a.c.page_stride + (long long)slot * a.c.token_stride : 0ll;
