@@ -143,7 +143,10 @@ def resize(table, lens, held, refcount, want, page_size, new_lens=None):
             good = 0 <= new_lens[b] <= int(held[b]) * page_size
             old = min(max(int(lens[b]), 0), int(held[b]) * page_size)
             if good and new_lens[b] < old and want[b] != 0:
-                stay = held[b] if want[b] < 0 else -(-int(want[b]) // page_size)
+                # entries that stay: all of them, unless the wish is one that will be followed
+                stay = held[b]
+                if new_lens[b] <= want[b] <= width * page_size:
+                    stay = -(-int(want[b]) // page_size)
                 for j in range(new_lens[b] // page_size, min(-(-old // page_size), stay)):
                     good = good and not (0 <= table[b, j] < len(before) and before[table[b, j]] > 1)
             if good:

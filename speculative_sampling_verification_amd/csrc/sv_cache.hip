@@ -275,8 +275,9 @@ __global__ __launch_bounds__(kPoolThreads) void k_pool_resize(CacheView c, const
       if (ok && nl < old && w != 0) {
         // cut back into committed tokens: their pages are written again, so no other sequence
         // may hold them.  (Counts before this call's changes; loads that leave none behind in
-        // the L1, as the changes are made in the L2.)
-        const int kept_to = w < 0 ? old : min(old, min(w, c.cap));
+        // the L1, as the changes are made in the L2.)  All pages stay where want is negative, or
+        // out of range and about to be refused.
+        const int kept_to = w < nl || w > c.cap ? old : min(old, w);
         const int end = (int)fast_div(c.page_div, (uint32_t)kept_to + c.page_div.d - 1);
         for (int j = (int)fast_div(c.page_div, (uint32_t)nl); j < end; ++j) {
           const int page = c.table[(size_t)b * c.width + j];

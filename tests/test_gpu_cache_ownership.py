@@ -123,3 +123,51 @@ def test_committed_rows_stay(svm, seed, tight):
         for b in range(S):
             assert (p.ref[p.table[b, p.lens[b] // page:p.held[b]]] == 1).all()
     assert refused > 0 or not tight
+
+
+def test_cut_with_a_refused_want(svm):
+    announce("resize: new lengths that cut into shared pages beside a want that is refused")
+    p = OwnedPool(svm, 5, 6, 6, 40, 8, 1, 1, 64)
+    p.resize(i32(40, 40, 40, 0, 0, 0))
+    p.lens[:3] = 37, 37, 35
+    p.upload()
+    assert p.fork(i32(0, 1), i32(3, 4)).all()
+    before = [p.text(b) for b in range(5)]
+    # 0: want below the new length; 1: want beyond the table; 2: below, but all pages are its own
+    ok = p.resize(i32(5, 49, 5, -1, -1, -1), i32(20, 20, 20, 37, 37, 0))
+    assert ok.tolist() == [0, 0, 0, 1, 1, 1]
+    assert p.lens.tolist() == [37, 37, 20, 37, 37, 0]
+    p.append(6)
+    for b in (0, 1, 3, 4):
+        np.testing.assert_array_equal(p.text(b), before[b])
+    # a cut that gives the shared pages back is taken
+    assert p.resize(i32(24, 24, 20, -1, -1, -1), i32(24, 24, 20, 37, 37, 0)).all()
+    p.append(6)
+    for b in (3, 4):
+        np.testing.assert_array_equal(p.text(b), before[b])
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_cuts_leave_shared_pages_whole(svm, seed):
+    rng = np.random.default_rng(200 + seed)
+    S, width, page = int(rng.integers(3, 16)), int(rng.integers(2, 9)), int(rng.integers(2, 9))
+    announce(f"random cuts and forks, seed={seed} S={S} width={width} page={page}")
+    p = OwnedPool(svm, seed, S, width, S * width, page, 1, 1, 64)
+    for step in range(15):
+        p.resize(rng.integers(-1, width * page + 2, S).astype(np.int32))
+        p.lens = np.where(p.lens == 0, rng.integers(0, page * width + 1, S), p.lens)
+        p.lens = np.minimum(p.lens, p.held * page).astype(np.int32)
+        p.upload()
+        src, dst = (rng.integers(0, S, S).astype(np.int32) for _ in range(2))
+        p.fork(src, dst)
+        for b in range(S):
+            assert (p.ref[p.table[b, p.lens[b] // page:p.held[b]]] == 1).all()
+        before = [p.text(b) for b in range(S)]
+        new = rng.integers(0, p.lens + 2).astype(np.int32)
+        p.resize(rng.integers(-1, width * page + 2, S).astype(np.int32), new)
+        for b in range(S):
+            assert (p.ref[p.table[b, p.lens[b] // page:p.held[b]]] == 1).all(), (step, b)
+        p.append(int(rng.integers(1, 2 * page)))
+        for b in range(S):
+            n = min(int(p.lens[b]), before[b].shape[2])
+            np.testing.assert_array_equal(p.text(b, 0, n), before[b][:, :, :n])
