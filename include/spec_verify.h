@@ -365,8 +365,10 @@ typedef struct {
  *               token is seen by every node
  *   num_nodes   [seqs] or NULL (N each): rows past it get zeros (lse -inf), and nobody sees them
  *   scale       > 0, of the products q.k
- *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype; apart from q
+ *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype
  *   out_lse     [seqs, N, q_heads] float or NULL: natural logarithm of the sum of exponentials
+ * out, out_lse and the workspace share no memory with each other, with q, with the layer's keys and
+ * values or with any other array of the call.
  * A row that sees nothing gives zeros and -inf.  Keys and values that a row does not see do not
  * reach it, whatever they hold (NaN and infinities too).  Sums and softmax statistics are kept
  * in fp32; with bf16 the weights are rounded to bf16 for the product with the values.
@@ -382,7 +384,8 @@ int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_he
 /*
  * Writes the keys and values of each sequence's nodes to positions seq_lens + 0 .. num_nodes - 1
  * of one layer.  k_new, v_new [seqs, N, kv_heads, head_dim] of the cache's dtype with element
- * strides new_strides[3] (NULL: dense), 16-byte aligned rows; num_nodes [seqs] or NULL (N each).
+ * strides new_strides[3] (NULL: dense), 16-byte aligned rows, none of them a row that the call
+ * writes; num_nodes [seqs] or NULL (N each).
  * The pages written are the sequence's own (spec_cache_fork shares full pages below seq_lens
  * only; what lies behind the pages held is dropped as said above).  seq_lens stays: the nodes are
  * not committed yet.
@@ -401,7 +404,7 @@ int spec_cache_append(const void* k_new, const void* v_new, const int64_t* new_s
  *   out_lens   [seqs]: seq_lens + depth of last_node + 1 (the root is committed too).  A
  *              sequence whose last_node is outside [0, N), whose path meets an invalid parent or
  *              whose path lies on a missing page is left alone: its out_lens is seq_lens.
- *              Must overlap neither seq_lens (spec_cache_resize stores it there) nor the inputs
+ *              Must overlap neither the cache's arrays (spec_cache_resize stores it) nor the inputs
  */
 int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int32_t* parent,
                       int N, int32_t* out_lens, hipStream_t stream);

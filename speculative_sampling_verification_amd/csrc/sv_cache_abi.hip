@@ -122,6 +122,35 @@ bool row_strides(const int64_t* given, int N, int H, int D, int es, int64_t (&s)
   return true;
 }
 
+// Bytes from a tensor's first element to behind its last (strides in bytes), false where no address
+// space holds them.
+template <int Dims>
+bool extent_of(int64_t row, const int64_t (&stride)[Dims], const int64_t (&size)[Dims],
+               uint64_t* bytes) {
+  int64_t span = row, step;
+  for (int i = 0; i < Dims; ++i)
+    if (__builtin_mul_overflow(stride[i], size[i] - 1, &step) ||
+        __builtin_add_overflow(span, step, &span))
+      return false;
+  *bytes = (uint64_t)span;
+  return true;
+}
+
+struct Range {
+  const void* at;  // null: an array that is not given
+  uint64_t bytes;
+};
+
+// Whether what an attention call writes (the first `outs` of the ranges) shares memory with
+// anything else that it reads or writes.
+template <int Count>
+bool outputs_apart(const Range (&r)[Count], int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < Count; ++j)
+      if (overlap(r[i].at, r[i].bytes, r[j].at, r[j].bytes)) return false;
+  return true;
+}
+
 bool attn_shape(const sv_cache* c, int N, int q_heads) {
   if (N < 1 || N > kCacheMaxNodes) return false;
   if (q_heads < 1 || q_heads > 64 * kMaxHeads || q_heads % c->kv_heads != 0) return false;
@@ -161,7 +190,25 @@ int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_he
   a.N = N;
   const AttnPlan p = plan_tree_attention(a.c, cache->dtype, N, a.G);
   if (!workspace || workspace_bytes < p.bytes) return SV_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned_to(workspace, 16) || out == q) return SV_ERR_INVALID_ARG;
+  if (!aligned_to(workspace, 16)) return SV_ERR_INVALID_ARG;
+  // workgroups write while others still read
+  const CacheView& v = a.c;
+  const int64_t row = (int64_t)v.head_dim * v.esize;
+  const int64_t cache_stride[3] = {v.page_stride, v.token_stride, v.head_stride};
+  const int64_t cache_size[3] = {v.pages, v.page_size, v.kv_heads};
+  const int64_t q_size[3] = {v.seqs, N, q_heads};
+  uint64_t layer_bytes, q_bytes;
+  if (!extent_of(row, cache_stride, cache_size, &layer_bytes) ||
+      !extent_of(row, s, q_size, &q_bytes))
+    return SV_ERR_INVALID_ARG;
+  const uint64_t rows = (uint64_t)v.seqs * N * q_heads, word = sizeof(int32_t);
+  const Range ranges[] = {{out, rows * row}, {out_lse, rows * sizeof(float)},
+                          {workspace, p.bytes}, {q, q_bytes},
+                          {v.k, layer_bytes}, {v.v, layer_bytes},
+                          {mask, (uint64_t)v.seqs * N * N}, {num_nodes, word * v.seqs},
+                          {v.table, word * v.seqs * v.width}, {v.lens, word * v.seqs},
+                          {v.held, word * v.seqs}, {v.refcount, word * v.pages}};
+  if (!outputs_apart(ranges, 3)) return SV_ERR_INVALID_ARG;
   a.q = static_cast<const char*>(q);
   a.q_seq = s[0];
   a.q_node = s[1];
@@ -208,7 +255,9 @@ int spec_cache_commit(const sv_cache* cache, const int32_t* last_node, const int
   // every workgroup of a sequence reads these while one of them stores the new length
   const uint64_t row = (uint64_t)v.seqs * sizeof(int32_t);
   if (overlap(out_lens, row, v.lens, row) || overlap(out_lens, row, last_node, row) ||
-      overlap(out_lens, row, parent, row * N) || overlap(out_lens, row, v.table, row * v.width))
+      overlap(out_lens, row, parent, row * N) || overlap(out_lens, row, v.table, row * v.width) ||
+      overlap(out_lens, row, v.held, row) ||
+      overlap(out_lens, row, v.refcount, (uint64_t)v.pages * sizeof(int32_t)))
     return SV_ERR_INVALID_ARG;
   return status_of(launch_cache_commit(v, parent, last_node, N, out_lens, stream));
 }
