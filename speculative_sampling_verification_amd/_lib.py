@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch  # loaded first so that the library binds to torch's HIP runtime
 
@@ -139,9 +140,16 @@ class SpecVerifyError(RuntimeError):
         self.code = code
 
 
-def _check(fn, code):
+# Held while a call enqueues its kernels: several of them share a workspace (one per stream), and
+# another thread's kernels on the same stream must not come between.
+_launches = threading.RLock()
+
+
+def _launch(name, fn, *args):
+    with _launches:
+        code = fn(*args)
     if code != SV_OK:
-        raise SpecVerifyError(fn, code)
+        raise SpecVerifyError(name, code)
 
 
 def _dtype_code(t):
@@ -184,13 +192,14 @@ def workspace(device, nbytes, stream=None):
     never freed, so work already captured in a HIP graph keeps valid memory."""
     s = stream if stream is not None else torch.cuda.current_stream(device)
     key = (device.type, device.index, s.cuda_stream)
-    buf = _workspaces.get(key)
-    if buf is None or buf.numel() < nbytes:
-        if buf is not None:
-            _outgrown.append(buf)
-        with torch.cuda.stream(s):  # memory whose earlier users are ordered before the work on s
-            buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-        _workspaces[key] = buf
+    with _launches:
+        buf = _workspaces.get(key)
+        if buf is None or buf.numel() < nbytes:
+            if buf is not None:
+                _outgrown.append(buf)
+            with torch.cuda.stream(s):  # memory whose earlier users are ordered before s's work
+                buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+            _workspaces[key] = buf
     return buf
 
 
@@ -199,6 +208,11 @@ def release_workspaces(device=None):
     captured graphs, after the device has finished the work queued on them.  A HIP graph
     captured over calls of this binding must not be replayed afterwards; the next call
     allocates afresh.  Returns the number of bytes released."""
+    with _launches:
+        return _release(device)
+
+
+def _release(device):
     freed = 0
     devs = {d for (_, d, _) in _workspaces} | {b.device.index for b in _outgrown}
     for d in devs:
@@ -295,17 +309,16 @@ def spec_verify(target_logits, draft_logits, draft_tokens, uniforms, *, temperat
         if draft_rows != K:
             raise ValueError("presampled needs draft_logits [B, K, V]")
         _need(presampled, "presampled", dev, torch.uint8)
-        _check("spec_verify_presampled", _lib.spec_verify_presampled(
-            args[0], args[1], dt, B, K, V, *args[7:15], _ptr(presampled), presampled.numel(),
-            *args[15:]))
+        _launch("spec_verify_presampled", _lib.spec_verify_presampled, args[0], args[1], dt, B, K,
+                V, *args[7:15], _ptr(presampled), presampled.numel(), *args[15:])
     elif want_rates:
-        _check("spec_verify_rates", _lib.spec_verify_rates(*args[:15], _ptr(out["rate"]),
-                                                           *args[15:]))
+        _launch("spec_verify_rates", _lib.spec_verify_rates, *args[:15], _ptr(out["rate"]),
+                *args[15:])
     elif events is None:
-        _check("spec_verify", _lib.spec_verify(*args))
+        _launch("spec_verify", _lib.spec_verify, *args)
     else:
         arr = (ctypes.c_void_p * len(events))(*events)
-        _check("spec_verify_profiled", _lib.spec_verify_profiled(*args, arr, len(events)))
+        _launch("spec_verify_profiled", _lib.spec_verify_profiled, *args, arr, len(events))
     return out
 
 
@@ -337,11 +350,11 @@ def spec_verify_noalloc(target_logits, draft_logits, draft_tokens, uniforms, out
         if k in out:
             _need(out[k], f"out {k}", dev, torch.float32, (B, K))
     samp = sampling(temperature, top_k, top_p, lenience, mentor_kl)
-    _check("spec_verify_noalloc", _lib.spec_verify_noalloc(
-        _ptr(target_logits), _ptr(draft_logits) if K > 0 else None, dt, B, K, V, draft_rows,
-        _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms), ctypes.byref(samp),
-        _ptr(out["tokens"]), _ptr(out["num_accepted"]), _ptr(out.get("accept_prob")),
-        _ptr(out.get("q_draft")), _ptr(out.get("p_draft")), _stream(dev, stream)))
+    _launch("spec_verify_noalloc", _lib.spec_verify_noalloc, _ptr(target_logits),
+            _ptr(draft_logits) if K > 0 else None, dt, B, K, V, draft_rows,
+            _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms), ctypes.byref(samp),
+            _ptr(out["tokens"]), _ptr(out["num_accepted"]), _ptr(out.get("accept_prob")),
+            _ptr(out.get("q_draft")), _ptr(out.get("p_draft")), _stream(dev, stream))
     return out
 
 
@@ -379,9 +392,8 @@ def spec_sample(logits, uniforms, *, temperature=1.0, top_k=0, top_p=1.0, out=No
         ws = summary
     else:
         ws = workspace(dev, need, stream)
-    _check("spec_sample", _lib.spec_sample(_ptr(logits), dt, R, V, _ptr(uniforms),
-                                           ctypes.byref(samp), _ptr(out), _ptr(ws), ws.numel(),
-                                           _stream(dev, stream)))
+    _launch("spec_sample", _lib.spec_sample, _ptr(logits), dt, R, V, _ptr(uniforms),
+            ctypes.byref(samp), _ptr(out), _ptr(ws), ws.numel(), _stream(dev, stream))
     return out
 
 
@@ -412,11 +424,11 @@ def spec_verify_tree(target_logits, parent, node_tokens, max_depth, *, out=None,
             _ptr(out["tokens"]), _ptr(out["num_accepted"]), _ptr(out["last_node"]), _ptr(ws),
             ws.numel(), _stream(dev, stream))
     if events is None:
-        _check("spec_verify_tree", _lib.spec_verify_tree(*args))
+        _launch("spec_verify_tree", _lib.spec_verify_tree, *args)
     else:
         arr = (ctypes.c_void_p * len(events))(*events)
-        _check("spec_verify_tree_profiled",
-               _lib.spec_verify_tree_profiled(*args, arr, len(events)))
+        _launch("spec_verify_tree_profiled", _lib.spec_verify_tree_profiled, *args, arr,
+                len(events))
     return out
 
 
@@ -438,10 +450,9 @@ def spec_build_tree(candidates, N, *, want_mask=True, out=None, stream=None):
     if want_mask:
         out.setdefault("mask", torch.empty((B, N, N), dtype=torch.uint8, device=dev))
         _need(out["mask"], "out mask", dev, torch.uint8, (B, N, N))
-    _check("spec_build_tree", _lib.spec_build_tree(
-        _ptr(candidates), B, M, L, int(N), _ptr(out["parent"]), _ptr(out["tokens"]),
-        _ptr(out["num_nodes"]), _ptr(out["depth"]), _ptr(out["weight"]), _ptr(out.get("mask")),
-        _stream(dev, stream)))
+    _launch("spec_build_tree", _lib.spec_build_tree, _ptr(candidates), B, M, L, int(N),
+            _ptr(out["parent"]), _ptr(out["tokens"]), _ptr(out["num_nodes"]), _ptr(out["depth"]),
+            _ptr(out["weight"]), _ptr(out.get("mask")), _stream(dev, stream))
     return out
 
 
@@ -455,9 +466,8 @@ def spec_philox_uniform(key, counter, n, *, device=None, out=None, stream=None):
     if out.numel() < n:
         raise ValueError("out is too small")
     k0, k1 = (int(k) & (2**64 - 1) for k in key)
-    _check("spec_philox_uniform", _lib.spec_philox_uniform(
-        k0, k1, int(counter) & (2**64 - 1), int(n), _ptr(out) if n else None,
-        _stream(dev, stream)))
+    _launch("spec_philox_uniform", _lib.spec_philox_uniform, k0, k1, int(counter) & (2**64 - 1),
+            int(n), _ptr(out) if n else None, _stream(dev, stream))
     return out
 
 
@@ -480,9 +490,9 @@ def spec_acceptance_rate(target_logits, draft_logits, *, temperature=1.0, top_k=
     if need == 0:
         raise SpecVerifyError("spec_verify_workspace_size", 1)
     ws = workspace(dev, need, stream)
-    _check("spec_acceptance_rate", _lib.spec_acceptance_rate(
-        _ptr(target_logits), _ptr(draft_logits), dt, B, K, V, draft_logits.shape[1],
-        ctypes.byref(samp), _ptr(out), _ptr(ws), ws.numel(), _stream(dev, stream)))
+    _launch("spec_acceptance_rate", _lib.spec_acceptance_rate, _ptr(target_logits),
+            _ptr(draft_logits), dt, B, K, V, draft_logits.shape[1], ctypes.byref(samp), _ptr(out),
+            _ptr(ws), ws.numel(), _stream(dev, stream))
     return out
 
 
@@ -583,12 +593,10 @@ def _raw_stream(cache, stream):
 def _cache_call(cache, name, fn, *args):
     """Calls fn with the cache's device current (a null stream is that device's)."""
     if torch._C._cuda_getDevice() == cache._index:
-        code = fn(*args)
+        _launch(name, fn, *args)
     else:
         with torch.cuda.device(cache._index):
-            code = fn(*args)
-    if code != SV_OK:
-        raise SpecVerifyError(name, code)
+            _launch(name, fn, *args)
 
 
 def _row_strides(t, name, cache, heads):
