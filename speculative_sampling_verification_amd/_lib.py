@@ -590,6 +590,16 @@ def _raw_stream(cache, stream):
     return torch._C._cuda_getCurrentRawStream(cache._index)
 
 
+def _capturing(cache, stream):
+    """Whether the stream to launch on is being captured into a graph."""
+    if stream is None:
+        if torch._C._cuda_getDevice() == cache._index:
+            return torch.cuda.is_current_stream_capturing()
+        stream = torch.cuda.current_stream(cache.device)
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _cache_call(cache, name, fn, *args):
     """Calls fn with the cache's device current (a null stream is that device's)."""
     if torch._C._cuda_getDevice() == cache._index:
@@ -647,7 +657,7 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     lse_at = _arg(out.get("lse"), "out lse", cache, torch.float32, (B, N, H))
     need = cache._attention_workspace(N, H)
     raw = _raw_stream(cache, stream)
-    if torch.cuda.is_current_stream_capturing():  # the graph's own: graphs may run side by side
+    if _capturing(cache, stream):  # the graph's own: graphs may run side by side
         ws = _new((need,), torch.uint8, dev, stream)
     else:
         ws = _workspaces.get((dev.type, cache._index, raw))
