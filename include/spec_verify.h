@@ -364,7 +364,7 @@ typedef struct {
  *               spec_build_tree's out_mask says; NULL: a chain, i sees j <= i.  Every committed
  *               token is seen by every node
  *   num_nodes   [seqs] or NULL (N each): rows past it get zeros (lse -inf), and nobody sees them
- *   scale       > 0, of the products q.k
+ *   scale       > 0, of the products q.k; scale * log2(e) is finite in fp32
  *   out         [seqs, N, q_heads, head_dim] dense, of the cache's dtype
  *   out_lse     [seqs, N, q_heads] float or NULL: natural logarithm of the sum of exponentials
  * out, out_lse and the workspace share no memory with each other, with q, with the layer's keys and

@@ -179,7 +179,8 @@ int spec_tree_attention(const void* q, const int64_t* q_strides, int N, int q_he
   const int st = view_of(cache, layer, 1, &a.c);
   if (st != SV_OK) return st;
   if (!q || !out || !attn_shape(cache, N, q_heads)) return SV_ERR_INVALID_ARG;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+  // the kernel multiplies scores by scale * log2(e)
+  if (!(scale > 0.0f) || !std::isfinite(scale * 1.44269504088896340736f)) return SV_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(out_lse, 4) ||
       !aligned_to(num_nodes, 4))
     return SV_ERR_INVALID_ARG;

@@ -1,5 +1,5 @@
 """CPU-side refusals of calls whose buffers share memory: what attention writes lies apart from all
-that it reads, and a commit's lengths apart from the cache's books."""
+that it reads, and a commit's lengths apart from the cache's books.  And of scales too large."""
 
 import ctypes
 
@@ -29,14 +29,14 @@ def cache(svl, at):
                        at["ref"])
 
 
-def attend(svl, layer=0, strides=None, heads=HEADS, ws_bytes=None, **moved):
+def attend(svl, layer=0, strides=None, heads=HEADS, ws_bytes=None, scale=0.125, **moved):
     at = {**AT, **moved}
     c = cache(svl, at)
     need = svl.lib().spec_tree_attention_workspace_size(ctypes.byref(c), N, heads)
     assert need > 0
     s = None if strides is None else (ctypes.c_int64 * 3)(*strides)
     return svl.lib().spec_tree_attention(at["q"], s, N, heads, ctypes.byref(c), layer, at["mask"],
-                                         at["nodes"], 0.125, at["out"], at["lse"], at["ws"],
+                                         at["nodes"], scale, at["out"], at["lse"], at["ws"],
                                          need if ws_bytes is None else ws_bytes, None), need
 
 
@@ -78,3 +78,11 @@ def test_committed_lengths_apart_from_the_books(svl):
         for off in (0, SIZE[name] - 4, 4 - 4 * SEQS):
             assert svl.lib().spec_cache_commit(ctypes.byref(c), AT["q"], AT["mask"], N,
                                                AT[name] + off, None) == INVALID, (name, off)
+
+
+def test_scales_whose_multiple_overflows(svl):
+    # scores are multiplied by scale * log2(e) = 1.4427 scale: 3.4028e38 / 1.4427 = 2.3587e38
+    for scale in (2.36e38, 3.4e38):
+        assert attend(svl, scale=scale, ws_bytes=0)[0] == INVALID
+    for scale in (2.358e38, 1e-38):
+        assert attend(svl, scale=scale, ws_bytes=0)[0] == WS
