@@ -498,7 +498,7 @@ def spec_acceptance_rate(target_logits, draft_logits, *, temperature=1.0, top_k=
 
 class PagedCache:
     """A paged key/value cache (sv_cache of include/spec_verify.h): the caller's tensors, checked
-    once and kept.
+    once and kept (their contents change, the tensors do not).
 
     k, v        [layers, pages, page_size, kv_heads, head_dim], or without the layers; bf16 or
                 fp32, any strides with rows on 16 bytes and apart (both tensors alike)
@@ -541,6 +541,13 @@ class PagedCache:
         self._ref = ctypes.byref(self._c)
         self._index = dev.index
         self._workspace_bytes = {}
+
+    def __setattr__(self, name, value):
+        # the addresses are taken once: another tensor in an attribute's place would be ignored
+        if self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} is fixed: change the tensor in place, or make another "
+                                 "PagedCache")
+        object.__setattr__(self, name, value)
 
     def _attention_workspace(self, N, q_heads):
         need = self._workspace_bytes.get((N, q_heads))
