@@ -154,6 +154,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
 struct PoolScan {
   int2 wave[2][kPoolWaves];
 };
+static_assert(3 * sizeof(int) * kCacheMaxSeqs + sizeof(PoolScan) <= 160 * 1024,
+              "both pool kernels keep three words a sequence in a compute unit's LDS");
 
 // Exclusive prefix of a pair a thread over the workgroup; totals in *all.  `side` alternates
 // between calls: one barrier each.

@@ -11,13 +11,14 @@
 
 namespace sv {
 
-constexpr int kCacheMaxSeqs = 8192;          // sequences of a cache (the page pool keeps two
+constexpr int kCacheMaxSeqs = 8192;          // sequences of a cache (the page pool keeps three
                                              // words of each in LDS)
 constexpr int kCacheMaxNodes = 2048;         // nodes per sequence (as spec_verify_tree)
 constexpr int kCacheMaxTokens = 1 << 30;     // table_width * page_size
 constexpr int kAttnCus = 256;                // compute units of a gfx950 GPU
 
-// t / d for 0 <= t < 2^31 by a multiplication (d >= 1): with s = ceil(log2 d) and
+// t / d for 0 <= t < 2^31 by a multiplication (d >= 1), after Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication" (1994): with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, t / d = (hi32(m t) + t) >> s; the sum stays below 2^32.
 struct FastDiv {
   uint32_t d, m, s;
