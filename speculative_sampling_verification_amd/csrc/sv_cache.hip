@@ -72,7 +72,7 @@ size_t commit_lds_bytes(int N) { return (size_t)N * (2 * sizeof(int64_t) + 4 + 2
 // them for every depth, eight rows in flight; no other thread touches them.  Every workgroup
 // finds the path anew in LDS (a few loads of LDS one after the other), which is less than another
 // launch.  Bound by latency: 32 trees of 64 nodes, paths of 6, in 32 layers of 8 kv heads of 128
-// bf16 (28 MB) take 6.6 us; one tree of 16 nodes in 12 layers 3.5 us.
+// bf16 (28 MB) take 6.8 us; one tree of 16 nodes in 12 layers 3.6 us.
 __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int32_t* parent,
                                                          const int32_t* last, int N,
                                                          int32_t* out_lens, FastDiv row_div,
@@ -147,9 +147,9 @@ __global__ __launch_bounds__(kMoveThreads) void k_commit(CacheView c, const int3
 // One workgroup: the counts of a full pool are at most a few hundred kilobytes, and each step
 // depends on the one before (what is given back can be taken, sequences are served in order), so
 // several would wait for each other across the GPU twice.  Bound by that chain of loads, prefix
-// sums and stores: 4 us for 8 sequences over 600 pages; 1024 sequences over 131072 pages 4.5 us
-// giving back and 9.6 us taking four pages each (the search passes 16 KB of counts a round, and
-// ends where enough are found).
+// sums and stores: for 8 sequences over 600 pages 5.4 us taking pages and 4.0 giving them back; for
+// 1024 sequences over 131072 pages, four each, 9.8 and 7.6 us (the search passes 16 KB of counts a
+// round, and ends where enough are found).
 
 struct PoolScan {
   int2 wave[2][kPoolWaves];

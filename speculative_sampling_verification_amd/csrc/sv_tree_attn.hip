@@ -19,14 +19,15 @@
 // that spans several workgroups leaves a part (O, m, l) with each, joined by k_tree_join in
 // workgroup order.
 //
-// What bounds it, by the rows r that share a kv head's keys (8 kv heads of 128 columns, bf16,
-// attention and join): few rows, the bytes of the keys and values: r = 4, 64 ragged sequences of
-// up to 8191 tokens, 1.21 GB in 227 us, 5.3 TB/s.  Many rows, the products and the exponentials
-// beside them (16 a lane and block of 32 keys take as many cycles as the block's 16 matrix
-// instructions): r = 512, 131072 tokens, 275 GFLOP in 310 us, 890 TFLOP/s, three quarters of what
-// a large library product reaches on the same card; LDS reads have no bank conflicts.  Between
-// them (r = 256, 32 ragged sequences of up to 4096 tokens, 69 GFLOP in 127 us) the cut itself
-// counts: 256 groups on 256 workgroups leave 64 MB of parts, written and read again.
+// What bounds it, by the rows r that share a kv head's keys (8 kv heads of 128 columns, bf16; whole
+// calls one behind the other, medians): few rows, the bytes of the keys and values: r = 4, 64
+// sequences of 1023 to 8191 tokens, 1.21 GB in 224 us, 5.4 TB/s.  Many rows, the products and the
+// exponentials beside them (16 a lane and block of 32 keys take as many cycles as the block's 16
+// matrix instructions): r = 512, 131072 tokens, 275 GFLOP in 316 us, 870 TFLOP/s, three quarters of
+// what a large library product reaches on the same card, matrix units busy 46% of the cycles of a
+// clock that the card lowers to 1.8 GHz; LDS reads have no bank conflicts.  Between them (r = 256,
+// 32 sequences of 512 to 4096 tokens, 69 GFLOP in 130 us) the cut itself counts: 256 groups on 256
+// workgroups leave 64 MB of parts, written and read again.
 
 #include <hip/hip_runtime.h>
 
@@ -376,8 +377,9 @@ void k_tree_attn(AttnArgs a) {
     const int first_node = mt * MT / a.G;
     const int last_node = (rows < (mt + 1) * MT ? sw.n : ((mt + 1) * MT - 1) / a.G + 1) - 1;
     // keys that every row of the tile sees, and the tiles behind those that some row sees (a chain:
-    // up to its own node; at least one tile, so that the part has a result).  The cut counts all
-    // tiles alike: 4 pieces of prompts of 1000 nodes take 128 us, 195 without leaving tiles out
+    // up to its own node; at least one tile, so that the part has a result).  4 pieces of prompts of
+    // 1000 nodes behind up to 1000 tokens take 128 us, 195 without leaving tiles out.  The cut
+    // counts all tiles alike, so a worker whose pieces all lie behind has an empty part to show
     const int open = a.mask ? sw.len : sw.len + first_node + 1;
     const int in_sight = a.mask ? part_end : (sw.len + last_node + BN) / BN;
     const int t1 = part_end < in_sight ? part_end : in_sight > t0 ? in_sight : t0 + 1;
@@ -611,8 +613,11 @@ void k_tree_attn(AttnArgs a) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
-          // P rounded to bf16 for the matrix instruction: half a step of 2^-8 per weight, the
-          // rounding the inputs carry; the sum l keeps the unrounded weights
+          // P rounded to bf16 for the matrix instruction: up to half a step, 2^-8, of a weight, as
+          // the inputs carry; the sum l keeps the unrounded weights.  Independent roundings of
+          // weights and of the result, each 1.7e-3 of its value in the mean square, make 2.3e-3 of
+          // the output's size (measured: 2.3e-3 to 2.4e-3).  Products of both halves of a split
+          // weight would take twice the matrix instructions here
           bf16x8 pf;
 #pragma unroll
           for (int i = 0; i < 8; ++i) pf[i] = (__bf16)s[j >> 1][8 * (j & 1) + i];
@@ -1112,9 +1117,9 @@ __global__ __launch_bounds__(256) void k_tree_join(AttnArgs a) {
 // loaded while one is computed, beside a second workgroup's two; longer ones: one tile, and the
 // other workgroups compute while it is loaded.  bf16 rows of 512 bytes: O and Q of 32 rows take 192
 // registers a lane, so four waves and one workgroup a compute unit, with two tiles, for more than
-// 64 rows (32 sequences of up to 4096 tokens, 256 rows: 299 us, 477 with the 64-row workgroups);
-// up to 64 two workgroups of two waves with a tile each (64 sequences of 300 tokens, 48 rows: 58
-// us, 84 with four waves and two tiles; 32 of up to 4096, 64 rows: 151 and 148).
+// 64 rows (32 sequences of 512 to 4096 tokens, 8 kv heads, 256 rows: 298 us, 483 with the 64-row
+// workgroups); up to 64 two workgroups of two waves with a tile each (64 sequences of 300 tokens,
+// 48 rows: 46 us, 50 with the 128-row workgroups; 32 of 512 to 4096, 64 rows: 151 and 150).
 struct Shape {
   int wm, wk, ks, nst, occ;
   int per_cu = 0;  // workgroups that a compute unit holds
@@ -1221,18 +1226,21 @@ Shape shape_of(int D, int row_tile) {
 }
 
 // Rows of a tile.  A tile too small reads the keys again for each further one, a tile too large
-// computes rows that do not exist and leaves larger parts; the smallest that holds all rows, but:
+// computes rows that do not exist and leaves larger parts; the smallest that holds all rows, but
+// (attention and join; 8 kv heads; A: 64 sequences of 1023 to 8191 tokens, 4 rows a kv head; B: 32
+// of 512 to 4096, the rows given; C: 32 of 4096, 4 rows):
 // - bf16 rows of 192 and 256 bytes take 64 instead of 32: LDS holds two workgroups either way and
-//   four waves load better than two (32 sequences of 4096 tokens, 8 kv heads of 128: 4 rows 112
-//   against 117 us, 32 rows 118 against 121; 64 ragged ones of up to 8191: 232 both).  With 128
-//   bytes LDS holds more workgroups of two waves (ragged, 64 columns: 122 us with 32 rows, 139
-//   with 64), with 512 one tile each (232 and 237), and fp32 products of rows that do not exist
-//   cost 16 times as much (64 columns: 146 and 198).
+//   four waves load better than two (128 columns, tiles of 64 against 32: C 108 and 114 us, B with
+//   20 rows 67 and 69, with 32 rows 71 and 74, A 222 and 221; 96 columns: C 86 and 89, B with 32
+//   rows 53 and 53, A 205 and 201).  With 128 bytes LDS holds more workgroups of two waves (A: 122
+//   us with 32 rows a tile, 142 with 64), with 512 one tile each (A: 422 and 428), and fp32 products
+//   of rows that do not exist cost 16 times as much (64 columns, A: 259 and 363).
 // - beyond 128 rows bf16 rows of 128 and 256 bytes take 256 rows a workgroup and the kernel's
-//   pipelined loop (256 rows of 128 columns: 169 us against 188 with tiles of 128; 128 rows: 153
-//   against 133).  Rows of 192 bytes do not spread evenly over eight waves' loads, those of 512
-//   leave no room for the loop's four tiles; fp32 is bound by its products (128 and 64 rows a tile:
-//   178 and 183 us at 128 rows).
+//   pipelined loop (B with 256 rows, tiles of 256 against 128: 126 and 144 us at 128 columns, 78
+//   and 82 at 64; with 128 rows, 128 columns: 106 and 96).  Rows of 192 bytes do not spread evenly
+//   over eight waves' loads, those of 512 leave no room for four tiles of the loop's 64 keys; fp32
+//   takes 128 (B with 128 rows, tiles of 128 against 64: 366 and 400 us at 128 columns, 187 and 202
+//   at 64).
 // - rows of 1024 bytes (fp32) stay at 64: O of a row takes 128 registers, Q 128.
 int row_tile_for(bool bf16, int row_bytes, long long rows) {
   if (rows <= 32 && !(bf16 && row_bytes > 128 && row_bytes <= 256)) return 32;
