@@ -81,9 +81,9 @@ def attention(c, mask=None, nodes=None):
         n = N if nodes is None else int(nodes[b])
         length = int(c.lens[b])
         at = c.slots(b, 0, length + n)
-        if n == 0:
-            continue
         there = at >= 0
+        if n == 0 or not there.any():
+            continue
         x = torch.arange(len(at), device="cuda")[there] - length
         at = at[there]
         if mask is None:
