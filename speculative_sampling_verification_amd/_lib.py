@@ -508,6 +508,9 @@ class PagedCache:
                 with them the other calls leave alone what another sequence holds by now
     """
 
+    _FIXED = frozenset(("k", "v", "page_table", "seq_lens", "seq_pages", "refcount", "device", "dtype",
+                        "layers", "pages", "page_size", "kv_heads", "head_dim", "seqs"))
+
     def __init__(self, k, v, page_table, seq_lens, *, seq_pages=None, refcount=None):
         dev = k.device
         if k.dim() == 4:
@@ -544,7 +547,7 @@ class PagedCache:
 
     def __setattr__(self, name, value):
         # the addresses are taken once: another tensor in an attribute's place would be ignored
-        if self.__dict__.get(name, value) is not value:
+        if name in self._FIXED and self.__dict__.get(name, value) is not value:
             raise AttributeError(f"{name} is fixed: change the tensor in place, or make another "
                                  "PagedCache")
         object.__setattr__(self, name, value)

@@ -14,6 +14,8 @@ def test_attributes_do_not_change_their_tensors():
             setattr(c, name, getattr(c, name).clone())
     with pytest.raises(AttributeError):
         c.page_size = 8
+    c.steps = 1              # a caller's own note
+    c.steps = 2
     c.seq_lens += 2          # in place: the same tensor
     c.seq_lens[1] = 7
     assert c.seq_lens is i and i.tolist() == [2, 7, 2]
