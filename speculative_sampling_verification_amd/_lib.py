@@ -562,16 +562,8 @@ class PagedCache:
         return need
 
 
-def _new(shape, dtype, device, stream):
-    """An output tensor of the stream that will write it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _new_like(t, stream):
-    """The same with a dense tensor's shape and type (less to parse for torch than those)."""
+    """An output tensor with a dense tensor's shape and type, of the stream that will write it."""
     if stream is None:
         return torch.empty_like(t)
     with torch.cuda.stream(stream):
@@ -600,13 +592,11 @@ def _raw_stream(cache, stream):
     return torch._C._cuda_getCurrentRawStream(cache._index)
 
 
-def _capturing(cache, stream):
-    """Whether the stream to launch on is being captured into a graph."""
-    if stream is None:
-        if torch._C._cuda_getDevice() == cache._index:
-            return torch.cuda.is_current_stream_capturing()
-        stream = torch.cuda.current_stream(cache.device)
-    with torch.cuda.stream(stream):
+def _capturing(cache):
+    """Whether the cache's device's current stream is being captured into a graph."""
+    if torch._C._cuda_getDevice() == cache._index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(cache._index):
         return torch.cuda.is_current_stream_capturing()
 
 
@@ -652,6 +642,11 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     Returns a dict: out (like q, dense) and, if want_lse, lse [seqs, N, q_heads] float32.
     ``out`` may hold preallocated tensors under the same keys.
     """
+    if stream is not None:
+        _raw_stream(cache, stream)  # refuses a stream of another device
+        with torch.cuda.stream(stream):
+            return spec_tree_attention(q, cache, layer=layer, mask=mask, num_nodes=num_nodes,
+                                       scale=scale, want_lse=want_lse, out=out)
     strides = _row_strides(q, "q", cache, None)
     shape = q.shape
     B, N, H, D = shape
@@ -660,19 +655,20 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (B,))
     out = dict(out) if out else {}
     if "out" not in out:
-        out["out"] = _new_like(q, stream) if strides is None else _new(shape, q.dtype, dev, stream)
+        out["out"] = torch.empty_like(q) if strides is None else torch.empty(
+            shape, dtype=q.dtype, device=dev)
     if want_lse and "lse" not in out:
-        out["lse"] = _new((B, N, H), torch.float32, dev, stream)
+        out["lse"] = torch.empty((B, N, H), dtype=torch.float32, device=dev)
     out_at = _arg(out["out"], "out out", cache, q.dtype, shape)
     lse_at = _arg(out.get("lse"), "out lse", cache, torch.float32, (B, N, H))
     need = cache._attention_workspace(N, H)
-    raw = _raw_stream(cache, stream)
-    if _capturing(cache, stream):  # the graph's own: graphs may run side by side
-        ws = _new((need,), torch.uint8, dev, stream)
+    raw = _raw_stream(cache, None)
+    if _capturing(cache):  # the graph's own: graphs may run side by side
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         ws = _workspaces.get((dev.type, cache._index, raw))
         if ws is None or ws.numel() < need:
-            ws = workspace(dev, need, stream)
+            ws = workspace(dev, need)
     _cache_call(cache, "spec_tree_attention", _lib.spec_tree_attention, q.data_ptr(), strides, N,
                 H, cache._ref, layer, mask_at, nodes_at, D ** -0.5 if scale is None else scale,
                 out_at, lse_at, ws.data_ptr(), ws.numel(), raw)
