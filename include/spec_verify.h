@@ -446,6 +446,78 @@ int spec_cache_resize(const sv_cache* cache, const int32_t* want, const int32_t*
 int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* dst, int F,
                     int32_t* out_ok, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Rotary positions, before the cache is written and attended to.
+ *
+ * Pair p of a head's columns, p < rot_dim / 2, is turned by the angle t inv_freq[p] of the token's
+ * position t and multiplied by `amplitude`:
+ *   x' = amplitude (x cos - y sin),  y' = amplitude (x sin + y cos)
+ * The pair is columns (p, p + rot_dim / 2), or (2 p, 2 p + 1) if `interleaved` is 1 (0 otherwise).
+ * Columns from rot_dim on are copied.  Token i of sequence b is at position
+ *   t = base[b] + (positions ? positions[b, i] : i),
+ * so that a tree's nodes are given their depths (spec_build_tree's out_depth) and a chain nothing;
+ * positions may be negative: the turn of -t undoes that of t, and is its gradient.  Positions are
+ * not slots: after spec_cache_evict a sequence's next position is still the number of tokens
+ * before it.  Angles are brought to their remainder in 64 bits, so far positions lose nothing;
+ * sums are in fp32, results rounded once.
+ * ---------------------------------------------------------------------------------------------
+ */
+
+/* How spec_rotary_frequencies stretches the frequencies theta^(-2 p / rot_dim) to longer contexts. */
+enum {
+  SV_ROTARY_PLAIN = 0,
+  SV_ROTARY_LINEAR = 1, /* all divided by factor (positions interpolated)                         */
+  SV_ROTARY_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)): the slowest divided by factor,
+                           the fastest kept                                                       */
+  SV_ROTARY_YARN = 3    /* by the turns r = original_length f / (2 pi) that a pair makes in the
+                           original context: kept from beta_fast turns on, divided by factor up to
+                           beta_slow, linear in r between (Peng et al., "YaRN: Efficient Context
+                           Window Extension of Large Language Models", NTK-by-parts; the paper's
+                           beta_fast 32, beta_slow 1); amplitude 0.1 ln(factor) + 1               */
+};
+
+/*
+ * Frequencies of the rot_dim / 2 pairs to HOST memory, and the amplitude that goes with them (1 but
+ * for SV_ROTARY_YARN; out_amplitude may be NULL).  rot_dim even, 2..4096; theta > 0; factor >= 1.
+ * No GPU work; any other table may be given to the calls below as well.
+ */
+int spec_rotary_frequencies(int rot_dim, double theta, int scaling, double factor,
+                            double original_length, double beta_fast, double beta_slow,
+                            double* out_inv_freq, float* out_amplitude);
+
+/*
+ * Turns queries and keys.
+ *   q           [seqs, N, q_heads, head_dim] with element strides q_strides[3] of sequence, token and
+ *               head (NULL: dense), 16-byte aligned rows; k likewise, with k_heads.  Either may be
+ *               NULL with 0 heads.  seqs * N <= 2^31 - 1; head_dim a multiple of 16 bytes, at most
+ *               1024
+ *   out_q       dense, or q itself: turned in place, with q's strides (rows that lie apart);
+ *               out_k likewise
+ *   inv_freq    [rot_dim / 2] double, device; rot_dim even, 2..head_dim
+ *   amplitude   finite
+ *   base        [seqs] or NULL (0); positions [seqs, N] or NULL (0 .. N - 1)
+ * What is written shares no memory with anything else of the call; queries and keys in place may be
+ * parts of one tensor, made by one product, whose tokens hold one after the other.
+ */
+int spec_rotary(const void* q, const int64_t* q_strides, int q_heads, void* out_q, const void* k,
+                const int64_t* k_strides, int k_heads, void* out_k, sv_dtype dtype, int seqs, int N,
+                int head_dim, const double* inv_freq, int rot_dim, int interleaved, float amplitude,
+                const int32_t* base, const int32_t* positions, hipStream_t stream);
+
+/*
+ * spec_rotary of q and k_new and spec_cache_append of the turned keys and of v_new in one pass.
+ *   q, out_q    as above, of the cache's dtype and head_dim (NULL with 0 heads: keys and values alone)
+ *   k_new, v_new, new_strides, N, num_nodes   as spec_cache_append takes them
+ *   base        [seqs] or NULL: the committed lengths seq_lens
+ * Rows of out_q past num_nodes are left as they were.
+ */
+int spec_rotary_append(const void* q, const int64_t* q_strides, int q_heads, void* out_q,
+                       const void* k_new, const void* v_new, const int64_t* new_strides, int N,
+                       const sv_cache* cache, int layer, const int32_t* num_nodes,
+                       const double* inv_freq, int rot_dim, int interleaved, float amplitude,
+                       const int32_t* base, const int32_t* positions, hipStream_t stream);
+
 /* Static string for a status code. */
 const char* spec_verify_status_string(int status);
 

@@ -50,6 +50,7 @@ EXPORTS = [
     "spec_verify_presampled", "spec_verify_noalloc",
     "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append",
     "spec_cache_commit", "spec_cache_resize", "spec_cache_fork",
+    "spec_rotary", "spec_rotary_append", "spec_rotary_frequencies",
     "spec_expected_tokens",
     "spec_walltime_speedup", "spec_ops_factor", "spec_optimal_gamma",
     "spec_verify_status_string",
@@ -110,6 +111,14 @@ def load(path=LIB_PATH):
     lib.spec_cache_fork.argtypes = [pcache, vp, vp, i32, vp, vp]
     lib.spec_cache_fork.restype = i32
     dbl = ctypes.c_double
+    lib.spec_rotary.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, i32,
+                                f32, vp, vp, vp]
+    lib.spec_rotary.restype = i32
+    lib.spec_rotary_append.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, pcache, i32, vp, vp, i32,
+                                       i32, f32, vp, vp, vp]
+    lib.spec_rotary_append.restype = i32
+    lib.spec_rotary_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, vp]
+    lib.spec_rotary_frequencies.restype = i32
     lib.spec_expected_tokens.argtypes = [dbl, i32]
     lib.spec_expected_tokens.restype = dbl
     lib.spec_walltime_speedup.argtypes = [dbl, i32, dbl]
@@ -609,6 +618,13 @@ def _cache_call(cache, name, fn, *args):
             _launch(name, fn, *args)
 
 
+class _Place:
+    """Where a call without a cache runs: what the helpers above ask of a PagedCache."""
+
+    def __init__(self, device):
+        self.device, self._index = device, device.index
+
+
 def _row_strides(t, name, cache, heads):
     """The element strides of a [seqs, N, heads, head_dim] tensor, None where it is dense."""
     if not isinstance(t, torch.Tensor):
@@ -745,6 +761,125 @@ def spec_cache_fork(cache, src, dst, *, out=None, stream=None):
         out = _new_like(src, stream)
     _cache_call(cache, "spec_cache_fork", _lib.spec_cache_fork, cache._ref, src_at, dst_at, F[0],
                 _arg(out, "out", cache, torch.int32, F), _raw_stream(cache, stream))
+    return out
+
+
+ROTARY_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}  # SV_ROTARY_*
+
+
+def rotary_frequencies(rot_dim, *, theta=10000.0, scaling=None, factor=1.0, original_length=0.0,
+                       beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """Frequencies theta ** (-2 p / rot_dim) of the rot_dim / 2 pairs for spec_rotary, as a float64
+    tensor on ``device``, and the amplitude that goes with them.  ``scaling`` stretches them to a
+    longer context by ``factor``: "linear", "ntk", or "yarn" (with the original_length that the
+    frequencies were made for; see include/spec_verify.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROTARY_SCALINGS)}, got {scaling!r}")
+    rot_dim = int(rot_dim)
+    freq = (ctypes.c_double * max(1, rot_dim // 2))()
+    amplitude = ctypes.c_float()
+    code = _lib.spec_rotary_frequencies(rot_dim, float(theta), ROTARY_SCALINGS[scaling],
+                                        float(factor), float(original_length), float(beta_fast),
+                                        float(beta_slow), freq, ctypes.byref(amplitude))
+    if code != SV_OK:
+        raise SpecVerifyError("spec_rotary_frequencies", code)
+    return torch.tensor(list(freq), dtype=torch.float64, device=device), amplitude.value
+
+
+def _turned_out(t, name, strides, given, stream):
+    """The tensor that t's turned rows go to: the one given (t itself or dense), or a new one."""
+    if given is None:
+        if strides is None:
+            return _new_like(t, stream)
+        with torch.cuda.stream(stream):  # None: the current one
+            return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if not isinstance(given, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if given.data_ptr() == t.data_ptr() and given.dtype is t.dtype and \
+            given.shape == t.shape and given.stride() == t.stride():
+        return given
+    _need(given, name, t.device, t.dtype, t.shape)
+    return given
+
+
+def _rotary_arg(inv_freq, place):
+    if not isinstance(inv_freq, torch.Tensor):
+        raise TypeError("inv_freq must be a torch.Tensor")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    return _arg(inv_freq, "inv_freq", place, torch.float64, inv_freq.shape)
+
+
+def spec_rotary(q, inv_freq, *, k=None, base=None, positions=None, interleaved=False,
+                amplitude=1.0, out=None, stream=None):
+    """Turns the first 2 * len(inv_freq) columns of queries and keys to their positions
+    base[seq] + positions[seq, i] (see include/spec_verify.h).
+
+    q, k [seqs, N, heads, head_dim] (bf16 or fp32; strided views with contiguous head_dim are taken
+    as they are); inv_freq float64 on the device (rotary_frequencies); base [seqs] int32 or None
+    (0); positions [seqs, N] int32 or None (0 .. N - 1).  Returns a dict: q and, if given, k.
+    ``out`` may hold tensors under the same keys: dense ones, or q and k themselves to turn them in
+    place."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 4:
+        raise ValueError("q must be [seqs, N, heads, head_dim]")
+    place = _Place(q.device)
+    place.dtype, (place.seqs, N, heads, place.head_dim) = q.dtype, q.shape
+    dt = _dtype_code(q)
+    strides = {"q": _row_strides(q, "q", place, None)}
+    if k is not None:
+        strides["k"] = _row_strides(k, "k", place, None)
+        if k.shape[1] != N:
+            raise ValueError(f"k must be [{place.seqs}, {N}, heads, {place.head_dim}], "
+                             f"got {tuple(k.shape)}")
+    freq_at = _rotary_arg(inv_freq, place)
+    base_at = _arg(base, "base", place, torch.int32, (place.seqs,))
+    at = _arg(positions, "positions", place, torch.int32, (place.seqs, N))
+    raw = _raw_stream(place, stream)
+    out = dict(out) if out else {}
+    out["q"] = _turned_out(q, "out q", strides["q"], out.get("q"), stream)
+    if k is not None:
+        out["k"] = _turned_out(k, "out k", strides["k"], out.get("k"), stream)
+    elif "k" in out:
+        raise ValueError("out holds k, but no k is given")
+    _cache_call(place, "spec_rotary", _lib.spec_rotary, q.data_ptr(), strides["q"], heads,
+                out["q"].data_ptr(), None if k is None else k.data_ptr(), strides.get("k"),
+                0 if k is None else k.shape[2], None if k is None else out["k"].data_ptr(), dt,
+                place.seqs, N, place.head_dim, freq_at, 2 * inv_freq.numel(), int(interleaved),
+                amplitude, base_at, at, raw)
+    return out
+
+
+def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, positions=None,
+                       num_nodes=None, interleaved=False, amplitude=1.0, out=None, stream=None):
+    """spec_rotary of q and k_new and spec_cache_append of the turned keys and of v_new in one pass
+    (see include/spec_verify.h).  base [seqs] int32 defaults to the cache's seq_lens: give a tree's
+    depths as ``positions``, and the tokens' number as ``base`` once some were evicted.  Returns
+    the turned queries: ``out`` (dense, or q itself to turn it in place), or a new tensor; rows past
+    num_nodes are left as they were."""
+    new_strides = _row_strides(k_new, "k_new", cache, cache.kv_heads)
+    v_strides = _row_strides(v_new, "v_new", cache, cache.kv_heads)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    if new_strides is not v_strides and (new_strides is None or v_strides is None
+                                         or list(new_strides) != list(v_strides)):
+        raise ValueError("k_new and v_new must have the same strides")
+    N = k_new.shape[1]
+    q_strides = _row_strides(q, "q", cache, None)
+    if q.shape[1] != N:
+        raise ValueError(f"q must be [{cache.seqs}, {N}, heads, {cache.head_dim}], "
+                         f"got {tuple(q.shape)}")
+    freq_at = _rotary_arg(inv_freq, cache)
+    base_at = _arg(base, "base", cache, torch.int32, (cache.seqs,))
+    at = _arg(positions, "positions", cache, torch.int32, (cache.seqs, N))
+    nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (cache.seqs,))
+    raw = _raw_stream(cache, stream)
+    out = _turned_out(q, "out", q_strides, out, stream)
+    _cache_call(cache, "spec_rotary_append", _lib.spec_rotary_append, q.data_ptr(), q_strides,
+                q.shape[2], out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new_strides, N,
+                cache._ref, layer, nodes_at, freq_at, 2 * inv_freq.numel(), int(interleaved),
+                amplitude, base_at, at, raw)
     return out
 
 

@@ -23,20 +23,6 @@ constexpr int kMoveThreads = 256;
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWaves = kPoolThreads / 64;
 
-// Byte offset of a position's row in the pages of sequence b, which holds `held` of them; -1 where
-// it has no page.
-__device__ __forceinline__ int64_t row_offset(const CacheView& c, int b, int held, int pos) {
-  if (pos < 0 || pos >= c.cap) return -1;
-  const uint32_t pi = fast_div(c.page_div, (uint32_t)pos);
-  const int page = c.table[(size_t)b * c.width + pi];
-  if (!names_page(c, held, pos, page)) return -1;
-  return (int64_t)page * c.page_stride + (int64_t)(pos - (int)(pi * c.page_div.d)) * c.token_stride;
-}
-
-__device__ __forceinline__ int clamp_len(const CacheView& c, int len) {
-  return len < 0 ? 0 : len > c.cap ? c.cap : len;
-}
-
 // One thread per 16 bytes of a node's keys, and the same of its values: both loads are on their
 // way together, and rows of a page are written in full lines.  Bound by the bytes (16 sequences of
 // up to 1000 tokens, 8 kv heads of 128 bf16: 124 MB read and written in 20 us, 6.2 TB/s); a few

@@ -65,6 +65,20 @@ __device__ __forceinline__ bool names_page(const CacheView& c, int held, int pos
   return pos < held || c.refcount[page] == 0;
 }
 
+// Byte offset of a position's row in the pages of sequence b, which holds `held` of them; -1 where
+// it has no page.
+__device__ __forceinline__ int64_t row_offset(const CacheView& c, int b, int held, int pos) {
+  if (pos < 0 || pos >= c.cap) return -1;
+  const uint32_t pi = fast_div(c.page_div, (uint32_t)pos);
+  const int page = c.table[(size_t)b * c.width + pi];
+  if (!names_page(c, held, pos, page)) return -1;
+  return (int64_t)page * c.page_stride + (int64_t)(pos - (int)(pi * c.page_div.d)) * c.token_stride;
+}
+
+__device__ __forceinline__ int clamp_len(const CacheView& c, int len) {
+  return len < 0 ? 0 : len > c.cap ? c.cap : len;
+}
+
 struct AttnArgs {
   CacheView c;
   const char* q;

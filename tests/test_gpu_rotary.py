@@ -1,0 +1,247 @@
+"""spec_rotary and spec_rotary_append (through the C ABI) against the oracle in 64 bits.
+
+Error bound, u = 2^-24 (a rounding to fp32 is off by u of the value at most).  The turn: the angle
+beyond whole quarter turns, f <= 1/2, is rounded to fp32, and times pi / 2: off by 3 u / 2; its
+product in 64 bits is off by 2^-51 of the angle; the Taylor sums (|.| <= 1, terms behind the first
+at most 0.31 in size) by 3 u: 5 u in all, 6 u with the amplitude.  A result x cos - y sin is a product
+rounded and a fused one: (|x| + |y|) s (8 u + 2^-50 |angle|), and bf16 rounds it once, by 2^-8 of it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.decode_step_oracle as O
+import oracle.paged_cache_oracle as PO
+from cache_cases import BF16_HALF_STEP, DTYPES, F32_HALF_STEP, announce, ints, random_tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def svm():
+    import speculative_sampling_verification_amd as m
+    return m
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def normal(rng, shape, dtype):
+    return torch.from_numpy(rng.standard_normal(shape)).to(DTYPES[dtype]).cuda()
+
+
+def table(freq):
+    return torch.from_numpy(freq).cuda()
+
+
+def check(got, x, position, freq, interleaved, amplitude, dtype, there=None):
+    """got against the oracle's turn of x, [B, N, H, D] all; `there` [B, N]: rows to look at."""
+    want = O.rotary(x, position, freq, interleaved, amplitude)
+    half = len(freq)
+    pair = np.abs(x)
+    if interleaved:
+        a = pair[..., 0:2 * half:2] + pair[..., 1:2 * half:2]
+        size = np.repeat(a, 2, axis=-1)
+    else:
+        a = pair[..., :half] + pair[..., half:2 * half]
+        size = np.concatenate([a, a], axis=-1)
+    angle = np.abs(position[..., None] * freq)
+    angle = np.repeat(angle, 2, -1) if interleaved else np.concatenate([angle, angle], -1)
+    tol = np.zeros_like(want)
+    tol[..., :2 * half] = size * abs(amplitude) * (8 * F32_HALF_STEP
+                                                   + 2.0 ** -50 * angle[:, :, None, :])
+    if dtype == "bf16":
+        tol[..., :2 * half] += (np.abs(want[..., :2 * half]) + tol[..., :2 * half]) * BF16_HALF_STEP
+    bad = ~(np.abs(got - want) <= tol)
+    if there is not None:
+        bad &= there[:, :, None, None]
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+# (B, N, Hq, Hk, D, rot, positions up to)
+SHAPES = [(1, 1, 1, 0, 64, 64, 0), (1, 5, 8, 8, 64, 64, 200), (3, 7, 6, 2, 96, 48, 131072),
+          (2, 33, 5, 1, 128, 20, 1000000), (5, 3, 4, 4, 256, 256, 8191), (2, 9, 3, 1, 8, 2, 77),
+          (1, 1000, 2, 1, 128, 128, 16000000), (64, 1, 32, 8, 128, 128, 8191),
+          (2, 5, 1, 1, 256, 6, 2 ** 30), (4, 65, 2, 3, 40, 24, 500), (700, 3, 1, 1, 16, 16, 99)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_turns(svm, shape, interleaved, dtype):
+    B, N, Hq, Hk, D, rot, top = shape
+    announce(f"rotary {shape} interleaved={interleaved} {dtype}")
+    rng = np.random.default_rng(D + rot)
+    freq, _ = O.rotary_frequencies(rot, theta=500000.0, scaling="yarn", factor=4.0,
+                                   original_length=8192)
+    q = normal(rng, (B, N, Hq, D), dtype)
+    k = normal(rng, (B, N, Hk, D), dtype) if Hk else None
+    base = rng.integers(0, top + 1, B).astype(np.int32)
+    for positions in (None, rng.integers(-N, N + 1, (B, N)).astype(np.int32)):
+        at = base[:, None].astype(np.int64) + (np.arange(N)[None, :] if positions is None
+                                               else positions)
+        got = svm.spec_rotary(q, table(freq), k=k, base=ints(base),
+                              positions=None if positions is None else ints(positions),
+                              interleaved=interleaved, amplitude=1.25)
+        check(host(got["q"]), host(q), at, freq, interleaved, 1.25, dtype)
+        assert ("k" in got) == (k is not None)
+        if k is not None:
+            check(host(got["k"]), host(k), at, freq, interleaved, 1.25, dtype)
+    # no base: positions from 0; in place, the same bits
+    plain = svm.spec_rotary(q, table(freq), interleaved=interleaved)["q"]
+    check(host(plain), host(q), np.tile(np.arange(N), (B, 1)), freq, interleaved, 1.0, dtype)
+    here = q.clone()
+    got = svm.spec_rotary(here, table(freq), interleaved=interleaved, out={"q": here})
+    assert got["q"] is here and torch.equal(here, plain)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_strided_parts_of_one_product_in_place(svm, interleaved):
+    announce("queries and keys as parts of one tensor, turned in place")
+    rng = np.random.default_rng(5)
+    B, N, Hq, Hk, D = 3, 6, 4, 2, 64
+    freq, _ = O.rotary_frequencies(32)
+    qkv = normal(rng, (B, N, Hq + 2 * Hk, D), "bf16")
+    before = qkv.clone()
+    q, k = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hk]
+    dense = svm.spec_rotary(q, table(freq), k=k, interleaved=interleaved)
+    assert dense["q"].is_contiguous() and torch.equal(qkv, before)
+    svm.spec_rotary(q, table(freq), k=k, interleaved=interleaved, out={"q": q, "k": k})
+    assert torch.equal(q, dense["q"]) and torch.equal(k, dense["k"])
+    assert torch.equal(qkv[:, :, Hq + Hk:], before[:, :, Hq + Hk:])
+    # tokens before sequences, a broadcast sequence
+    t = normal(rng, (N, B, Hq, D), "f32").transpose(0, 1)
+    one = normal(rng, (1, N, Hq, D), "f32").expand(B, -1, -1, -1)
+    base = np.array([3, 900, 70000], dtype=np.int32)
+    at = base[:, None] + np.arange(N)
+    for x in (t, one):
+        got = svm.spec_rotary(x, table(freq), base=ints(base), interleaved=interleaved)["q"]
+        check(host(got), host(x), at, freq, interleaved, 1.0, "f32")
+
+
+def test_turn_back(svm):
+    announce("the turn of -t undoes that of t")
+    rng = np.random.default_rng(6)
+    freq, _ = O.rotary_frequencies(64)
+    x = normal(rng, (2, 9, 3, 64), "f32")
+    t = ints(rng.integers(0, 100000, (2, 9)).astype(np.int32))
+    y = svm.spec_rotary(x, table(freq), positions=t)["q"]
+    back = svm.spec_rotary(y, table(freq), positions=-t)["q"]
+    # two turns, each off by 8 u (|x| + |y|), the first one's error turned once more
+    size = x[..., :32].abs() + x[..., 32:].abs()
+    tol = torch.cat([size, size], -1) * (24 * F32_HALF_STEP)
+    assert ((back - x).abs() <= tol).all()
+
+
+class Books:
+    """A cache of B sequences with books; sequence 2's last page is missing, sequence 3 is full."""
+
+    def __init__(self, svm, dtype, N, Hkv, D, page=8):
+        rng = self.rng = np.random.default_rng(N + D)
+        self.lens = np.array([0, 13, 7, 3 * page, 5], dtype=np.int32)
+        B, width = 5, 3 + -(-N // page)
+        pages = B * width + 3
+        self.table = rng.permutation(pages)[:B * width].reshape(B, width).astype(np.int32)
+        self.table[2, (7 + N - 1) // page] = -1
+        # what the last sequence names behind its one page is another's by now
+        self.held = np.array([width] * 4 + [1], dtype=np.int32)
+        self.ref = np.zeros(pages, dtype=np.int32)
+        for b in range(4):
+            self.ref[self.table[b][self.table[b] >= 0]] = 1
+        self.ref[self.table[4]] = 1
+        self.width, self.page = width, page
+        self.k, self.v = (normal(rng, (2, pages, page, Hkv, D), dtype) for _ in range(2))
+        self.cache = svm.PagedCache(self.k, self.v, ints(self.table), ints(self.lens),
+                                    seq_pages=ints(self.held), refcount=ints(self.ref))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,Hq,Hkv,D,rot,interleaved", [
+    (1, 4, 2, 64, 64, False), (6, 3, 3, 128, 32, True), (11, 4, 1, 96, 20, False),
+    (17, 8, 2, 40, 40, True), (70, 2, 2, 256, 128, False)])
+def test_append(svm, N, Hq, Hkv, D, rot, interleaved, dtype):
+    announce(f"rotary_append N={N} {Hq}/{Hkv}x{D} rot={rot} {dtype}")
+    c = Books(svm, dtype, N, Hkv, D)
+    rng = c.rng
+    freq, _ = O.rotary_frequencies(rot)
+    q = normal(rng, (5, N, Hq, D), dtype)
+    new = normal(rng, (5, N, 2 * Hkv, D), dtype)
+    k_new, v_new = new[:, :, :Hkv], new[:, :, Hkv:]
+    depth = np.zeros((5, N), dtype=np.int32)
+    parent, _ = random_tree(rng, 5, N)
+    for i in range(1, N):
+        depth[:, i] = depth[np.arange(5), parent[:, i]] + 1
+    base = rng.integers(0, 50000, 5).astype(np.int32)
+    for nodes, positions, start in ((None, None, None), (rng.integers(0, N + 1, 5), depth, base)):
+        kd, vd = host(c.k), host(c.v)
+        nodes = None if nodes is None else nodes.astype(np.int32)
+        out = torch.full_like(q, 7.0)
+        got = svm.spec_rotary_append(
+            q, k_new, v_new, c.cache, table(freq), layer=1, interleaved=interleaved,
+            base=None if start is None else ints(start), out=out,
+            positions=None if positions is None else ints(positions),
+            num_nodes=None if nodes is None else ints(nodes), amplitude=0.9)
+        assert got is out
+        at = (c.lens if start is None else start)[:, None] + \
+            (np.arange(N)[None, :] if positions is None else positions)
+        there = np.arange(N)[None, :] < (np.full(5, N) if nodes is None else nodes)[:, None]
+        check(host(out), host(q), at, freq, interleaved, 0.9, dtype, there)
+        assert (host(out)[~there] == 7).all()
+        # the turned keys as spec_rotary makes them, in the rows that the oracle appends to
+        turned = svm.spec_rotary(k_new, table(freq), base=ints(c.lens if start is None else start),
+                                 positions=None if positions is None else ints(positions),
+                                 interleaved=interleaved, amplitude=0.9)["q"]
+        PO.append(kd[1], vd[1], host(turned), host(v_new), c.table, c.lens, nodes, c.held, c.ref)
+        np.testing.assert_array_equal(host(c.k), kd)
+        np.testing.assert_array_equal(host(c.v), vd)
+
+
+def test_append_without_room_writes_nothing(svm):
+    announce("rotary_append: no pages, lengths out of range")
+    rng = np.random.default_rng(9)
+    k, v = (normal(rng, (1, 4, 8, 2, 64), "bf16") for _ in range(2))
+    kb, vb = k.clone(), v.clone()
+    freq, _ = O.rotary_frequencies(64)
+    tab = ints(np.array([[-1, 9], [1, 2]], dtype=np.int32))
+    cache = svm.PagedCache(k, v, tab, ints(np.array([0, 2 ** 31 - 1], dtype=np.int32)))
+    new = normal(rng, (2, 5, 2, 64), "bf16")
+    q = svm.spec_rotary_append(new, new, new, cache, table(freq))
+    torch.cuda.synchronize()
+    assert torch.equal(k, kb) and torch.equal(v, vb)
+    assert torch.isfinite(q[0].float()).all()
+
+
+def test_streams_and_graphs(svm):
+    announce("rotary_append on another stream, and captured with lengths that change")
+    rng = np.random.default_rng(11)
+    freq, _ = O.rotary_frequencies(64)
+    B, N = 3, 4
+    k, v = (normal(rng, (1, 30, 8, 2, 64), "f32") for _ in range(2))
+    lens = ints(np.array([1, 9, 20], dtype=np.int32))
+    tab = ints(np.arange(30, dtype=np.int32).reshape(3, 10))
+    cache = svm.PagedCache(k, v, tab, lens)
+    q, new = normal(rng, (B, N, 4, 64), "f32"), normal(rng, (B, N, 2, 64), "f32")
+    f = table(freq)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = svm.spec_rotary_append(q, new, new, cache, f, stream=side)
+    z = svm.spec_rotary(q, f, base=lens, stream=side)["q"]
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        svm.spec_rotary_append(q, new, new, cache, f, out=out)
+    for rep in range(4):
+        lens += 3
+        out.zero_()
+        k.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = svm.spec_rotary(q, f, k=new, base=lens)
+        assert torch.equal(out, want["q"])
+        for b, n in enumerate(lens.tolist()):
+            at = torch.arange(n, n + N, device="cuda")
+            assert torch.equal(k[0, tab[b, at // 8].long(), at % 8], want["k"][b])

@@ -1,0 +1,125 @@
+"""CPU-side refusals of the entry points around tree attention: each bad argument returns its status
+before anything touches a GPU, and the binding names what is wrong with a tensor."""
+
+import ctypes
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from test_cache_abi import BAD_CACHES, cache
+
+INVALID, DTYPE = 1, 2
+D0 = 1 << 20  # stands for device memory; never dereferenced
+Q, QO, K, KO, V, F, B, P, N = (i * 64 * D0 for i in range(3, 12))  # far from each other
+
+
+@pytest.fixture(scope="module")
+def svl():
+    from speculative_sampling_verification_amd import _lib
+    return _lib
+
+
+def strides(*s):
+    return (ctypes.c_int64 * 3)(*s)
+
+
+ROTARY = dict(q=Q, qs=None, hq=4, oq=QO, k=K, ks=None, hk=2, ok=KO, dtype=1, seqs=3, N=5, D=64,
+              freq=F, rot=64, inter=0, amplitude=1.0, base=B, positions=P)
+
+
+def rotary(svl, **over):
+    a = dict(ROTARY)
+    a.update(over)
+    return svl.lib().spec_rotary(*a.values(), None)
+
+
+BAD_ROTARY = [
+    dict(q=None), dict(oq=None), dict(k=None), dict(ok=None), dict(hq=0), dict(hk=0), dict(hq=-1),
+    dict(hq=65537), dict(q=None, oq=None, hq=0, k=None, ok=None, hk=0), dict(seqs=0), dict(N=0),
+    dict(seqs=2 ** 16, N=2 ** 15), dict(D=0), dict(D=60), dict(D=520), dict(freq=None),
+    dict(freq=F + 4), dict(rot=0), dict(rot=7), dict(rot=66), dict(inter=2), dict(inter=-1),
+    dict(amplitude=float("nan")), dict(amplitude=float("inf")), dict(q=Q + 8), dict(oq=QO + 2),
+    dict(k=K + 4), dict(ok=KO + 8), dict(base=B + 2), dict(positions=P + 1),
+    dict(qs=strides(5 * 256, 256, 60)), dict(ks=strides(-640, 128, 64)),
+    # what is written is apart from all else
+    dict(oq=Q + 64), dict(oq=K), dict(ok=Q), dict(ok=QO), dict(oq=F - 16), dict(ok=B - 16),
+    dict(oq=P), dict(ok=K + 16),
+    # in place: rows that lie apart
+    dict(oq=Q, qs=strides(0, 256, 64)), dict(ok=K, ks=strides(640, 0, 64)),
+    dict(oq=Q, qs=strides(5 * 512, 512, 64), k=Q + 2 * 128, ks=strides(5 * 512, 512, 64)),
+    dict(oq=Q, qs=strides(5 * 512, 512, 64), k=Q + 2 * 256, ks=strides(5 * 512, 1024, 64)),
+    dict(oq=Q, qs=strides(5 * 320, 320, 64), k=Q + 2 * 256, ks=strides(5 * 320, 320, 64)),
+]
+
+
+@pytest.mark.parametrize("over", BAD_ROTARY, ids=str)
+def test_rotary_arguments(svl, over):
+    assert rotary(svl, **over) == INVALID
+
+
+def test_rotary_dtype(svl):
+    assert rotary(svl, dtype=2) == DTYPE and rotary(svl, dtype=-1) == DTYPE
+
+
+def append(svl, c=None, **over):
+    a = dict(q=Q, qs=None, hq=4, oq=QO, k=K, v=V, ns=None, N=5,
+             cache=ctypes.byref(c if c is not None else cache(svl)), layer=1, nodes=N, freq=F,
+             rot=64, inter=0, amplitude=1.0, base=B, positions=P)
+    a.update(over)
+    return svl.lib().spec_rotary_append(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHES, ids=[str(b[0]) for b in BAD_CACHES])
+def test_append_refuses_a_bad_cache(svl, over, status):
+    assert append(svl, cache(svl, **over)) == status
+
+
+@pytest.mark.parametrize("over", [
+    dict(k=None), dict(v=None), dict(N=0), dict(N=2049), dict(layer=2), dict(layer=-1),
+    dict(cache=None), dict(q=None), dict(oq=None), dict(hq=0), dict(hq=-2), dict(nodes=N + 1),
+    dict(rot=0), dict(rot=66), dict(freq=None), dict(inter=3), dict(amplitude=float("nan")),
+    dict(v=V + 8), dict(ns=strides(640, 128, 4)), dict(oq=K), dict(oq=V), dict(oq=N), dict(oq=P),
+    # the layer's keys and values, its tables
+    dict(oq=D0), dict(oq=D0 + 2 * 10 * 16 * 128), dict(k=D0 + 2 * 10 * 16 * 128),
+    dict(v=D0 + 2 * 10 * 16 * 128), dict(freq=D0 + 2 * 10 * 16 * 128),
+    dict(q=2 * D0 + 2 * 10 * 16 * 128)], ids=str)
+def test_append_arguments(svl, over):
+    assert append(svl, **over) == INVALID
+
+
+def test_keys_and_values_share_no_row(svl):
+    assert append(svl, cache(svl, v=D0)) == INVALID
+
+
+def test_binding_names_bad_tensors(svl):
+    q, f = torch.zeros((3, 4, 2, 64)), torch.zeros(32, dtype=torch.float64)
+    i = torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: svl.spec_rotary(None, f), lambda: svl.spec_rotary(q[0], f),
+                 lambda: svl.spec_rotary(q.double(), f), lambda: svl.spec_rotary(q.long(), f),
+                 lambda: svl.spec_rotary(q, f.float()), lambda: svl.spec_rotary(q, f[None]),
+                 lambda: svl.spec_rotary(q, None), lambda: svl.spec_rotary(q, f[::2]),
+                 lambda: svl.spec_rotary(q, f, k=q[:, :3]), lambda: svl.spec_rotary(q, f, k=q[:2]),
+                 lambda: svl.spec_rotary(q, f, k=q.bfloat16()),
+                 lambda: svl.spec_rotary(q, f, base=i[:2]),
+                 lambda: svl.spec_rotary(q, f, base=i.long()),
+                 lambda: svl.spec_rotary(q, f, positions=i),
+                 lambda: svl.spec_rotary(q.transpose(2, 3), f),
+                 lambda: svl.spec_rotary(q, f)):  # host memory
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    k = torch.zeros((2, 6, 4, 2, 64))
+    c = svl.PagedCache(k, k.clone(), torch.zeros((3, 5), dtype=torch.int32), i)
+    new = torch.zeros((3, 4, 2, 64))
+    for call in (lambda: svl.spec_rotary_append(q, new, new[:, :3], c, f),
+                 lambda: svl.spec_rotary_append(q[:, :3], new, new, c, f),
+                 lambda: svl.spec_rotary_append(q, q[:, :, :1], q[:, :, :1], c, f),
+                 lambda: svl.spec_rotary_append(q.bfloat16(), new, new, c, f),
+                 lambda: svl.spec_rotary_append(q, new, new, c, f.float()),
+                 lambda: svl.spec_rotary_append(q, new, new, c, f, base=i.long()),
+                 lambda: svl.spec_rotary_append(q, new, new, c, f, num_nodes=i[:1]),
+                 lambda: svl.spec_rotary_append(q, new, new, c, f),
+                 lambda: svl.spec_rotary_append(q, new, new, c, f, stream=SimpleNamespace(
+                     cuda_stream=0, device=torch.device("cuda", 1)))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
