@@ -518,6 +518,58 @@ int spec_rotary_append(const void* q, const int64_t* q_strides, int q_heads, voi
                        const double* inv_freq, int rot_dim, int interleaved, float amplitude,
                        const int32_t* base, const int32_t* positions, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: sequences kept at a budget of tokens.
+ *
+ * weights [layers, seqs, kv_heads, length] float holds what the queries so far gave to the token at
+ * each position, one number a layer and kv head.  A step adds its own behind spec_tree_attention
+ * (spec_cache_weigh, layer by layer); spec_cache_evict then keeps the tokens of largest weight, each
+ * head its own, and spec_cache_resize stores the lengths and gives the pages back, as after
+ * spec_cache_commit.  New tokens start at the weights that lie behind the length: zeros, if the
+ * array began as zeros.
+ * ---------------------------------------------------------------------------------------------
+ */
+
+/*
+ * Adds to the weight of every committed token j of one layer what the nodes' rows give it:
+ *   w[b, h, j] <- decay w[b, h, j] + sum over i < num_nodes and the query heads x of kv head h, with
+ *                 j < seen[b, i], of exp(scale q[b, i, x].k[b, j, h] - lse[b, i, x])
+ *   q, q_strides, N, q_heads, layer, num_nodes, scale   as spec_tree_attention takes them
+ *   lse         [seqs, N, q_heads] of that call; a row of -inf gives nothing
+ *   seen        [seqs, N] or NULL (all): how many of the committed tokens the node sees: its own
+ *               position + 1 where the nodes are committed already (the last tokens of a prompt
+ *               after spec_cache_commit), 0 for a node that is not to count
+ *   decay       in [0, 1]; 0: the array's values are replaced, whatever they are
+ *   weights     as above; positions from `length` on are not weighed, those from seq_lens on are
+ *               left as they are.  Shares no memory with the other arrays
+ * A token without a page gets nothing.  Sums are in fp32, in a fixed order.
+ */
+int spec_cache_weigh(const void* q, const int64_t* q_strides, int N, int q_heads, const float* lse,
+                     const sv_cache* cache, int layer, const int32_t* seen,
+                     const int32_t* num_nodes, float scale, float decay, float* weights, int length,
+                     hipStream_t stream);
+
+/*
+ * Keeps keep[b] tokens of each sequence, in every layer and kv head: the first `sinks`, the last
+ * `recent`, and of those between the ones of largest weight (ties: the earlier; NaN below all).
+ * Kept tokens stay in order: token kept[j]'s rows of keys and values move to position j.
+ *   keep        [seqs]: < 0 leaves the sequence alone, and so does a sequence of no more tokens
+ *   max_keep    1..length, an upper bound of keep
+ *   out_weights like weights, or weights itself: the kept tokens' weights at their new positions, 0
+ *               up to seq_lens, the values of weights behind
+ *   out_lens    [seqs]: keep[b], or seq_lens where the sequence was left alone, as happens too if
+ *               keep[b] > max_keep or < sinks + recent, seq_lens > length, a token has no page, or
+ *               (with refcount) a page that is written (between sinks and keep[b]) belongs to
+ *               another sequence too.  Stored by spec_cache_resize
+ *   out_kept    [layers, seqs, kv_heads, max_keep]: former position of each token kept, -1 behind
+ *               the last; all -1 where the sequence was left alone
+ * Apart from out_weights, what is written shares no memory with the other arrays.
+ */
+int spec_cache_evict(const sv_cache* cache, const float* weights, int length, const int32_t* keep,
+                     int max_keep, int sinks, int recent, float* out_weights, int32_t* out_lens,
+                     int32_t* out_kept, hipStream_t stream);
+
 /* Static string for a status code. */
 const char* spec_verify_status_string(int status);
 

@@ -42,3 +42,91 @@ def rotary(x, position, freq, interleaved=False, amplitude=1.0):
         out[..., c0] = amplitude * (u * cos - v * sin)
         out[..., c1] = amplitude * (u * sin + v * cos)
     return out
+
+
+# ------------------------------------------------------------------------------------- eviction
+def _books(held, refcount, b):
+    return None if held is None or refcount is None else (int(held[b]), refcount)
+
+
+def _length(lens, b, cap):
+    return min(max(int(lens[b]), 0), cap)
+
+
+def weigh(q, lse, k, table, lens, weights, seen=None, nodes=None, scale=None, decay=1.0, held=None,
+          refcount=None):
+    """weights [B, Hkv, L] of one layer after a step whose nodes' queries are q [B, N, Hq, D]; k
+    [pages, page_size, Hkv, D].  Also returns what error bounds are made of, each [B, Hkv, L]: given
+    (what the step adds) and doubt = sum over rows of weight * (scale * sum |q k| * (D + 8)
+    + 4 |lse| + 4)."""
+    B, N, Hq, D = q.shape
+    pages, page_size, Hkv, _ = k.shape
+    G = Hq // Hkv
+    scale = D ** -0.5 if scale is None else scale
+    out = np.array(weights, dtype=np.float64)
+    L = out.shape[2]
+    given, doubt = np.zeros_like(out), np.zeros_like(out)
+    for b in range(B):
+        length = min(_length(lens, b, table.shape[1] * page_size), L)
+        n = N if nodes is None else min(max(int(nodes[b]), 0), N)
+        for x, page, slot in cache_positions(table[b], page_size, pages, 0, length,
+                                             _books(held, refcount, b)):
+            for i in range(n):
+                if seen is not None and x >= int(seen[b, i]):
+                    continue
+                for h in range(Hq):
+                    if lse[b, i, h] == -np.inf:
+                        continue
+                    kk = k[page, slot, h // G]
+                    w = np.exp(scale * (q[b, i, h] @ kk) - lse[b, i, h])
+                    given[b, h // G, x] += w
+                    doubt[b, h // G, x] += w * (scale * (np.abs(q[b, i, h]) @ np.abs(kk)) * (D + 8)
+                                                + 4 * abs(lse[b, i, h]) + 4)
+        if decay == 0:
+            out[b, :, :length] = given[b, :, :length]
+        else:
+            out[b, :, :length] = decay * out[b, :, :length] + given[b, :, :length]
+    return out, given, doubt
+
+
+def evict(k, v, table, lens, weights, keep, sinks=0, recent=0, max_keep=None, held=None,
+          refcount=None):
+    """Changes k, v [layers, pages, page_size, Hkv, D]; returns (lens, kept, weights) as
+    spec_cache_evict does."""
+    layers, pages, page_size, Hkv, _ = k.shape
+    B, L = weights.shape[1], weights.shape[3]
+    max_keep = L if max_keep is None else max_keep
+    out = np.array(weights)
+    kept = np.full((layers, B, Hkv, max_keep), -1, dtype=np.int32)
+    new_lens = np.zeros(B, dtype=np.int32)
+    for b in range(B):
+        n, want = _length(lens, b, table.shape[1] * page_size), int(keep[b])
+        new_lens[b] = n
+        where = cache_positions(table[b], page_size, pages, 0, n, _books(held, refcount, b))
+        if want < 0 or want > max_keep or want < sinks + recent or n <= want or n > L:
+            continue
+        if len(where) < n:
+            continue
+        if refcount is not None and any(refcount[page] > 1 for x, page, _ in where
+                                        if x // page_size * page_size < want
+                                        and (x // page_size + 1) * page_size > sinks):
+            continue
+        new_lens[b] = want
+        for layer in range(layers):
+            for h in range(Hkv):
+                w = weights[layer, b, h]
+                middle = list(range(sinks, n - recent))
+                # largest first, NaN behind all, ties by position (Python's sort is stable)
+                middle.sort(key=lambda x: np.inf if np.isnan(w[x]) else -float(w[x]))
+                nans = [x for x in middle if np.isnan(w[x])]
+                middle = [x for x in middle if not np.isnan(w[x])] + nans
+                stay = list(range(sinks)) + sorted(middle[:want - sinks - recent]) + \
+                    list(range(n - recent, n))
+                kept[layer, b, h, :want] = stay
+                out[layer, b, h, :n] = 0
+                out[layer, b, h, :want] = w[stay]
+                for t in (k, v):
+                    rows = [t[layer, where[x][1], where[x][2], h].copy() for x in stay]
+                    for j, row in enumerate(rows):
+                        t[layer, where[j][1], where[j][2], h] = row
+    return new_lens, kept, out

@@ -51,6 +51,7 @@ EXPORTS = [
     "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append",
     "spec_cache_commit", "spec_cache_resize", "spec_cache_fork",
     "spec_rotary", "spec_rotary_append", "spec_rotary_frequencies",
+    "spec_cache_weigh", "spec_cache_evict",
     "spec_expected_tokens",
     "spec_walltime_speedup", "spec_ops_factor", "spec_optimal_gamma",
     "spec_verify_status_string",
@@ -117,6 +118,11 @@ def load(path=LIB_PATH):
     lib.spec_rotary_append.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, pcache, i32, vp, vp, i32,
                                        i32, f32, vp, vp, vp]
     lib.spec_rotary_append.restype = i32
+    lib.spec_cache_weigh.argtypes = [vp, vp, i32, i32, vp, pcache, i32, vp, vp, f32, f32, vp, i32,
+                                     vp]
+    lib.spec_cache_weigh.restype = i32
+    lib.spec_cache_evict.argtypes = [pcache, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.spec_cache_evict.restype = i32
     lib.spec_rotary_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, vp]
     lib.spec_rotary_frequencies.restype = i32
     lib.spec_expected_tokens.argtypes = [dbl, i32]
@@ -880,6 +886,72 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
                 q.shape[2], out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new_strides, N,
                 cache._ref, layer, nodes_at, freq_at, 2 * inv_freq.numel(), int(interleaved),
                 amplitude, base_at, at, raw)
+    return out
+
+
+def _weights_arg(weights, name, cache):
+    """The address of a tensor of attention weights [layers, seqs, kv_heads, length]."""
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    length = weights.shape[3] if weights.dim() == 4 else 0
+    return _arg(weights, name, cache, torch.float32,
+                (cache.layers, cache.seqs, cache.kv_heads, length))
+
+
+def spec_cache_weigh(q, lse, cache, weights, *, layer=0, seen=None, num_nodes=None, scale=None,
+                     decay=1.0, stream=None):
+    """Adds to ``weights`` [layers, seqs, kv_heads, length] float32, in one layer, the attention that
+    the nodes of q [seqs, N, q_heads, head_dim] give to every committed token, times decay what was
+    there (see include/spec_verify.h).
+
+    lse [seqs, N, q_heads] as spec_tree_attention(want_lse=True) returns it for the same q; seen
+    [seqs, N] int32: how many committed tokens each node sees (None: all; 0: the node does not
+    count).  Returns weights."""
+    q_strides = _row_strides(q, "q", cache, None)
+    B, N, H, D = q.shape
+    lse_at = _arg(lse, "lse", cache, torch.float32, (B, N, H))
+    if lse_at is None:
+        raise TypeError("lse must be a torch.Tensor")
+    weights_at = _weights_arg(weights, "weights", cache)
+    seen_at = _arg(seen, "seen", cache, torch.int32, (B, N))
+    nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (B,))
+    _cache_call(cache, "spec_cache_weigh", _lib.spec_cache_weigh, q.data_ptr(), q_strides, N, H,
+                lse_at, cache._ref, layer, seen_at, nodes_at, D ** -0.5 if scale is None else scale,
+                decay, weights_at, weights.shape[3], _raw_stream(cache, stream))
+    return weights
+
+
+def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, out=None,
+                     stream=None):
+    """Keeps keep [seqs] int32 tokens of each sequence in every layer and kv head: the first
+    ``sinks``, the last ``recent`` and, between them, those of largest weight (see
+    include/spec_verify.h).  seq_lens itself stays until spec_cache_resize(new_lens=...) stores it.
+
+    weights [layers, seqs, kv_heads, length] float32 as spec_cache_weigh makes them; max_keep bounds
+    keep (default: length).  Returns a dict: lens [seqs] int32, kept [layers, seqs, kv_heads,
+    max_keep] int32 (former positions, -1 behind the last) and weights (moved like the tokens).
+    ``out`` may hold preallocated tensors under the same keys; weights may be ``weights`` itself."""
+    weights_at = _weights_arg(weights, "weights", cache)
+    length = weights.shape[3]
+    keep_at = _arg(keep, "keep", cache, torch.int32, (cache.seqs,))
+    if keep_at is None:
+        raise TypeError("keep must be a torch.Tensor")
+    max_keep = length if max_keep is None else int(max_keep)
+    kept_shape = (cache.layers, cache.seqs, cache.kv_heads, max(0, max_keep))
+    raw = _raw_stream(cache, stream)
+    out = dict(out) if out else {}
+    if "lens" not in out:
+        out["lens"] = _new_like(keep, stream)
+    if "weights" not in out:
+        out["weights"] = _new_like(weights, stream)
+    if "kept" not in out:
+        with torch.cuda.stream(stream):  # None: the current one
+            out["kept"] = torch.empty(kept_shape, dtype=torch.int32, device=cache.device)
+    _cache_call(cache, "spec_cache_evict", _lib.spec_cache_evict, cache._ref, weights_at, length,
+                keep_at, max_keep, sinks, recent,
+                _arg(out["weights"], "out weights", cache, torch.float32, weights.shape),
+                _arg(out["lens"], "out lens", cache, torch.int32, (cache.seqs,)),
+                _arg(out["kept"], "out kept", cache, torch.int32, kept_shape), raw)
     return out
 
 

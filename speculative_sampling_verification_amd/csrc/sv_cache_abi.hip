@@ -10,18 +10,6 @@
 
 using namespace sv;
 
-namespace {
-
-bool attn_shape(const sv_cache* c, int N, int q_heads) {
-  if (N < 1 || N > kCacheMaxNodes) return false;
-  if (q_heads < 1 || q_heads > 64 * kMaxHeads || q_heads % c->kv_heads != 0) return false;
-  const int D = c->head_dim;
-  if (D != 64 && D != 96 && D != 128 && D != 256) return false;
-  return (int64_t)N * (q_heads / c->kv_heads) <= INT_MAX / 2;
-}
-
-}  // namespace
-
 extern "C" {
 
 size_t spec_tree_attention_workspace_size(const sv_cache* cache, int N, int q_heads) {

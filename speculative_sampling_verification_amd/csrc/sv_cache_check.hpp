@@ -150,6 +150,15 @@ bool outputs_apart(const Range (&r)[Count], int outs) {
   return true;
 }
 
+// Whether attention, and what follows it, takes N nodes of q_heads heads.
+inline bool attn_shape(const sv_cache* c, int N, int q_heads) {
+  if (N < 1 || N > kCacheMaxNodes) return false;
+  if (q_heads < 1 || q_heads > 64 * kMaxHeads || q_heads % c->kv_heads != 0) return false;
+  const int D = c->head_dim;
+  if (D != 64 && D != 96 && D != 128 && D != 256) return false;
+  return (int64_t)N * (q_heads / c->kv_heads) <= INT_MAX / 2;
+}
+
 inline int status_of(hipError_t e) { return e == hipSuccess ? SV_OK : SV_ERR_LAUNCH; }
 
 }  // namespace sv

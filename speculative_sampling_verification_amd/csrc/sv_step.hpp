@@ -31,4 +31,32 @@ struct RotaryArgs {
 hipError_t launch_rotary(const RotaryArgs& a, sv_dtype dt, bool interleaved, bool to_cache,
                          hipStream_t stream);
 
+struct WeighArgs {
+  CacheView c;  // one layer
+  RowView q;
+  const float* lse;      // [seqs, N, G kv_heads]
+  const int32_t* seen;   // [seqs, N] or null: every committed token
+  const int32_t* nodes;  // [seqs] or null: N each
+  int N, G;
+  FastDiv g_div;         // by G
+  float scale, decay;
+  float* w;              // [seqs, kv_heads, length]
+  int length;
+};
+
+hipError_t launch_cache_weigh(const WeighArgs& a, sv_dtype dt, hipStream_t stream);
+
+struct EvictArgs {
+  CacheView c;  // all layers
+  const float* w;  // [layers, seqs, kv_heads, length]
+  float* out_w;    // w itself, or apart from it
+  int length;
+  const int32_t* keep;  // [seqs]
+  int max_keep, sinks, recent;
+  int32_t* out_lens;  // [seqs]
+  int32_t* kept;      // [layers, seqs, kv_heads, max_keep]
+};
+
+hipError_t launch_cache_evict(const EvictArgs& a, hipStream_t stream);
+
 }  // namespace sv

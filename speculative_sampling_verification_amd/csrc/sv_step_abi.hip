@@ -11,6 +11,7 @@ using namespace sv;
 
 namespace {
 
+constexpr uint64_t kMaxWeights = (uint64_t)1 << 60;  // an array of attention weights
 constexpr double kTurn = 6.283185307179586476925;  // 2 pi
 
 bool dtype_ok(sv_dtype dt) { return dt == SV_DTYPE_F32 || dt == SV_DTYPE_BF16; }
@@ -197,6 +198,100 @@ int spec_rotary_append(const void* q, const int64_t* q_strides, int q_heads, voi
   const int bad_values = rotary_args(r, values, more, &unused);
   if (bad_values != SV_OK) return bad_values;
   return status_of(launch_rotary(a, cache->dtype, interleaved != 0, true, stream));
+}
+
+int spec_cache_weigh(const void* q, const int64_t* q_strides, int N, int q_heads, const float* lse,
+                     const sv_cache* cache, int layer, const int32_t* seen,
+                     const int32_t* num_nodes, float scale, float decay, float* weights, int length,
+                     hipStream_t stream) {
+  WeighArgs a{};
+  const int st = view_of(cache, layer, 1, &a.c);
+  if (st != SV_OK) return st;
+  const CacheView& v = a.c;
+  if (!q || !lse || !weights || !attn_shape(cache, N, q_heads)) return SV_ERR_INVALID_ARG;
+  if (length < 1 || length > kCacheMaxTokens) return SV_ERR_INVALID_ARG;
+  // the kernel multiplies scores by scale * log2(e)
+  if (!(scale > 0.0f) || !std::isfinite(scale * 1.44269504088896340736f)) return SV_ERR_INVALID_ARG;
+  if (!(decay >= 0.0f && decay <= 1.0f)) return SV_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(lse, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(seen, 4) || !aligned_to(num_nodes, 4))
+    return SV_ERR_INVALID_ARG;
+  Rows r{};
+  if (!rows_of(q_strides, v.seqs, N, q_heads, v.head_dim, v.esize, &r)) return SV_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)v.head_dim * v.esize;
+  const int64_t stride[3] = {v.page_stride, v.token_stride, v.head_stride};
+  const int64_t size[3] = {v.pages, v.page_size, v.kv_heads};
+  uint64_t bytes;
+  if (!extent_of(row, stride, size, &bytes)) return SV_ERR_INVALID_ARG;
+  const uint64_t word = sizeof(int32_t);
+  const uint64_t slab = (uint64_t)v.seqs * v.kv_heads * length;  // at most 2^53
+  if (slab > kMaxWeights / cache->layers) return SV_ERR_INVALID_ARG;
+  const Range ranges[] = {{weights + slab * layer, word * slab}, {q, r.bytes},
+                          {lse, word * v.seqs * N * q_heads}, {seen, word * v.seqs * N},
+                          {num_nodes, word * v.seqs}, {v.k, bytes},
+                          {v.table, word * v.seqs * v.width}, {v.lens, word * v.seqs},
+                          {v.held, word * v.seqs}, {v.refcount, word * v.pages}};
+  if (!outputs_apart(ranges, 1)) return SV_ERR_INVALID_ARG;
+  a.q = view_rows(q, r);
+  a.lse = lse;
+  a.seen = seen;
+  a.nodes = num_nodes;
+  a.N = N;
+  a.G = q_heads / v.kv_heads;
+  a.g_div = make_fast_div((uint32_t)a.G);
+  a.scale = scale;
+  a.decay = decay;
+  a.w = weights + slab * layer;
+  a.length = length;
+  return status_of(launch_cache_weigh(a, cache->dtype, stream));
+}
+
+int spec_cache_evict(const sv_cache* cache, const float* weights, int length, const int32_t* keep,
+                     int max_keep, int sinks, int recent, float* out_weights, int32_t* out_lens,
+                     int32_t* out_kept, hipStream_t stream) {
+  EvictArgs a{};
+  const int st = view_of(cache, 0, cache ? cache->layers : 0, &a.c);
+  if (st != SV_OK) return st;
+  const CacheView& v = a.c;
+  if (!values_apart(cache) || !weights || !keep || !out_weights || !out_lens || !out_kept)
+    return SV_ERR_INVALID_ARG;
+  if (length < 1 || length > kCacheMaxTokens || max_keep < 1 || max_keep > length || sinks < 0 ||
+      recent < 0)
+    return SV_ERR_INVALID_ARG;
+  if (!aligned_to(weights, 4) || !aligned_to(keep, 4) || !aligned_to(out_weights, 4) ||
+      !aligned_to(out_lens, 4) || !aligned_to(out_kept, 4))
+    return SV_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)v.head_dim * v.esize;
+  const int64_t stride[4] = {v.layer_stride, v.page_stride, v.token_stride, v.head_stride};
+  const int64_t size[4] = {v.layers, v.pages, v.page_size, v.kv_heads};
+  uint64_t bytes, groups;
+  if (!extent_of(row, stride, size, &bytes)) return SV_ERR_INVALID_ARG;
+  groups = (uint64_t)v.layers * v.seqs * v.kv_heads;  // at most 2^36
+  if (groups > kMaxWeights / length) return SV_ERR_INVALID_ARG;
+  const uint64_t word = sizeof(int32_t), all = word * groups * length;
+  const bool in_place = out_weights == weights;
+  const Range ranges[] = {{out_weights, all}, {out_lens, word * v.seqs},
+                          {out_kept, word * groups * max_keep}, {v.k, bytes}, {keep, word * v.seqs},
+                          {in_place ? nullptr : weights, all},
+                          {v.table, word * v.seqs * v.width}, {v.lens, word * v.seqs},
+                          {v.held, word * v.seqs}, {v.refcount, word * v.pages}};
+  const Range values[] = {{v.v, bytes}, {out_weights, all}, {out_lens, word * v.seqs},
+                          {out_kept, word * groups * max_keep}, {keep, word * v.seqs},
+                          {weights, all}, {v.table, word * v.seqs * v.width},
+                          {v.lens, word * v.seqs}, {v.held, word * v.seqs},
+                          {v.refcount, word * v.pages}};
+  // keys and values may be parts of one tensor, whose rows lie apart
+  if (!outputs_apart(ranges, 4) || !outputs_apart(values, 1)) return SV_ERR_INVALID_ARG;
+  a.w = weights;
+  a.out_w = out_weights;
+  a.length = length;
+  a.keep = keep;
+  a.max_keep = max_keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.out_lens = out_lens;
+  a.kept = out_kept;
+  return status_of(launch_cache_evict(a, stream));
 }
 
 int spec_rotary_frequencies(int rot_dim, double theta, int scaling, double factor,

@@ -123,3 +123,94 @@ def test_binding_names_bad_tensors(svl):
                      cuda_stream=0, device=torch.device("cuda", 1)))):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+W = 13 * 64 * D0
+LSE, SEEN, KEEP, LENS, KEPT, OW = ((14 + i) * 64 * D0 for i in range(6))
+
+
+def weigh(svl, c=None, **over):
+    a = dict(q=Q, qs=None, N=5, hq=4, lse=LSE, cache=ctypes.byref(c if c is not None else cache(svl)),
+             layer=1, seen=SEEN, nodes=N, scale=0.125, decay=1.0, w=W, length=70)
+    a.update(over)
+    return svl.lib().spec_cache_weigh(*a.values(), None)
+
+
+def evict(svl, c=None, **over):
+    a = dict(cache=ctypes.byref(c if c is not None else cache(svl)), w=W, length=70, keep=KEEP,
+             max_keep=40, sinks=2, recent=3, ow=OW, lens=LENS, kept=KEPT)
+    a.update(over)
+    return svl.lib().spec_cache_evict(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHES, ids=[str(b[0]) for b in BAD_CACHES])
+def test_weigh_and_evict_refuse_a_bad_cache(svl, over, status):
+    assert weigh(svl, cache(svl, **over)) == status
+    assert evict(svl, cache(svl, **over)) == status
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=None), dict(lse=None), dict(w=None), dict(cache=None), dict(layer=-1), dict(layer=2),
+    dict(N=0), dict(N=2049), dict(hq=0), dict(hq=3), dict(scale=0.0), dict(scale=float("nan")),
+    dict(scale=3e38), dict(decay=-0.1), dict(decay=1.1), dict(decay=float("nan")), dict(length=0),
+    dict(length=2 ** 30 + 1), dict(q=Q + 4), dict(lse=LSE + 2), dict(seen=SEEN + 1),
+    dict(nodes=N + 2), dict(w=W + 2), dict(qs=strides(1280, 256, 60)), dict(qs=strides(-16, 256, 64)),
+    # the layer's weights (layer 1: 3 * 2 * 70 floats in) share no memory with what is read
+    dict(w=Q - 4 * 3 * 2 * 70), dict(w=LSE - 4 * 3 * 2 * 70), dict(w=SEEN - 4 * 3 * 2 * 70),
+    dict(w=N - 4 * 3 * 2 * 70), dict(w=D0 + 2 * 10 * 16 * 128 - 4 * 3 * 2 * 70)], ids=str)
+def test_weigh_arguments(svl, over):
+    assert weigh(svl, **over) == INVALID
+
+
+def test_weigh_takes_the_heads_that_attention_takes(svl):
+    for dim in (32, 80, 512):
+        c = cache(svl, head_dim=dim, head_stride=dim, token_stride=2 * dim, page_stride=32 * dim,
+                  layer_stride=320 * dim)
+        assert weigh(svl, c) == INVALID
+
+
+@pytest.mark.parametrize("over", [
+    dict(w=None), dict(keep=None), dict(ow=None), dict(lens=None), dict(kept=None), dict(cache=None),
+    dict(length=0), dict(length=2 ** 30 + 1), dict(max_keep=0), dict(max_keep=71), dict(sinks=-1),
+    dict(recent=-1), dict(w=W + 1), dict(keep=KEEP + 2), dict(ow=OW + 2), dict(lens=LENS + 2),
+    dict(kept=KEPT + 2), dict(ow=W + 4), dict(ow=KEPT), dict(lens=KEEP + 8), dict(lens=KEPT),
+    dict(kept=KEEP - 4), dict(kept=W), dict(ow=D0), dict(kept=2 * D0 - 4), dict(keep=D0 + 4),
+    dict(w=2 * D0)], ids=str)
+def test_evict_arguments(svl, over):
+    assert evict(svl, **over) == INVALID
+
+
+def test_evict_writes_no_shared_rows_and_no_huge_arrays(svl):
+    assert evict(svl, cache(svl, v=D0)) == INVALID
+    huge = cache(svl, layers=8192, kv_heads=1024, seqs=8192, pages=1, page_size=1, token_stride=0,
+                 page_stride=0, head_stride=64, layer_stride=65536)
+    assert evict(svl, huge, length=2 ** 30, max_keep=1) == INVALID
+    assert weigh(svl, huge, hq=1024, length=2 ** 30) == INVALID
+    # lengths over seq_lens: spec_cache_resize stores them
+    c = cache(svl, seq_lens=LENS, v=4096 * D0)
+    assert evict(svl, c) == INVALID
+
+
+def test_binding_names_bad_weights(svl):
+    k, i = torch.zeros((2, 6, 4, 2, 64)), torch.zeros(3, dtype=torch.int32)
+    c = svl.PagedCache(k, k.clone(), torch.zeros((3, 5), dtype=torch.int32), i)
+    q, lse = torch.zeros((3, 4, 4, 64)), torch.zeros((3, 4, 4))
+    w = torch.zeros((2, 3, 2, 20))
+    for bad in (w[:1], w[..., 0], w.double(), None, w.transpose(1, 2), w[..., ::2]):
+        with pytest.raises((TypeError, ValueError)):
+            svl.spec_cache_weigh(q, lse, c, bad)
+        with pytest.raises((TypeError, ValueError)):
+            svl.spec_cache_evict(c, bad, i)
+    for call in (lambda: svl.spec_cache_weigh(q, lse[:, :3], c, w),
+                 lambda: svl.spec_cache_weigh(q, None, c, w),
+                 lambda: svl.spec_cache_weigh(q, lse.double(), c, w),
+                 lambda: svl.spec_cache_weigh(q.bfloat16(), lse, c, w),
+                 lambda: svl.spec_cache_weigh(q, lse, c, w, seen=i),
+                 lambda: svl.spec_cache_weigh(q, lse, c, w),
+                 lambda: svl.spec_cache_evict(c, w, i.long()),
+                 lambda: svl.spec_cache_evict(c, w, None),
+                 lambda: svl.spec_cache_evict(c, w, i, out={"weights": w[..., :10]}),
+                 lambda: svl.spec_cache_evict(c, w, i, out={"kept": i}),
+                 lambda: svl.spec_cache_evict(c, w, i)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
