@@ -447,6 +447,35 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* ds
                     int32_t* out_ok, hipStream_t stream);
 
 /*
+ * Log probabilities of given tokens under softmax(logits / temperature), with the entropy of the
+ * whole distribution, the tokens' ranks and the most probable alternatives: what a server reports
+ * beside the tokens that spec_verify, spec_verify_tree or spec_sample emitted.  The logits are read
+ * once.
+ *   logits      [num_rows, V] of dtype
+ *   rows        [R] int32 or NULL (row r; then R == num_rows): the row that token r is looked up in,
+ *               as a tree's nodes in their parents' rows; rows may come up again
+ *   tokens      [R] int32 or NULL (then out_logprob and out_rank are NULL too)
+ *   temperature > 0, finite, log2(e) / temperature finite in fp32
+ *   top_n       0..64 alternatives
+ *   out_logprob [R] float; out_rank [R] int32 or NULL: how many tokens come first in the order
+ *               (logit descending, index ascending), 0 for the argmax
+ *   out_entropy [R] float or NULL, in nats
+ *   out_top_tokens [R, top_n] int32, out_top_logprobs [R, top_n] float: the first of that order
+ *               (NULL if top_n is 0).  A logit of -inf is no alternative: where there are fewer than
+ *               top_n others, the rest holds -1 and -inf
+ * A token outside [0, V) has log probability -inf and rank -1.  A row outside [0, num_rows), or
+ * without a finite logit, has no distribution: -inf, entropy 0, no alternatives.  Sums are in fp32
+ * a thread and joined in 64 bits.  Outputs and workspace share no memory with each other or the
+ * inputs.
+ */
+size_t spec_token_logprobs_workspace_size(int R, int V, sv_dtype dtype, int top_n);
+int spec_token_logprobs(const void* logits, sv_dtype dtype, int num_rows, int V,
+                        const int32_t* rows, const int32_t* tokens, int R, float temperature,
+                        int top_n, float* out_logprob, int32_t* out_rank, float* out_entropy,
+                        int32_t* out_top_tokens, float* out_top_logprobs, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/*
  * ---------------------------------------------------------------------------------------------
  * Rotary positions, before the cache is written and attended to.
  *

@@ -130,3 +130,41 @@ def evict(k, v, table, lens, weights, keep, sinks=0, recent=0, max_keep=None, he
                     for j, row in enumerate(rows):
                         t[layer, where[j][1], where[j][2], h] = row
     return new_lens, kept, out
+
+
+# --------------------------------------------------------------------- token log probabilities
+def token_logprobs(logits, tokens=None, rows=None, temperature=1.0, top_n=0):
+    """logits [num_rows, V] float64, tokens [R], rows [R]: a dict as spec_token_logprobs returns it,
+    everything wanted, and what error bounds are made of, [R] each: spread = |x_t - x_max|, mean and
+    square = the means of |x - x_max| and its square under the distribution (x = logits / T)."""
+    num_rows, V = logits.shape
+    R = num_rows if rows is None else len(rows)
+    out = dict(logprob=np.full(R, -np.inf), rank=np.full(R, -1, dtype=np.int64),
+               entropy=np.zeros(R), top_tokens=np.full((R, top_n), -1, dtype=np.int64),
+               top_logprobs=np.full((R, top_n), -np.inf), spread=np.zeros(R), mean=np.zeros(R),
+               square=np.zeros(R))
+    for r in range(R):
+        row = r if rows is None else int(rows[r])
+        if not 0 <= row < num_rows:
+            continue
+        z = np.asarray(logits[row], dtype=np.float64)
+        t = -1 if tokens is None else int(tokens[r])
+        if 0 <= t < V:
+            out["rank"][r] = (z > z[t]).sum() + (z[:t] == z[t]).sum()
+        some = np.flatnonzero(z > -np.inf)
+        if len(some) == 0:
+            continue
+        x = (z - z.max()) / temperature
+        e = np.exp(x)
+        log_total = np.log(e.sum())
+        p = e / e.sum()
+        far = np.where(p > 0, -x, 0.0)
+        if 0 <= t < V:
+            out["logprob"][r] = x[t] - log_total
+            out["spread"][r] = -x[t] if z[t] > -np.inf else 0.0
+        out["entropy"][r] = log_total + (p * far).sum()
+        out["mean"][r], out["square"][r] = (p * far).sum(), (p * far ** 2).sum()
+        first = some[np.lexsort((some, -z[some]))][:top_n]
+        out["top_tokens"][r, :len(first)] = first
+        out["top_logprobs"][r, :len(first)] = x[first] - log_total
+    return out

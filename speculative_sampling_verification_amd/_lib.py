@@ -9,6 +9,7 @@ missing the import fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -52,6 +53,7 @@ EXPORTS = [
     "spec_cache_commit", "spec_cache_resize", "spec_cache_fork",
     "spec_rotary", "spec_rotary_append", "spec_rotary_frequencies",
     "spec_cache_weigh", "spec_cache_evict",
+    "spec_token_logprobs_workspace_size", "spec_token_logprobs",
     "spec_expected_tokens",
     "spec_walltime_speedup", "spec_ops_factor", "spec_optimal_gamma",
     "spec_verify_status_string",
@@ -118,6 +120,11 @@ def load(path=LIB_PATH):
     lib.spec_rotary_append.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, pcache, i32, vp, vp, i32,
                                        i32, f32, vp, vp, vp]
     lib.spec_rotary_append.restype = i32
+    lib.spec_token_logprobs_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.spec_token_logprobs_workspace_size.restype = sz
+    lib.spec_token_logprobs.argtypes = [vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp,
+                                        vp, sz, vp]
+    lib.spec_token_logprobs.restype = i32
     lib.spec_cache_weigh.argtypes = [vp, vp, i32, i32, vp, pcache, i32, vp, vp, f32, f32, vp, i32,
                                      vp]
     lib.spec_cache_weigh.restype = i32
@@ -952,6 +959,75 @@ def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, 
                 _arg(out["weights"], "out weights", cache, torch.float32, weights.shape),
                 _arg(out["lens"], "out lens", cache, torch.int32, (cache.seqs,)),
                 _arg(out["kept"], "out kept", cache, torch.int32, kept_shape), raw)
+    return out
+
+
+def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_n=0,
+                        want_rank=False, want_entropy=False, out=None, stream=None):
+    """Log probabilities of tokens under softmax(logits / temperature) (see include/spec_verify.h).
+
+    logits [..., V] (bf16 or fp32), tokens int32 with the leading shape, as spec_verify(...)["tokens"]
+    fits its target logits (-1 where nothing was emitted).  ``rows`` int32, of any shape, looks the
+    tokens (of that shape) up in those rows of logits viewed as [-1, V].  Returns a dict: logprob,
+    if wanted rank and entropy (float32), and with top_n > 0 top_tokens and top_logprobs [..., top_n].
+    Without tokens only what does not need them.  ``out`` may hold preallocated tensors under the
+    same keys."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dim() < 1:
+        raise ValueError("logits must be [..., V]")
+    if stream is not None:
+        _raw_stream(_Place(logits.device), stream)  # refuses a stream of another device
+        with torch.cuda.stream(stream):
+            return spec_token_logprobs(logits, tokens, rows=rows, temperature=temperature,
+                                       top_n=top_n, want_rank=want_rank,
+                                       want_entropy=want_entropy, out=out)
+    dev, V = logits.device, logits.shape[-1]
+    place = _Place(dev)
+    _need(logits, "logits", dev)
+    dt = _dtype_code(logits)
+    if rows is not None and not isinstance(rows, torch.Tensor):
+        raise TypeError("rows must be a torch.Tensor")
+    shape = tuple(logits.shape[:-1] if rows is None else rows.shape)
+    rows_at = _arg(rows, "rows", place, torch.int32, shape)
+    tokens_at = _arg(tokens, "tokens", place, torch.int32, shape)
+    if want_rank and tokens is None:
+        raise ValueError("ranks need tokens")
+    R, top_n = math.prod(shape), int(top_n)
+    if V < 1 or max(R, logits.numel() // V) >= 2**31:
+        raise ValueError(f"logits {tuple(logits.shape)} for {R} tokens is out of range")
+    kinds = {}
+    if tokens is not None:
+        kinds["logprob"] = (torch.float32, shape)
+    if want_rank:
+        kinds["rank"] = (torch.int32, shape)
+    if want_entropy:
+        kinds["entropy"] = (torch.float32, shape)
+    if top_n > 0:
+        kinds["top_tokens"] = (torch.int32, shape + (top_n,))
+        kinds["top_logprobs"] = (torch.float32, shape + (top_n,))
+    out = dict(out) if out else {}
+    for name in out:
+        if name not in kinds:
+            raise ValueError(f"out holds {name}, which is not asked for")
+    raw = _raw_stream(place, None)
+    need = _lib.spec_token_logprobs_workspace_size(R, V, dt, top_n)
+    if need == 0:
+        raise SpecVerifyError("spec_token_logprobs_workspace_size", 1)
+    for name, (dtype, dims) in kinds.items():
+        if name not in out:
+            out[name] = torch.empty(dims, dtype=dtype, device=dev)
+    at = {name: _arg(out[name], f"out {name}", place, *kinds[name]) for name in kinds}
+    if _capturing(place):  # the graph's own: graphs may run side by side
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        ws = _workspaces.get((dev.type, dev.index, raw))
+        if ws is None or ws.numel() < need:
+            ws = workspace(dev, need)
+    _cache_call(place, "spec_token_logprobs", _lib.spec_token_logprobs, logits.data_ptr(), dt,
+                logits.numel() // V, V, rows_at, tokens_at, R, temperature, top_n,
+                at.get("logprob"), at.get("rank"), at.get("entropy"), at.get("top_tokens"),
+                at.get("top_logprobs"), ws.data_ptr(), ws.numel(), raw)
     return out
 
 

@@ -9,7 +9,8 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 SOURCES = ["sv_kernels.hip", "sv_rest.hip", "sv_rng.hip", "sv_tree_attn.hip", "sv_cache.hip",
            "sv_abi.hip", "sv_cache_abi.hip", "sv_rotary.hip",
-           "sv_weigh.hip", "sv_evict.hip", "sv_step_abi.hip"]
+           "sv_weigh.hip", "sv_evict.hip", "sv_step_abi.hip", "sv_logprob.hip",
+           "sv_logprob_abi.hip"]
 LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 

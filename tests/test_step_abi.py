@@ -214,3 +214,54 @@ def test_binding_names_bad_weights(svl):
                  lambda: svl.spec_cache_evict(c, w, i)):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def logprobs(svl, **over):
+    a = dict(logits=Q, dtype=1, num_rows=6, V=100000, rows=None, tokens=K, R=6, T=1.0, n=5, lp=KO,
+             rank=V, ent=F, top=B, toplp=P, ws=W, ws_bytes=1 << 30)
+    a.update(over)
+    return svl.lib().spec_token_logprobs(*a.values(), None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(logits=None), dict(num_rows=0), dict(V=0), dict(R=0), dict(R=5), dict(rows=N, R=0),
+    dict(T=0.0), dict(T=-1.0), dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-39), dict(n=-1),
+    dict(n=65), dict(tokens=None), dict(lp=None), dict(n=0), dict(top=None), dict(toplp=None),
+    dict(n=0, top=None, toplp=None, tokens=None, lp=None, rank=None, ent=None),
+    dict(tokens=None, lp=None), dict(logits=Q + 1), dict(dtype=0, logits=Q + 2), dict(tokens=K + 2),
+    dict(rows=N + 1), dict(lp=KO + 2), dict(rank=V + 1), dict(ent=F + 2), dict(top=B + 2),
+    dict(toplp=P + 2), dict(ws=W + 8), dict(lp=Q), dict(rank=KO + 20), dict(ent=KO), dict(top=P - 100),
+    dict(toplp=Q + 6 * 100000 * 2 - 4), dict(ws=Q), dict(lp=K - 4), dict(rows=N, R=6, lp=N),
+    dict(ws=KO)], ids=str)
+def test_logprob_arguments(svl, over):
+    assert logprobs(svl, **over) == INVALID
+
+
+def test_logprob_workspace(svl):
+    size = svl.lib().spec_token_logprobs_workspace_size
+    assert logprobs(svl, dtype=3) == DTYPE
+    need = size(6, 100000, 1, 5)
+    assert need > 16 and logprobs(svl, ws_bytes=need - 1) == 3 and logprobs(svl, ws=None) == 3
+    for bad in ((0, 10, 1, 0), (1, 0, 1, 0), (1, 10, 2, 0), (1, 10, 1, -1), (1, 10, 1, 65)):
+        assert size(*bad) == 0
+    for R, V, n in ((1, 1, 0), (2 ** 31 - 1, 2 ** 31 - 1, 64), (1, 2 ** 31 - 1, 64), (511, 128256, 20)):
+        for dt in (0, 1):
+            assert 16 <= size(R, V, dt, n) < 2 ** 24 + R * 64
+
+
+def test_binding_names_bad_logits(svl):
+    z, t = torch.zeros((3, 4, 50)), torch.zeros((3, 4), dtype=torch.int32)
+    for call in (lambda: svl.spec_token_logprobs(None, t), lambda: svl.spec_token_logprobs(z[..., ::2], t),
+                 lambda: svl.spec_token_logprobs(z.double(), t), lambda: svl.spec_token_logprobs(z, t[:2]),
+                 lambda: svl.spec_token_logprobs(z, t.long()), lambda: svl.spec_token_logprobs(z, 3),
+                 lambda: svl.spec_token_logprobs(z, want_rank=True, top_n=2),
+                 lambda: svl.spec_token_logprobs(z, t, rows=t[0]),
+                 lambda: svl.spec_token_logprobs(z, t, rows=[1]),
+                 lambda: svl.spec_token_logprobs(z, t, out={"entropy": z[..., 0]}),
+                 lambda: svl.spec_token_logprobs(z[..., :0], t),
+                 lambda: svl.spec_token_logprobs(torch.tensor(1.0), None, top_n=1),
+                 lambda: svl.spec_token_logprobs(z, t),  # host memory
+                 lambda: svl.spec_token_logprobs(z, t, stream=SimpleNamespace(
+                     cuda_stream=0, device=torch.device("cuda", 1)))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
