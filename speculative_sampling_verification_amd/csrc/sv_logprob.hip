@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_logprob.hpp"
 
@@ -25,12 +26,16 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVecs = 8;              // vectors a thread and tile
-constexpr int kTile = kThreads * kVecs;
-constexpr int kList = 128;            // vectors a wave keeps
+constexpr int vecs_of(bool bf16) { return bf16 ? 4 : 8; }  // a thread and tile: 32 logits
+constexpr int kSpare = 48;            // vectors a wave keeps beyond n until it cuts its list
+constexpr int kList = kLogprobMaxTop + kSpare + 64 * 8;
 constexpr int kMaxParts = 64;         // of a row: one a lane of the join
 constexpr int64_t kMaxBlocks = 1 << 20;
 constexpr double kLn2 = 0.69314718055994530942;
+
+// Every lambda of the kernel is part of its loop: the captures of one that the compiler calls
+// instead are kept in memory.
+#define SV_INLINE __attribute__((always_inline))
 
 // Order-preserving key of a logit (the two zeros alike) and its inverse.
 __device__ __forceinline__ uint32_t key_of(float z) {
@@ -45,15 +50,24 @@ template <bool BF16>
 struct Row {
   static constexpr int kES = BF16 ? 2 : 4;
   static constexpr int kPer = 16 / kES;  // elements a vector
-  const char* at;   // aligned start: vector 0 may begin before the row
-  int phase;        // elements of vector 0 that lie before the row
-  int V, vecs;
+  const char* at;    // aligned start: vector 0 may begin before the row
+  int phase;         // elements of vector 0 that lie before the row
+  int V;
+  int first, last;   // vectors first .. last - 1 lie in the row as a whole
+  int head;          // elements of the row before them; behind them: from tail() on
 
   __device__ __forceinline__ Row(const char* row, int V_) : V(V_) {
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
     at = row - off;
     phase = (int)off / kES;
-    vecs = (int)(((int64_t)phase + V + kPer - 1) / kPer);
+    first = phase ? 1 : 0;
+    last = (int)(((int64_t)phase + V) / kPer);
+    head = !phase ? 0 : V < kPer - phase ? V : kPer - phase;
+    if (last < first) last = first;
+  }
+  __device__ __forceinline__ int64_t tail() const {
+    const int64_t i = (int64_t)last * kPer - phase;
+    return i > head ? i : head;
   }
   __device__ __forceinline__ float load(int64_t i) const {
     const char* p = at + (i + phase) * kES;
@@ -68,6 +82,12 @@ struct Row {
   }
 };
 
+// The same logits to the compiler's eyes new ones: decoded again instead of kept decoded.
+__device__ __forceinline__ u32x4 anew(u32x4 v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 template <class T, class Op>
 __device__ __forceinline__ T wave_all(T x, Op op) {
 #pragma unroll
@@ -75,10 +95,11 @@ __device__ __forceinline__ T wave_all(T x, Op op) {
   return x;
 }
 
-// The n-th largest of the wave's keys, one or two a lane (largest k with n keys >= k).
+// The n-th largest of the wave's keys, several a lane (the largest k with n keys >= k).
 template <int Keys>
 __device__ __forceinline__ uint32_t nth_key(const uint32_t (&k)[Keys], int n) {
   uint32_t t = 0;
+#pragma unroll 1
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t c = t | 1u << bit;
     int count = 0;
@@ -93,6 +114,7 @@ struct Lds {
   float val[kWaves][kList];
   uint32_t pos[kWaves][kList];
   unsigned long long keys[kWaves][kLogprobMaxTop];
+  unsigned long long edge[2];  // the row's first and last vector where they are not whole
   unsigned long long picked[kLogprobMaxTop];
   unsigned long long elems[kLogprobMaxTop * 8];
   LogprobPart stat[kWaves];
@@ -100,7 +122,7 @@ struct Lds {
   int found;
 };
 
-// Kept vectors of a wave, in order of position.
+// Vectors that a wave keeps, in order of position.
 struct Kept {
   float* val;
   uint32_t* pos;
@@ -108,58 +130,48 @@ struct Kept {
   float tau;  // vectors count only above it
 
   // keeps the n first by (value, position)
-  __device__ __forceinline__ void cut(int n) {
+  template <int Keys>
+  __device__ __forceinline__ void cut_some(int n) {
     const int lane = threadIdx.x & 63;
-    __builtin_amdgcn_wave_barrier();
-    uint32_t k[2], p[2];
-    float v[2];
+    uint32_t k[Keys], p[Keys];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Keys; ++i) {
       const int at = lane + 64 * i;
-      v[i] = at < count ? val[at] : 0.0f;
+      k[i] = at < count ? key_of(val[at]) : 0u;
       p[i] = at < count ? pos[at] : 0u;
-      k[i] = at < count ? key_of(v[i]) : 0u;
     }
     const uint32_t t = nth_key(k, n);
     const unsigned long long below = (1ull << lane) - 1;
-    unsigned long long level[2];
     int quota = n;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      quota -= __popcll(__ballot(k[i] > t));
-      level[i] = __ballot(k[i] == t);
-    }
-    const bool take0 = k[0] > t || (k[0] == t && __popcll(level[0] & below) < quota);
-    const bool take1 =
-        k[1] > t || (k[1] == t && __popcll(level[0]) + __popcll(level[1] & below) < quota);
-    const unsigned long long m0 = __ballot(take0), m1 = __ballot(take1);
+    for (int i = 0; i < Keys; ++i) quota -= __popcll(__ballot(k[i] > t));
     __builtin_amdgcn_wave_barrier();
-    if (take0) {
-      val[__popcll(m0 & below)] = v[0];
-      pos[__popcll(m0 & below)] = p[0];
-    }
-    if (take1) {
-      val[__popcll(m0) + __popcll(m1 & below)] = v[1];
-      pos[__popcll(m0) + __popcll(m1 & below)] = p[1];
+    int at = 0, level_before = 0;
+#pragma unroll
+    for (int i = 0; i < Keys; ++i) {
+      const unsigned long long level = __ballot(k[i] == t);
+      const bool take = k[i] > t || (k[i] == t && level_before + __popcll(level & below) < quota);
+      const unsigned long long m = __ballot(take);
+      if (take) {
+        val[at + __popcll(m & below)] = of_key(k[i]);
+        pos[at + __popcll(m & below)] = p[i];
+      }
+      at += __popcll(m);
+      level_before += __popcll(level);
     }
     __builtin_amdgcn_wave_barrier();
     count = n;
     tau = of_key(t);
   }
+  __device__ __forceinline__ void cut(int n) {
+    __builtin_amdgcn_wave_barrier();
+    if (count <= 128) cut_some<2>(n);
+    else cut_some<(kList + 63) / 64>(n);
+  }
 
-  __device__ __forceinline__ void add(bool hit, float v, uint32_t p, int n) {
+  __device__ __forceinline__ void add(bool hit, float v, uint32_t p) {
     const unsigned long long m = __ballot(hit);
     if (!m) return;
-    if (count + __popcll(m) > kList) {
-      cut(n);
-      // some may not count any more
-      add_all(hit && v > tau, v, p);
-      return;
-    }
-    add_all(hit, v, p);
-  }
-  __device__ __forceinline__ void add_all(bool hit, float v, uint32_t p) {
-    const unsigned long long m = __ballot(hit);
     const int at = count + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1));
     if (hit) {
       val[at] = v;
@@ -246,211 +258,237 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 }
 
 template <bool BF16, bool Entropy, bool Rank, bool Top>
-__global__ __launch_bounds__(kThreads) void k_logprob(LogprobArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
   using R = Row<BF16>;
-  constexpr int kPer = R::kPer;
+  constexpr int kPer = R::kPer, kVecs = vecs_of(BF16), kTile = kThreads * kVecs;
   __shared__ Lds s;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t units = (int64_t)a.R * a.parts;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int r = (int)(unit / a.parts), part = (int)(unit - (int64_t)r * a.parts);
-    const int at = row_index(a, r);
-    const int token = a.tokens ? a.tokens[r] : -1;
-    if (at < 0) {  // no such row
-      if (part == 0) finish<BF16>(a, s, nullptr, r, LogprobPart{}, -1);
-      continue;
+  const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int r = (int)(unit / a.parts), part = (int)(unit - (int64_t)r * a.parts);
+  if (r >= a.R) return;
+  const int at = row_index(a, r);
+  const int token = a.tokens ? a.tokens[r] : -1;
+  if (at < 0) {  // no such row
+    if (part == 0) finish<BF16>(a, s, nullptr, r, LogprobPart{}, -1);
+    return;
+  }
+  const R row(a.logits + (int64_t)at * a.V * R::kES, a.V);
+  const int v0 = row.first + part * a.part_vecs;
+  const int v1 = row.last - v0 < a.part_vecs ? row.last : v0 + a.part_vecs;
+  // a vector's elements come first if they are >= `level` (it lies before the token's) or
+  // >= `beyond`, the next number; those level with the token in its own vector are counted below
+  const bool ranked = Rank && token >= 0 && token < a.V;
+  const float level = ranked ? row.load(token) : INFINITY;
+  const float beyond = ranked ? of_key(key_of(level) + 1) : INFINITY;
+  const int token_vec = ranked ? (int)(((int64_t)row.phase + token) / kPer) : 0;
+
+  float sum = 0.0f, sum_x = 0.0f, top = -INFINITY;
+  float m0 = -INFINITY, k = 0.0f;  // the shift as a logit (wave-wide), and as c m0
+  bool far = false;                // |c m0| is 2^22 or more, and its rounding (then over
+                                   // 1/8) shows in x - k: differences of logits first
+  int above = 0;
+  Kept kept{s.val[wave], s.pos[wave], 0, -INFINITY};
+
+  bool clamp = false;  // logits of -inf, or far: pass<true>
+
+  // the shift follows a maximum that lies 2^24 above it
+  auto raise = [&](float most) SV_INLINE {
+    if (!__any(most > m0 && (m0 == -INFINITY || (most - m0) * a.c > 24.0f))) return;
+    const float m = wave_all(most, [](float x, float y) { return fmaxf(x, y); });
+    const float kn = a.c * m;
+    const bool far_n = !(fabsf(kn) < 4194304.0f);
+    if (m0 > -INFINITY) {
+      const float d = far || far_n ? (m0 - m) * a.c : k - kn;
+      const float f = exp2f(d);
+      sum_x = f > 0.0f ? f * fmaf(d, sum, sum_x) : 0.0f;
+      sum *= f;
     }
-    const R row(a.logits + (int64_t)at * a.V * R::kES, a.V);
-    const int v0 = part * a.part_vecs;
-    const int v1 = v0 + a.part_vecs < row.vecs ? v0 + a.part_vecs : row.vecs;
-    const bool ranked = Rank && token >= 0 && token < a.V;
-    const float zt = ranked ? row.load(token) : 0.0f;
-
-    float sum = 0.0f, sum_x = 0.0f, top = -INFINITY;
-    float m0 = -INFINITY, k = 0.0f;  // the shift as a logit (wave-wide), and as c m0
-    bool far = false;                // |c m0| is 2^22 or more, and its rounding (then over
-                                     // 1/8) shows in x - k: differences of logits first
-    int above = 0;
-    Kept kept{s.val[wave], s.pos[wave], 0, -INFINITY};
-    bool first = true;
-
-    auto load_tile = [&](int t, u32x4 (&v)[kVecs]) {
-      if (t >= v1) return;
-      const bool whole = (t > 0 || row.phase == 0) && t + kTile <= v1 &&
-                         ((int64_t)(t + kTile)) * kPer - row.phase <= a.V;
-      if (whole) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(row.at) + t + tid;
+    m0 = m;
+    k = kn;
+    far = far_n;
+    clamp |= far;
+  };
+  auto vec_max = [&](const u32x4& v) SV_INLINE {
+    float m = R::elem(v, 0);
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) v[u] = p[u * kThreads];
-        return;
+    for (int e = 1; e < kPer; ++e) m = fmaxf(m, R::elem(v, e));
+    return m;
+  };
+
+  // behind the last vector: that one again
+  auto load_tile = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
+    if (t >= v1) return;
+    const u32x4* p = reinterpret_cast<const u32x4*>(row.at);
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int j = t + u * kThreads + tid;
+      v[u] = p[j < v1 ? j : v1 - 1];
+    }
+  };
+
+  // Adds a tile's logits at the shift as it is; false, with nothing added, if that does not do.
+  // Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and far shifts are
+  // subtracted first.
+  auto pass = [&](auto clamped, int t, const u32x4 (&v)[kVecs], float (&vm)[kVecs],
+                  float& most) SV_INLINE {
+    constexpr bool Clamp = decltype(clamped)::value;
+    const float z0 = Clamp && far ? m0 : 0.0f, k0 = Clamp && far ? 0.0f : k;
+    float f = 0.0f, fx = 0.0f;
+    int n = 0;
+    most = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int j = t + u * kThreads + tid;
+      const float th = !Rank ? 0.0f : j >= v1 ? INFINITY : j < token_vec ? level : beyond;
+      const u32x4 x4 = Clamp ? anew(v[u]) : v[u];
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const float z = R::elem(x4, e);
+        float x = fmaf(Clamp ? z - z0 : z, a.c, -k0);
+        if constexpr (Clamp) x = fmaxf(x, -200.0f);
+        const float w = __builtin_amdgcn_exp2f(x);
+        m = fmaxf(m, z);
+        f += w;
+        if constexpr (Entropy) fx = fmaf(w, x, fx);
+        if constexpr (Rank) n += __popcll(__ballot(z >= th));
       }
+      vm[u] = j < v1 ? m : -INFINITY;
+      most = fmaxf(most, vm[u]);
+      __builtin_amdgcn_sched_barrier(0);  // few decoded logits at a time
+    }
+    if constexpr (!Clamp) {
+      const bool odd = Entropy && fx != fx;
+      clamp = __any(odd);
+      if (clamp || __any((most - m0) * a.c > 24.0f)) return false;
+    }
+    sum += f;
+    sum_x += fx;
+    above += n;
+    return true;
+  };
+  auto step = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
+    float vm[kVecs], most;
+    if (t + kTile > v1) {
+      const uint32_t none = BF16 ? 0xF149F149u : 0xF149F2CAu;  // about -1e30, of no weight
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+        if (t + u * kThreads + tid >= v1) v[u] = u32x4{none, none, none, none};
+    }
+    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(anew(v[0])) : -INFINITY);
+    if (clamp || !pass(std::false_type{}, t, v, vm, most)) {
+      float m = -INFINITY;
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) {
-        const int j = t + u * kThreads + tid;
-        const int64_t e0 = (int64_t)j * kPer - row.phase;
-        const uint32_t fill = BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
-        v[u] = u32x4{fill, fill, fill, fill};
-        if (j >= v1) continue;
-        if (e0 >= 0 && e0 + kPer <= a.V) {
-          v[u] = reinterpret_cast<const u32x4*>(row.at)[j];
-        } else {
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            if (e0 + e < 0 || e0 + e >= a.V) continue;
-            const uint32_t bits = __float_as_uint(row.load(e0 + e));
-            if constexpr (!BF16) v[u][e] = bits;
-            else v[u][e >> 1] = e & 1 ? (v[u][e >> 1] & 0xFFFFu) | bits
-                                      : (v[u][e >> 1] & 0xFFFF0000u) | bits >> 16;
-          }
-        }
+        m = fmaxf(m, t + u * kThreads + tid < v1 ? vec_max(anew(v[u])) : -INFINITY);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    };
-
-    auto step = [&](int t, const u32x4 (&v)[kVecs]) {
-      float vm[kVecs], most = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        vm[u] = R::elem(v[u], 0);
-#pragma unroll
-        for (int e = 1; e < kPer; ++e) vm[u] = fmaxf(vm[u], R::elem(v[u], e));
-        most = fmaxf(most, vm[u]);
+      raise(m);
+      pass(std::true_type{}, t, v, vm, most);
+    }
+    top = fmaxf(top, most);
+    if constexpr (Top) {
+      if (t == v0) {  // n lanes hold as much as `bound`, in different vectors
+        const uint32_t one[1] = {key_of(most)};
+        const uint32_t bound = nth_key(one, a.n);
+        kept.tau = bound <= key_of(-INFINITY)
+                       ? -INFINITY : of_key(bound - (bound == 0x80000000u ? 2u : 1u));
       }
-      top = fmaxf(top, most);
-      // 2^(x - k) of up to 2^24 cost nothing
-      if (__any(most > m0 && (m0 == -INFINITY || (most - m0) * a.c > 24.0f))) {
-        const float m = wave_all(most, [](float x, float y) { return fmaxf(x, y); });
-        const float kn = a.c * m;
-        const bool far_n = !(fabsf(kn) < 4194304.0f);
-        if (m0 > -INFINITY) {
-          const float d = far || far_n ? (m0 - m) * a.c : k - kn;
-          const float f = exp2f(d);
-          sum_x = f > 0.0f ? f * fmaf(d, sum, sum_x) : 0.0f;
-          sum *= f;
-        }
-        m0 = m;
-        far = far_n;
-        k = kn;
-      }
-      // without a finite logit so far (x - k) is -inf, or NaN and put right below
-      const float sum_was = sum, sum_x_was = sum_x;
-      if (!far) {
+      if (__any(most > kept.tau)) {
 #pragma unroll
         for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            const float x = fmaf(R::elem(v[u], e), a.c, -k);
-            const float w = __builtin_amdgcn_exp2f(x);
-            sum += w;
-            if constexpr (Entropy) sum_x = fmaf(w, x, sum_x);
-          }
+          kept.add(vm[u] > kept.tau, vm[u], (uint32_t)(t + u * kThreads + tid));
+        if (kept.count > a.n + kSpare) kept.cut(a.n);
       }
-      if (far || (Entropy && __any(sum_x != sum_x))) {
-        // -inf, or out of range: a logit of no weight must not count as 0 * inf
-        sum = sum_was;
-        sum_x = sum_x_was;
-        if (m0 > -INFINITY) {
+    }
+  };
+
+  u32x4 v[kVecs];
+  load_tile(v0, v);
+  for (int t = v0; t < v1; t += kTile) {
+    u32x4 next[kVecs];
+    load_tile(t + kTile, next);
+    step(t, v);
 #pragma unroll
-          for (int u = 0; u < kVecs; ++u)
+    for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+  }
+
+  // By the first wave: the elements of vectors that are not whole (lanes 0 .. 7 the head's, 8 .. 15
+  // the tail's), and those of the token's own vector that are level with it.
+  if (tid < 2) s.edge[tid] = 0;
+  if (wave == 0 && part == 0) {
+    const int64_t i = lane < 8 ? (lane < row.head ? lane : a.V) : row.tail() + lane - 8;
+    const bool mine = lane < 16 && i < a.V;
+    const float z = mine ? row.load(i) : -INFINITY;
+    raise(z);
+    const float x = fmaxf(far ? (z - m0) * a.c : fmaf(z, a.c, -k), -200.0f);
+    const float w = __builtin_amdgcn_exp2f(x);
+    sum += w;
+    sum_x = fmaf(w, x, sum_x);
+    top = fmaxf(top, z);
+    if constexpr (Rank) {
+      above += __popcll(__ballot(mine && (z > level || (z == level && i < token))));
+      const int64_t own = (int64_t)token_vec * kPer - row.phase + lane;
+      const bool whole = ranked && token_vec >= row.first && token_vec < row.last;
+      above += __popcll(__ballot(whole && lane < kPer && own < token && row.load(own) == level));
+    }
+    if constexpr (Top) {
+      float m = z;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const float z = R::elem(v[u], e);
-              const float x = fmaxf(far ? (z - m0) * a.c : fmaf(z, a.c, -k), -200.0f);
-              const float w = __builtin_amdgcn_exp2f(x);
-              sum += w;
-              if constexpr (Entropy) sum_x = fmaf(w, x, sum_x);
-            }
-        }
-      }
-      if (ranked) {
-        const int64_t lo = (int64_t)t * kPer - row.phase, hi = lo + (int64_t)kTile * kPer;
-        if (hi <= token && zt > -INFINITY) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) above += __popcll(__ballot(R::elem(v[u], e) >= zt));
-        } else if (lo > token) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) above += __popcll(__ballot(R::elem(v[u], e) > zt));
-        } else {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const int64_t j = t + u * kThreads + tid, i = j * kPer - row.phase + e;
-              const float z = R::elem(v[u], e);
-              above += __popcll(
-                  __ballot(z > zt || (z == zt && i >= 0 && i < token && j < v1)));
-            }
-        }
-      }
-      if constexpr (Top) {
-        if (first) {  // n lanes hold as much as `bound`, in different vectors
-          const uint32_t one[1] = {key_of(most)};
-          const uint32_t bound = nth_key(one, a.n);
-          kept.tau = bound <= key_of(-INFINITY)
-                         ? -INFINITY : of_key(bound - (bound == 0x80000000u ? 2u : 1u));
-        }
-        if (__any(most > kept.tau)) {
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-            kept.add(vm[u] > kept.tau, vm[u], (uint32_t)(t + u * kThreads + tid), a.n);
-        }
-      }
-      first = false;
+      for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+      if ((lane == 0 || lane == 8) && m > -INFINITY)
+        s.edge[lane / 8] = (unsigned long long)key_of(m) << 32 |
+                           (lane ? ~(uint32_t)row.last : ~0u);
+    }
+  }
+
+  // the waves' sums, then the part's
+  auto add = [](float x, float y) SV_INLINE { return x + y; };
+  sum = wave_all(sum, add);
+  sum_x = wave_all(sum_x, add);
+  top = wave_all(top, [](float x, float y) { return fmaxf(x, y); });
+  if (lane == 0) {
+    const double shift = m0 == -INFINITY ? -INFINITY : far ? (double)a.c * m0 : (double)k;
+    s.stat[wave] = LogprobPart{shift, sum, sum_x, top, above, {0, 0}};
+  }
+  if constexpr (Top) {
+    if (kept.count > a.n) kept.cut(a.n);
+    __builtin_amdgcn_wave_barrier();
+    if (lane < kept.count)
+      s.keys[wave][lane] = (unsigned long long)key_of(kept.val[lane]) << 32 | ~kept.pos[lane];
+    if (lane == 0) s.count[wave] = kept.count;
+  }
+  __syncthreads();
+  LogprobPart st = joined(s.stat, kWaves);
+  if constexpr (Top) {
+    // a vector's rank among the waves' kept ones and the two that are not whole
+    auto rank_of = [&](unsigned long long me) SV_INLINE {
+      int rank = (s.edge[0] > me) + (s.edge[1] > me);
+      for (int i = 0; i < kWaves; ++i)
+        for (int j = 0; j < s.count[i]; ++j) rank += s.keys[i][j] > me;
+      return rank;
     };
-
-    u32x4 v[kVecs], w[kVecs];
-    load_tile(v0, v);
-    for (int t = v0; t < v1; t += 2 * kTile) {
-      load_tile(t + kTile, w);
-      step(t, v);
-      if (t + kTile >= v1) break;
-      load_tile(t + 2 * kTile, v);
-      step(t + kTile, w);
+    const unsigned long long me = lane < kept.count ? s.keys[wave][lane] : 0;
+    const int rank = rank_of(me);
+    if (me && rank < a.n) s.picked[rank] = me;
+    if (tid < 2 && s.edge[tid]) {
+      const int at = rank_of(s.edge[tid]);
+      if (at < a.n) s.picked[at] = s.edge[tid];
     }
-
-    // the waves' sums, then the part's
-    auto add = [](float x, float y) { return x + y; };
-    sum = wave_all(sum, add);
-    sum_x = wave_all(sum_x, add);
-    top = wave_all(top, [](float x, float y) { return fmaxf(x, y); });
-    if (lane == 0) {
-      const double shift = m0 == -INFINITY ? -INFINITY : far ? (double)a.c * m0 : (double)k;
-      s.stat[wave] = LogprobPart{shift, sum, sum_x, top, above, {0, 0}};
+    if (tid == 0) {
+      int all = (s.edge[0] != 0) + (s.edge[1] != 0);
+      for (int i = 0; i < kWaves; ++i) all += s.count[i];
+      s.found = all < a.n ? all : a.n;
     }
-    if constexpr (Top) {
-      if (kept.count > a.n) kept.cut(a.n);
-      __builtin_amdgcn_wave_barrier();
-      if (lane < kept.count)
-        s.keys[wave][lane] = (unsigned long long)key_of(kept.val[lane]) << 32 | ~kept.pos[lane];
-      if (lane == 0) s.count[wave] = kept.count;
-    }
-    __syncthreads();
-    LogprobPart st = joined(s.stat, kWaves);
-    if constexpr (Top) {
-      // a vector's rank among the waves' kept ones
-      unsigned long long me = lane < kept.count ? s.keys[wave][lane] : 0;
-      int rank = 0, all = 0;
-      for (int i = 0; i < kWaves; ++i) {
-        const int count = s.count[i];
-        all += count;
-        for (int j = 0; j < count; ++j) rank += s.keys[i][j] > me;
-      }
-      if (me && rank < a.n) s.picked[rank] = me;
-      if (tid == 0) s.found = all < a.n ? all : a.n;
-    }
-    __syncthreads();
-    if (a.parts == 1) {
-      finish<BF16>(a, s, &row, r, st, token);
-    } else {
-      if (tid == 0) a.part[unit] = st;
-      for (int j = tid; j < a.n; j += kThreads)
-        a.part_top[unit * a.n + j] = j < s.found ? s.picked[j] : 0ull;
-    }
-    __syncthreads();
+  }
+  __syncthreads();
+  if (a.parts == 1) {
+    finish<BF16>(a, s, &row, r, st, token);
+  } else {
+    if (tid == 0) a.part[unit] = st;
+    for (int j = tid; j < a.n; j += kThreads)
+      a.part_top[unit * a.n + j] = j < s.found ? s.picked[j] : 0ull;
   }
 }
 
@@ -487,19 +525,20 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a) {
 }
 
 template <bool BF16, bool Entropy, bool Rank>
-void launch_top(const LogprobArgs& a, unsigned blocks, hipStream_t stream) {
+void launch_top(const LogprobArgs& a, dim3 blocks, hipStream_t stream) {
   if (a.n)
-    hipLaunchKernelGGL((k_logprob<BF16, Entropy, Rank, true>), dim3(blocks), dim3(kThreads), 0,
+    hipLaunchKernelGGL((k_logprob<BF16, Entropy, Rank, true>), blocks, dim3(kThreads), 0,
                        stream, a);
   else
-    hipLaunchKernelGGL((k_logprob<BF16, Entropy, Rank, false>), dim3(blocks), dim3(kThreads), 0,
+    hipLaunchKernelGGL((k_logprob<BF16, Entropy, Rank, false>), blocks, dim3(kThreads), 0,
                        stream, a);
 }
 
 template <bool BF16>
 hipError_t launch(const LogprobArgs& a, hipStream_t stream) {
   const int64_t units = (int64_t)a.R * a.parts;
-  const unsigned blocks = (unsigned)(units < kMaxBlocks ? units : kMaxBlocks);
+  const unsigned wide = (unsigned)(units < kMaxBlocks ? units : kMaxBlocks);
+  const dim3 blocks(wide, (unsigned)((units + wide - 1) / wide));
   if (a.entropy && a.rank) launch_top<BF16, true, true>(a, blocks, stream);
   else if (a.entropy) launch_top<BF16, true, false>(a, blocks, stream);
   else if (a.rank) launch_top<BF16, false, true>(a, blocks, stream);
@@ -516,14 +555,15 @@ hipError_t launch(const LogprobArgs& a, hipStream_t stream) {
 LogprobPlan plan_logprobs(int R, int V, sv_dtype dt, int n) {
   LogprobPlan p{};
   const int per = dt == SV_DTYPE_BF16 ? 8 : 4;
-  const int64_t vecs = ((int64_t)V + 2 * (per - 1)) / per + 1;  // of a row at any phase, at most
-  const int64_t tiles = (vecs + kTile - 1) / kTile;
+  const int64_t vecs = V / per > 1 ? V / per : 1;  // whole ones of a row, at most
+  const int tile = kThreads * vecs_of(dt == SV_DTYPE_BF16);
+  const int64_t tiles = (vecs + tile - 1) / tile;
   // two workgroups a compute unit, a tile each at least
   int64_t parts = (512 + (int64_t)R - 1) / R;
   parts = parts < tiles ? parts : tiles;
   parts = parts < kMaxParts ? parts : kMaxParts;
   const int64_t each = (tiles + parts - 1) / parts;
-  p.part_vecs = (int)(each * kTile);
+  p.part_vecs = (int)(each * tile);
   p.parts = (int)((tiles + each - 1) / each);
   if (p.parts > 1) {
     p.o_top = (size_t)R * p.parts * sizeof(LogprobPart);
