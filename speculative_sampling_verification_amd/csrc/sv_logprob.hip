@@ -26,9 +26,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int vecs_of(bool bf16) { return bf16 ? 4 : 8; }  // a thread and tile: 32 logits
+constexpr int kVecs = 8;              // vectors a thread and tile
+constexpr int kTile = kThreads * kVecs;
 constexpr int kSpare = 48;            // vectors a wave keeps beyond n until it cuts its list
-constexpr int kList = kLogprobMaxTop + kSpare + 64 * 8;
+constexpr int kList = kLogprobMaxTop + kSpare + 64 * kVecs;
 constexpr int kMaxParts = 64;         // of a row: one a lane of the join
 constexpr int64_t kMaxBlocks = 1 << 20;
 constexpr double kLn2 = 0.69314718055994530942;
@@ -81,12 +82,6 @@ struct Row {
     else return __uint_as_float(v[e]);
   }
 };
-
-// The same logits to the compiler's eyes new ones: decoded again instead of kept decoded.
-__device__ __forceinline__ u32x4 anew(u32x4 v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 template <class T, class Op>
 __device__ __forceinline__ T wave_all(T x, Op op) {
@@ -260,7 +255,7 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 template <bool BF16, bool Entropy, bool Rank, bool Top>
 __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
   using R = Row<BF16>;
-  constexpr int kPer = R::kPer, kVecs = vecs_of(BF16), kTile = kThreads * kVecs;
+  constexpr int kPer = R::kPer;
   __shared__ Lds s;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -309,6 +304,13 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
     far = far_n;
     clamp |= far;
   };
+  // one logit, whatever it is
+  auto take = [&](float z) SV_INLINE {
+    const float x = fmaxf(far ? (z - m0) * a.c : fmaf(z, a.c, -k), -200.0f);
+    const float w = __builtin_amdgcn_exp2f(x);
+    sum += w;
+    sum_x = fmaf(w, x, sum_x);
+  };
   auto vec_max = [&](const u32x4& v) SV_INLINE {
     float m = R::elem(v, 0);
 #pragma unroll
@@ -317,56 +319,69 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
   };
 
   // behind the last vector: that one again
-  auto load_tile = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
-    if (t >= v1) return;
-    const u32x4* p = reinterpret_cast<const u32x4*>(row.at);
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int j = t + u * kThreads + tid;
-      v[u] = p[j < v1 ? j : v1 - 1];
-    }
+  const u32x4* vecs = reinterpret_cast<const u32x4*>(row.at);
+  auto load_vec = [&](int t, int u) SV_INLINE {
+    const int j = t + u * kThreads + tid;
+    return vecs[j < v1 ? j : v1 - 1];
   };
 
-  // Adds a tile's logits at the shift as it is; false, with nothing added, if that does not do.
-  // Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and far shifts are
-  // subtracted first.
-  auto pass = [&](auto clamped, int t, const u32x4 (&v)[kVecs], float (&vm)[kVecs],
+  // One tile.  A vector's registers take the next tile's as soon as it is done, so that 8 KB a wave
+  // are always on their way.  The sums are formed at the shift as it is, and again (`redo`) where
+  // that does not do.  Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and
+  // far shifts are subtracted first.
+  auto pass = [&](auto clamped, int t, u32x4 (&v)[kVecs], float (&vm)[kVecs],
                   float& most) SV_INLINE {
     constexpr bool Clamp = decltype(clamped)::value;
     const float z0 = Clamp && far ? m0 : 0.0f, k0 = Clamp && far ? 0.0f : k;
     float f = 0.0f, fx = 0.0f;
-    int n = 0;
     most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int j = t + u * kThreads + tid;
-      const float th = !Rank ? 0.0f : j >= v1 ? INFINITY : j < token_vec ? level : beyond;
-      const u32x4 x4 = Clamp ? anew(v[u]) : v[u];
       float m = -INFINITY;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        const float z = R::elem(x4, e);
+        const float z = R::elem(v[u], e);
         float x = fmaf(Clamp ? z - z0 : z, a.c, -k0);
         if constexpr (Clamp) x = fmaxf(x, -200.0f);
         const float w = __builtin_amdgcn_exp2f(x);
         m = fmaxf(m, z);
         f += w;
         if constexpr (Entropy) fx = fmaf(w, x, fx);
-        if constexpr (Rank) n += __popcll(__ballot(z >= th));
       }
       vm[u] = j < v1 ? m : -INFINITY;
       most = fmaxf(most, vm[u]);
-      __builtin_amdgcn_sched_barrier(0);  // few decoded logits at a time
+      if constexpr (Rank) {
+        const float th = j < token_vec ? level : beyond;
+        if (__any(vm[u] >= th && j < v1)) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            above += __popcll(__ballot(R::elem(v[u], e) >= th && j < v1));
+        }
+      }
+      v[u] = load_vec(t + kTile, u);
+      // few decoded logits at a time: nothing moves over this
+      asm volatile("" : "+v"(f), "+v"(fx), "+v"(vm[u]));
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (!Clamp) {
-      const bool odd = Entropy && fx != fx;
-      clamp = __any(odd);
-      if (clamp || __any((most - m0) * a.c > 24.0f)) return false;
+    const bool odd = !Clamp && Entropy && fx != fx;
+    if (__any(odd)) clamp = true;
+    else if (!__any((most - m0) * a.c > 24.0f)) {
+      sum += f;
+      sum_x += fx;
+      return true;
     }
-    sum += f;
-    sum_x += fx;
-    above += n;
-    return true;
+    return false;
+  };
+  auto redo = [&](int t, float most) SV_INLINE {
+    raise(most);
+#pragma unroll 1
+    for (int u = 0; u < kVecs; ++u) {
+      if (t + u * kThreads + tid >= v1) continue;
+      const u32x4 y = load_vec(t, u);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) take(R::elem(y, e));
+    }
   };
   auto step = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
     float vm[kVecs], most;
@@ -376,17 +391,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
       for (int u = 0; u < kVecs; ++u)
         if (t + u * kThreads + tid >= v1) v[u] = u32x4{none, none, none, none};
     }
-    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(anew(v[0])) : -INFINITY);
-    if (clamp || !pass(std::false_type{}, t, v, vm, most)) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        m = fmaxf(m, t + u * kThreads + tid < v1 ? vec_max(anew(v[u])) : -INFINITY);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      raise(m);
-      pass(std::true_type{}, t, v, vm, most);
-    }
+    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(v[0]) : -INFINITY);
+    const bool done = clamp ? pass(std::true_type{}, t, v, vm, most)
+                            : pass(std::false_type{}, t, v, vm, most);
+    if (!done) redo(t, most);
     top = fmaxf(top, most);
     if constexpr (Top) {
       if (t == v0) {  // n lanes hold as much as `bound`, in different vectors
@@ -404,14 +412,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
     }
   };
 
-  u32x4 v[kVecs];
-  load_tile(v0, v);
-  for (int t = v0; t < v1; t += kTile) {
-    u32x4 next[kVecs];
-    load_tile(t + kTile, next);
-    step(t, v);
+  if (v0 < v1) {
+    u32x4 v[kVecs];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+    for (int u = 0; u < kVecs; ++u) v[u] = load_vec(v0, u);
+    for (int t = v0; t < v1; t += kTile) step(t, v);
   }
 
   // By the first wave: the elements of vectors that are not whole (lanes 0 .. 7 the head's, 8 .. 15
@@ -422,10 +427,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
     const bool mine = lane < 16 && i < a.V;
     const float z = mine ? row.load(i) : -INFINITY;
     raise(z);
-    const float x = fmaxf(far ? (z - m0) * a.c : fmaf(z, a.c, -k), -200.0f);
-    const float w = __builtin_amdgcn_exp2f(x);
-    sum += w;
-    sum_x = fmaf(w, x, sum_x);
+    take(z);
     top = fmaxf(top, z);
     if constexpr (Rank) {
       above += __popcll(__ballot(mine && (z > level || (z == level && i < token))));
@@ -556,14 +558,13 @@ LogprobPlan plan_logprobs(int R, int V, sv_dtype dt, int n) {
   LogprobPlan p{};
   const int per = dt == SV_DTYPE_BF16 ? 8 : 4;
   const int64_t vecs = V / per > 1 ? V / per : 1;  // whole ones of a row, at most
-  const int tile = kThreads * vecs_of(dt == SV_DTYPE_BF16);
-  const int64_t tiles = (vecs + tile - 1) / tile;
+  const int64_t tiles = (vecs + kTile - 1) / kTile;
   // two workgroups a compute unit, a tile each at least
   int64_t parts = (512 + (int64_t)R - 1) / R;
   parts = parts < tiles ? parts : tiles;
   parts = parts < kMaxParts ? parts : kMaxParts;
   const int64_t each = (tiles + parts - 1) / parts;
-  p.part_vecs = (int)(each * tile);
+  p.part_vecs = (int)(each * kTile);
   p.parts = (int)((tiles + each - 1) / each);
   if (p.parts > 1) {
     p.o_top = (size_t)R * p.parts * sizeof(LogprobPart);
