@@ -90,19 +90,20 @@ __device__ __forceinline__ T wave_all(T x, Op op) {
   return x;
 }
 
-// The n-th largest of the wave's keys, several a lane (the largest k with n keys >= k).
-template <int Keys>
+// The n-th largest of the wave's keys, several a lane (the largest k with n keys >= k).  Keys of
+// bf16 are told apart by their upper halves: half as many steps.
+template <bool BF16, int Keys>
 __device__ __forceinline__ uint32_t nth_key(const uint32_t (&k)[Keys], int n) {
   uint32_t t = 0;
 #pragma unroll 1
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = t | 1u << bit;
+  for (uint32_t bit = 0x80000000u; bit >= (BF16 ? 0x10000u : 1u); bit >>= 1) {
+    const uint32_t c = t | bit;
     int count = 0;
 #pragma unroll
     for (int i = 0; i < Keys; ++i) count += __popcll(__ballot(k[i] >= c));
     if (count >= n) t = c;
   }
-  return t;
+  return BF16 && !(t & 0x80000000u) && t ? t | 0xFFFFu : t;  // a negative number's lower half
 }
 
 struct Lds {
@@ -114,10 +115,11 @@ struct Lds {
   unsigned long long elems[kLogprobMaxTop * 8];
   LogprobPart stat[kWaves];
   int count[kWaves];
-  int found;
+  int found, near;
 };
 
 // Vectors that a wave keeps, in order of position.
+template <bool BF16>
 struct Kept {
   float* val;
   uint32_t* pos;
@@ -135,7 +137,7 @@ struct Kept {
       k[i] = at < count ? key_of(val[at]) : 0u;
       p[i] = at < count ? pos[at] : 0u;
     }
-    const uint32_t t = nth_key(k, n);
+    const uint32_t t = nth_key<BF16>(k, n);
     const unsigned long long below = (1ull << lane) - 1;
     int quota = n;
 #pragma unroll
@@ -217,31 +219,30 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, Lds& s, const Row<B
   }
   if (!a.n) return;
   const int vecs = some ? s.found : 0, all = vecs * Row<BF16>::kPer;
+  if (tid == 0) s.near = 0;
+  __syncthreads();
+  // elements that may be among the first: no less than the last vector's largest where there are n
+  // vectors; in no order, as their keys are all different
+  const unsigned long long least = vecs == a.n ? s.picked[vecs - 1] >> 32 << 32 : 0ull;
   for (int e = tid; e < all; e += kThreads) {
     const uint32_t v = ~(uint32_t)s.picked[e / Row<BF16>::kPer];
     const int64_t i = (int64_t)v * Row<BF16>::kPer - row->phase + e % Row<BF16>::kPer;
     const float z = i >= 0 && i < a.V ? row->load(i) : -INFINITY;
-    s.elems[e] = z > -INFINITY ? (unsigned long long)key_of(z) << 32 | (uint32_t)~(uint32_t)i : 0;
+    const unsigned long long key = (unsigned long long)key_of(z) << 32 | (uint32_t)~(uint32_t)i;
+    if (z > -INFINITY && key >= least) s.elems[atomicAdd(&s.near, 1)] = key;
   }
   __syncthreads();
-  int real = 0;
-  for (int e0 = 0; e0 < all; e0 += kThreads) {
-    const int e = e0 + tid;
-    const unsigned long long me = e < all ? s.elems[e] : 0;
+  const int near = s.near;
+  for (int e = tid; e < near; e += kThreads) {
+    const unsigned long long me = s.elems[e];
     int rank = 0;
-    real = 0;
-    for (int j = 0; j < all; ++j) {
-      const unsigned long long k = s.elems[j];
-      rank += k > me;
-      real += k != 0;
-    }
-    if (me && rank < a.n) {
-      const uint32_t i = ~(uint32_t)me;
-      a.top_tokens[(int64_t)r * a.n + rank] = (int32_t)i;
-      a.top_logprobs[(int64_t)r * a.n + rank] = logprob(row->load(i));
+    for (int j = 0; j < near; ++j) rank += s.elems[j] > me;
+    if (rank < a.n) {
+      a.top_tokens[(int64_t)r * a.n + rank] = (int32_t) ~(uint32_t)me;
+      a.top_logprobs[(int64_t)r * a.n + rank] = logprob(of_key((uint32_t)(me >> 32)));
     }
   }
-  for (int j = real + tid; j < a.n; j += kThreads) {
+  for (int j = near + tid; j < a.n; j += kThreads) {
     a.top_tokens[(int64_t)r * a.n + j] = -1;
     a.top_logprobs[(int64_t)r * a.n + j] = -INFINITY;
   }
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
   bool far = false;                // |c m0| is 2^22 or more, and its rounding (then over
                                    // 1/8) shows in x - k: differences of logits first
   int above = 0;
-  Kept kept{s.val[wave], s.pos[wave], 0, -INFINITY};
+  Kept<BF16> kept{s.val[wave], s.pos[wave], 0, -INFINITY};
 
   bool clamp = false;  // logits of -inf, or far: pass<true>
 
@@ -352,11 +353,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
       vm[u] = j < v1 ? m : -INFINITY;
       most = fmaxf(most, vm[u]);
       if constexpr (Rank) {
-        const float th = j < token_vec ? level : beyond;
-        if (__any(vm[u] >= th && j < v1)) {
+        const float th = j >= v1 ? INFINITY : j < token_vec ? level : beyond;
+        if (__any(m >= th)) {
 #pragma unroll
-          for (int e = 0; e < kPer; ++e)
-            above += __popcll(__ballot(R::elem(v[u], e) >= th && j < v1));
+          for (int e = 0; e < kPer; ++e) above += __popcll(__ballot(R::elem(v[u], e) >= th));
         }
       }
       v[u] = load_vec(t + kTile, u);
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
     if constexpr (Top) {
       if (t == v0) {  // n lanes hold as much as `bound`, in different vectors
         const uint32_t one[1] = {key_of(most)};
-        const uint32_t bound = nth_key(one, a.n);
+        const uint32_t bound = nth_key<BF16>(one, a.n);
         kept.tau = bound <= key_of(-INFINITY)
                        ? -INFINITY : of_key(bound - (bound == 0x80000000u ? 2u : 1u));
       }
