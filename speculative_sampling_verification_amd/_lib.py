@@ -996,28 +996,34 @@ def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_
     R, top_n = math.prod(shape), int(top_n)
     if V < 1 or max(R, logits.numel() // V) >= 2**31:
         raise ValueError(f"logits {tuple(logits.shape)} for {R} tokens is out of range")
-    kinds = {}
-    if tokens is not None:
-        kinds["logprob"] = (torch.float32, shape)
-    if want_rank:
-        kinds["rank"] = (torch.int32, shape)
-    if want_entropy:
-        kinds["entropy"] = (torch.float32, shape)
-    if top_n > 0:
-        kinds["top_tokens"] = (torch.int32, shape + (top_n,))
-        kinds["top_logprobs"] = (torch.float32, shape + (top_n,))
-    out = dict(out) if out else {}
-    for name in out:
-        if name not in kinds:
-            raise ValueError(f"out holds {name}, which is not asked for")
     raw = _raw_stream(place, None)
     need = _lib.spec_token_logprobs_workspace_size(R, V, dt, top_n)
     if need == 0:
         raise SpecVerifyError("spec_token_logprobs_workspace_size", 1)
-    for name, (dtype, dims) in kinds.items():
-        if name not in out:
-            out[name] = torch.empty(dims, dtype=dtype, device=dev)
-    at = {name: _arg(out[name], f"out {name}", place, *kinds[name]) for name in kinds}
+    out = dict(out) if out else {}
+    at = {}
+
+    def give(name, wanted, dtype, dims):
+        if not wanted:
+            if name in out:
+                raise ValueError(f"out holds {name}, which is not asked for")
+            at[name] = None
+        elif name in out:
+            at[name] = _arg(out[name], f"out {name}", place, dtype, dims)
+        else:
+            # of the tokens' shape mostly: made like them, the cheapest way
+            t = torch.empty_like(tokens, dtype=dtype) if dims is shape and tokens is not None \
+                else torch.empty(dims, dtype=dtype, device=dev)
+            out[name] = t
+            at[name] = t.data_ptr()
+    give("logprob", tokens is not None, torch.float32, shape)
+    give("rank", want_rank, torch.int32, shape)
+    give("entropy", want_entropy, torch.float32, shape)
+    give("top_tokens", top_n > 0, torch.int32, shape + (top_n,))
+    give("top_logprobs", top_n > 0, torch.float32, shape + (top_n,))
+    for name in out:
+        if name not in at:
+            raise ValueError(f"out holds {name}, which is no result")
     if _capturing(place):  # the graph's own: graphs may run side by side
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
@@ -1026,8 +1032,8 @@ def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_
             ws = workspace(dev, need)
     _cache_call(place, "spec_token_logprobs", _lib.spec_token_logprobs, logits.data_ptr(), dt,
                 logits.numel() // V, V, rows_at, tokens_at, R, temperature, top_n,
-                at.get("logprob"), at.get("rank"), at.get("entropy"), at.get("top_tokens"),
-                at.get("top_logprobs"), ws.data_ptr(), ws.numel(), raw)
+                at["logprob"], at["rank"], at["entropy"], at["top_tokens"], at["top_logprobs"],
+                ws.data_ptr(), ws.numel(), raw)
     return out
 
 

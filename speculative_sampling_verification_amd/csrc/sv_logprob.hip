@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
   const u32x4* vecs = reinterpret_cast<const u32x4*>(row.at);
   auto load_vec = [&](int t, int u) SV_INLINE {
     const int j = t + u * kThreads + tid;
-    return vecs[j < v1 ? j : v1 - 1];
+    return __builtin_nontemporal_load(&vecs[j < v1 ? j : v1 - 1]);
   };
 
   // One tile.  A vector's registers take the next tile's as soon as it is done, so that 8 KB a wave
