@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_step.hpp"
 
@@ -21,11 +22,12 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
-constexpr int kWeighWorkgroups = 4 * kAttnCus;
+constexpr int kFewRows = 16;  // rows a kv head up to which k_weigh is taken
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Keys of sequence b that are weighed.
@@ -84,27 +86,221 @@ __device__ __forceinline__ void find_piece(const WeighArgs& a, long long* total,
   *off_out = pos < all ? start_off : 0;
 }
 
-// KT blocks of 16 keys a piece.
-template <bool BF16, int D, int KT>
-__global__ __launch_bounds__(kWeighThreads) void k_weigh(WeighArgs a) {
-  constexpr int kES = BF16 ? 2 : 4, kRow = D * kES;
-  constexpr int NF = kRow / 64;   // 16-byte pieces of a row that a lane holds
-  constexpr int kKeys = 16 * KT;
+// Up to 16 rows: a wave takes KT blocks of 16 keys at a time.  Its pieces' loads form a line: while one
+// piece is computed the next one's keys and queries are on their way, and the page numbers of the one
+// after that before them (loads come back in order, so none waits for a younger one).
+template <bool BF16, int D>
+struct Few {
+  static constexpr int kRow = D * (BF16 ? 2 : 4);
+  static constexpr int NF = kRow / 64;  // 16-byte pieces of a row that a lane holds
+  static constexpr int KT = kRow <= 256 ? 4 : kRow <= 512 ? 2 : 1;  // 64 registers of keys
+  static constexpr int kKeys = 16 * KT;
+  static constexpr int kOcc = kRow <= 512 ? 3 : 2;  // workgroups a compute unit
+};
+
+template <bool BF16, int D>
+__global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(WeighArgs a) {
+  using C = Few<BF16, D>;
+  constexpr int KT = C::KT, NF = C::NF;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const float sl2 = a.scale * kLog2e;
+  const int Hkv = a.c.kv_heads;
+  struct Piece {
+    int b, h, key0, keys, held;
+  };
+  // the wave's place in the line of pieces
   long long total, off;
   int b;
-  find_piece<kKeys>(a, &total, &b, &off);
+  find_piece<C::kKeys>(a, &total, &b, &off);
+  b = __builtin_amdgcn_readfirstlane(b);
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   long long pos = per * blockIdx.x + wave;
   const long long last = per * (blockIdx.x + 1), end = last < total ? last : total;
   off += wave;
+  auto next_piece = [&](Piece& p) __attribute__((always_inline)) {
+    if (pos >= end) return false;
+    int keys = keys_of(a, b);
+    long long n = (long long)Hkv * ((keys + C::kKeys - 1) / C::kKeys);
+    while (off >= n) {
+      off -= n;
+      if (++b >= a.c.seqs) return false;
+      keys = keys_of(a, b);
+      n = (long long)Hkv * ((keys + C::kKeys - 1) / C::kKeys);
+    }
+    const int tile = (int)(off >> 31 ? off / Hkv : (uint32_t)off / (uint32_t)Hkv);
+    p.b = b;
+    p.h = (int)(off - (long long)tile * Hkv);
+    p.key0 = tile * C::kKeys;
+    p.keys = keys;
+    p.held = positions_held(a.c, b);
+    pos += kWeighWaves;
+    off += kWeighWaves;
+    return true;
+  };
+  auto load_pages = [&](const Piece& p, int (&page)[KT]) __attribute__((always_inline)) {
+    const int32_t* table = a.c.table + (size_t)p.b * a.c.width;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int key = p.key0 + t * 16 + col;
+      page[t] = table[fast_div(a.c.page_div, (uint32_t)(key < p.keys ? key : p.keys - 1))];
+    }
+  };
+  u32x4 kf[KT][NF], qf[NF];
+  int number[KT];  // of this lane's keys; out of every row's sight where one does not exist
+  float lse[4], old = 0.0f;
+  int see[4];
+  auto load_piece = [&](const Piece& p, const int (&page)[KT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int key = p.key0 + t * 16 + col;
+      int64_t row = 0;
+      number[t] = INT32_MAX;
+      if (key < p.keys && names_page(a.c, p.held, key, page[t])) {
+        const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
+        row = (int64_t)page[t] * a.c.page_stride +
+              (int64_t)(key - (int)(pi * a.c.page_div.d)) * a.c.token_stride;
+        number[t] = key;
+      }
+      const char* at = a.c.k + row + (int64_t)p.h * a.c.head_stride + quad * 16;
+#pragma unroll
+      for (int s = 0; s < NF; ++s) kf[t][s] = *reinterpret_cast<const u32x4*>(at + s * 64);
+    }
+    int n = a.nodes ? a.nodes[p.b] : a.N;
+    n = n < 0 ? 0 : n < a.N ? n : a.N;
+    const int rows = n * a.G;
+    {
+      const int node = (int)fast_div(a.g_div, (uint32_t)col), g = col - node * a.G;
+      const char* at = a.q.at + (int64_t)p.b * a.q.seq + (int64_t)node * a.q.node +
+                       (int64_t)(p.h * a.G + g) * a.q.head + quad * 16;
+#pragma unroll
+      for (int s = 0; s < NF; ++s)
+        qf[s] = col < rows ? *reinterpret_cast<const u32x4*>(at + s * 64) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = quad * 4 + e;
+      lse[e] = -INFINITY;
+      see[e] = 0;
+      if (r < rows) {
+        const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
+        const int64_t at = (int64_t)p.b * a.N + node;
+        lse[e] = a.lse[at * ((int64_t)Hkv * a.G) + p.h * a.G + g];
+        see[e] = a.seen ? a.seen[at] : INT32_MAX - 1;
+      }
+    }
+    if (a.decay != 0.0f && lane < C::kKeys && p.key0 + lane < p.keys)
+      old = a.w[((int64_t)p.b * Hkv + p.h) * a.length + p.key0 + lane];
+  };
+
+  Piece p, ahead;
+  int page[KT], page_ahead[KT];
+  bool some = next_piece(p), more = false;
+  if (some) {
+    load_pages(p, page);
+    more = next_piece(ahead);
+    if (more) load_pages(ahead, page_ahead);
+    load_piece(p, page);
+  }
+  while (some) {
+    float lse2[4];
+    int limit[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool live = lse[e] != -INFINITY;
+      lse2[e] = live ? lse[e] * kLog2e : 0.0f;
+      limit[e] = !live ? 0 : see[e] < p.keys ? see[e] : p.keys;
+    }
+    float mine = 0.0f;  // the sum of this lane's key: lane 16 t + c has key c of block t
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < NF; ++s) {
+        if constexpr (BF16) {
+          z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[s]),
+                                                      __builtin_bit_cast(bf16x8, kf[t][s]), z, 0, 0,
+                                                      0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(qf[s][e]),
+                                                     __uint_as_float(kf[t][s][e]), z, 0, 0, 0);
+        }
+      }
+      float x = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = __builtin_amdgcn_exp2f(fmaf(z[e], sl2, -lse2[e]));
+        x += number[t] < limit[e] ? w : 0.0f;
+      }
+      x += __shfl_xor(x, 16);  // the four lanes that share a key
+      x += __shfl_xor(x, 32);
+      mine = quad == t ? x : mine;
+    }
+    if (lane < C::kKeys && p.key0 + lane < p.keys)
+      a.w[((int64_t)p.b * Hkv + p.h) * a.length + p.key0 + lane] =
+          a.decay == 0.0f ? mine : fmaf(a.decay, old, mine);
+    some = more;
+    if (some) {
+      p = ahead;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) page[t] = page_ahead[t];
+      more = next_piece(ahead);
+      if (more) load_pages(ahead, page_ahead);
+      load_piece(p, page);
+    }
+  }
+}
+
+// Many rows: a workgroup takes 32 KB keys, 32 (KB a wave) at a time in registers, and all rows come
+// by through LDS, RT at a time, two stages of them.
+template <bool BF16, int D, int KB, int RT>
+struct Rows {
+  static constexpr int kES = BF16 ? 2 : 4;
+  static constexpr int kRow = D * kES;
+  static constexpr int kChunks = kRow / 16;            // 16-byte pieces of a row
+  static constexpr int kFrags = kChunks / 2;           // ... that a lane holds
+  static constexpr int kKeys = 32 * KB * kWeighWaves;  // of a workgroup
+  static constexpr int kLoads = RT * kChunks / kWeighThreads;  // pieces a thread loads a stage
+  // the keys of 1024-byte rows take half of the registers of two waves a SIMD
+  static constexpr int kOcc = kRow > 512 ? 1 : 2;
+  static_assert(RT % 32 == 0 && RT <= kWeighThreads && RT * kChunks % kWeighThreads == 0, "stage");
+
+  // Piece c of row r lies at place c ^ swz(r): rows read together lie in different banks.
+  __device__ static __forceinline__ int swz(int r) {
+    if constexpr (kRow % 256 == 0) return r & 15;
+    else if constexpr (kRow == 128) return (r >> 1) & 7;
+    else return (r >> 2) & 3;
+  }
+
+  struct Lds {
+    alignas(16) char q[2][RT * kRow];
+    alignas(16) float lse2[2][RT];
+    alignas(16) int see[2][RT];
+  };
+};
+
+template <bool BF16, int D, int KB, int RT>
+__global__ __launch_bounds__(kWeighThreads)
+__attribute__((amdgpu_waves_per_eu(Rows<BF16, D, KB, RT>::kOcc, Rows<BF16, D, KB, RT>::kOcc)))
+void k_weigh_rows(WeighArgs a) {
+  using C = Rows<BF16, D, KB, RT>;
+  __shared__ typename C::Lds S;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const float sl2 = a.scale * kLog2e;
+  long long total, off;
+  int b;
+  find_piece<C::kKeys>(a, &total, &b, &off);
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long last = per * (blockIdx.x + 1), end = last < total ? last : total;
   const int Hkv = a.c.kv_heads;
-  for (; pos < end; pos += kWeighWaves, off += kWeighWaves) {
+  for (long long pos = per * blockIdx.x; pos < end; ++pos, ++off) {
     for (; b < a.c.seqs; ++b) {
-      const long long n = pieces_of<kKeys>(a, b);
+      const long long n = pieces_of<C::kKeys>(a, b);
       if (off < n) break;
       off -= n;
     }
@@ -113,126 +309,199 @@ __global__ __launch_bounds__(kWeighThreads) void k_weigh(WeighArgs a) {
     const int h = (int)(off - (long long)tile * Hkv);
     const int keys = keys_of(a, b), held = positions_held(a.c, b);
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
-    // this lane's keys
-    u32x4 kf[KT][NF];
-    int limit[KT];  // key number, out of every row's sight where it does not exist
+    int n = a.nodes ? a.nodes[b] : a.N;
+    n = n < 0 ? 0 : n < a.N ? n : a.N;
+    const int rows = n * a.G;
+
+    // a stage of rows: on its way in registers, then in LDS
+    u32x4 next[C::kLoads];
+    float next_lse = 0.0f;
+    int next_see = 0;
+    // this thread's pieces and row; from stage to stage they are a fixed step apart where a node's
+    // heads do not straddle stages
+    auto row_at = [&](int r, int c) __attribute__((always_inline)) {
+      const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
+      return a.q.at + (int64_t)b * a.q.seq + (int64_t)node * a.q.node +
+             (int64_t)(h * a.G + g) * a.q.head + c * 16;
+    };
+    const bool even = RT % a.G == 0;
+    const int64_t step = even ? (int64_t)(RT / a.G) * a.q.node : 0;
+    const char* piece[C::kLoads];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const int key = tile * kKeys + t * 16 + col;
+    for (int i = 0; i < C::kLoads; ++i) {
+      const int x = tid + i * kWeighThreads;
+      piece[i] = row_at(x / C::kChunks, x % C::kChunks);
+    }
+    auto load = [&](int r0) __attribute__((always_inline)) {
+      const bool whole = even && r0 + RT <= rows;
+#pragma unroll
+      for (int i = 0; i < C::kLoads; ++i) {
+        const int x = tid + i * kWeighThreads, r = r0 + x / C::kChunks;
+        if (whole) next[i] = *reinterpret_cast<const u32x4*>(piece[i]);
+        else if (r < rows) next[i] = *reinterpret_cast<const u32x4*>(row_at(r, x % C::kChunks));
+        piece[i] += step;
+      }
+      next_lse = -INFINITY;
+      next_see = 0;
+      const int r = r0 + tid;
+      if (tid < RT && r < rows) {
+        const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
+        next_lse = a.lse[((int64_t)b * a.N + node) * ((int64_t)Hkv * a.G) + h * a.G + g];
+        next_see = a.seen ? a.seen[(int64_t)b * a.N + node] : INT32_MAX;
+      }
+    };
+    auto store = [&](int to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < C::kLoads; ++i) {
+        const int x = tid + i * kWeighThreads, r = x / C::kChunks, c = x % C::kChunks;
+        *reinterpret_cast<u32x4*>(&S.q[to][r * C::kRow + (c ^ C::swz(r)) * 16]) = next[i];
+      }
+      if (tid < RT) {
+        const bool live = next_lse != -INFINITY;
+        S.lse2[to][tid] = live ? next_lse * kLog2e : 0.0f;
+        S.see[to][tid] = !live ? 0 : next_see < keys ? next_see : keys;
+      }
+    };
+    load(0);
+
+    // this wave's keys
+    const int key0 = tile * C::kKeys + wave * (32 * KB);
+    u32x4 kf[KB][C::kFrags];
+    int number[KB];  // -1: the key does not exist
+#pragma unroll
+    for (int t = 0; t < KB; ++t) {
+      const int key = key0 + t * 32 + col;
       int64_t row = 0;
-      limit[t] = INT32_MAX;
+      number[t] = -1;
       if (key < keys) {
         const uint32_t pi = fast_div(a.c.page_div, (uint32_t)key);
         const int page = table[pi];
         if (names_page(a.c, held, key, page)) {
           row = (int64_t)page * a.c.page_stride +
                 (int64_t)(key - (int)(pi * a.c.page_div.d)) * a.c.token_stride;
-          limit[t] = key;
+          number[t] = key;
         }
       }
-      const char* p = a.c.k + row + (int64_t)h * a.c.head_stride + quad * 16;
+      const char* p = a.c.k + row + (int64_t)h * a.c.head_stride + half * 16;
 #pragma unroll
-      for (int s = 0; s < NF; ++s) kf[t][s] = *reinterpret_cast<const u32x4*>(p + s * 64);
+      for (int s = 0; s < C::kFrags; ++s) kf[t][s] = *reinterpret_cast<const u32x4*>(p + s * 32);
     }
-    float sum[KT];
+    float sum[KB];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) sum[t] = 0.0f;
-    int n = a.nodes ? a.nodes[b] : a.N;
-    n = n < 0 ? 0 : n < a.N ? n : a.N;
-    const int rows = n * a.G;
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-      const int r = r0 + col;
-      u32x4 qf[NF];
-      {
-        const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
-        const char* p = a.q.at + (int64_t)b * a.q.seq + (int64_t)node * a.q.node +
-                        (int64_t)(h * a.G + g) * a.q.head + quad * 16;
+    for (int t = 0; t < KB; ++t) sum[t] = 0.0f;
+
+    store(0);
+    __syncthreads();
+    int at = 0;
+    for (int r0 = 0; r0 < rows; r0 += RT, at ^= 1) {
+      const bool more = r0 + RT < rows;
+      if (more) load(r0 + RT);
+      const int see = S.see[at][lane % RT];
+      const bool open = __all(see >= key0 + 32 * KB);  // every row sees all of the wave's keys
+      if (__any(see > key0)) {
+#pragma unroll 1
+        for (int m = 0; m < RT; m += 32) {
+          if (r0 + m >= rows) break;
+          f32x16 z[KB];
+          u32x4 qf[C::kFrags];
+          const char* q = &S.q[at][(m + col) * C::kRow];
 #pragma unroll
-        for (int s = 0; s < NF; ++s)
-          qf[s] = r < rows ? *reinterpret_cast<const u32x4*>(p + s * 64) : u32x4{0, 0, 0, 0};
-      }
-      float lse2[4];
-      int see[4];  // keys that the row sees
+          for (int s = 0; s < C::kFrags; ++s)
+            qf[s] = *reinterpret_cast<const u32x4*>(q + ((2 * s + half) ^ C::swz(m + col)) * 16);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int rr = r0 + quad * 4 + e;
-        lse2[e] = 0.0f;
-        see[e] = 0;
-        if (rr < rows) {
-          const int node = (int)fast_div(a.g_div, (uint32_t)rr), g = rr - node * a.G;
-          const float x = a.lse[((int64_t)b * a.N + node) * ((int64_t)Hkv * a.G) + h * a.G + g];
-          const int s = a.seen ? a.seen[(int64_t)b * a.N + node] : INT32_MAX;
-          lse2[e] = x * kLog2e;
-          see[e] = x == -INFINITY ? 0 : s < keys ? s : keys;
-        }
-      }
+          for (int t = 0; t < KB; ++t) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int e = 0; e < 16; ++e) z[t][e] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < NF; ++s) {
-          if constexpr (BF16) {
-            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[s]),
-                                                        __builtin_bit_cast(bf16x8, kf[t][s]), z, 0,
-                                                        0, 0);
-          } else {
+            for (int s = 0; s < C::kFrags; ++s) {
+              if constexpr (BF16) {
+                z[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, qf[s]), __builtin_bit_cast(bf16x8, kf[t][s]), z[t],
+                    0, 0, 0);
+              } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              z = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(qf[s][e]),
-                                                       __uint_as_float(kf[t][s][e]), z, 0, 0, 0);
+                for (int e = 0; e < 4; ++e)
+                  z[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                      __uint_as_float(qf[s][e]), __uint_as_float(kf[t][s][e]), z[t], 0, 0, 0);
+              }
+            }
           }
-        }
+          // register e is row 8 (e / 4) + 4 half + e % 4
+          auto add = [&](auto all) __attribute__((always_inline)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = __builtin_amdgcn_exp2f(fmaf(z[e], sl2, -lse2[e]));
-          sum[t] += limit[t] < see[e] ? w : 0.0f;
+            for (int e = 0; e < 16; e += 4) {
+              const int r = m + 2 * e + 4 * half;
+              const f32x4 l = *reinterpret_cast<const f32x4*>(&S.lse2[at][r]);
+              const int4 see = *reinterpret_cast<const int4*>(&S.see[at][r]);
+              const int limit[4] = {see.x, see.y, see.z, see.w};
+#pragma unroll
+              for (int t = 0; t < KB; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float w = __builtin_amdgcn_exp2f(fmaf(z[t][e + i], sl2, -l[i]));
+                  sum[t] += decltype(all)::value || key0 + t * 32 + col < limit[i] ? w : 0.0f;
+                }
+            }
+          };
+          if (open) add(std::true_type{});
+          else add(std::false_type{});
         }
       }
+      if (more) store(at ^ 1);
+      __syncthreads();
     }
-    // the four lanes of a key, then lane 16 t + c has key c of block t
-    float mine = 0.0f;
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      float x = sum[t];
-      x += __shfl_xor(x, 16);
-      x += __shfl_xor(x, 32);
-      mine = quad == t ? x : mine;
-    }
-    const int key = tile * kKeys + lane;
-    if (lane < kKeys && key < keys) {
-      float* w = a.w + ((int64_t)b * Hkv + h) * a.length + key;
-      *w = a.decay == 0.0f ? mine : fmaf(a.decay, *w, mine);
+    for (int t = 0; t < KB; ++t) {
+      const float x = sum[t] + __shfl_xor(sum[t], 32);
+      const int key = key0 + t * 32 + col;
+      if (half == 0 && key < keys) {
+        float* w = a.w + ((int64_t)b * Hkv + h) * a.length + key;
+        const float mine = number[t] >= 0 ? x : 0.0f;
+        *w = a.decay == 0.0f ? mine : fmaf(a.decay, *w, mine);
+      }
     }
   }
 }
 
-template <bool BF16, int D, int KT>
-void launch(const WeighArgs& a, hipStream_t stream) {
+template <int Keys>
+unsigned grid_for(const WeighArgs& a, int waves_a_piece, int a_unit) {
+  const int most = a_unit * kAttnCus;  // all that run at once
   const int longest = a.c.cap < a.length ? a.c.cap : a.length;
-  const int64_t pieces =
-      (int64_t)a.c.seqs * a.c.kv_heads * ((longest + 16 * KT - 1) / (16 * KT));
-  const int64_t groups = (pieces + kWeighWaves - 1) / kWeighWaves;
-  const unsigned grid = (unsigned)(groups < kWeighWorkgroups ? groups : kWeighWorkgroups);
-  hipLaunchKernelGGL((k_weigh<BF16, D, KT>), dim3(grid), dim3(kWeighThreads), 0, stream, a);
+  const int64_t pieces = (int64_t)a.c.seqs * a.c.kv_heads * ((longest + Keys - 1) / Keys);
+  const int64_t groups = (pieces * waves_a_piece + kWeighWaves - 1) / kWeighWaves;
+  return (unsigned)(groups < most ? groups : most);
+}
+
+template <bool BF16, int D, int KB, int RT>
+void launch(const WeighArgs& a, hipStream_t stream) {
+  if ((int64_t)a.N * a.G > kFewRows) {
+    using C = Rows<BF16, D, KB, RT>;
+    hipLaunchKernelGGL((k_weigh_rows<BF16, D, KB, RT>),
+                       dim3(grid_for<C::kKeys>(a, kWeighWaves, C::kOcc)),
+                       dim3(kWeighThreads), 0, stream, a);
+    return;
+  }
+  using C = Few<BF16, D>;
+  hipLaunchKernelGGL((k_weigh<BF16, D>), dim3(grid_for<C::kKeys>(a, 1, C::kOcc)),
+                     dim3(kWeighThreads), 0, stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_cache_weigh(const WeighArgs& a, sv_dtype dt, hipStream_t stream) {
-  // 64 registers of keys a lane
   if (dt == SV_DTYPE_BF16) {
     switch (a.c.head_dim) {
-      case 64: launch<true, 64, 4>(a, stream); break;
-      case 96: launch<true, 96, 4>(a, stream); break;
-      case 128: launch<true, 128, 4>(a, stream); break;
-      default: launch<true, 256, 2>(a, stream);
+      case 64: launch<true, 64, 2, 64>(a, stream); break;
+      case 96: launch<true, 96, 2, 64>(a, stream); break;
+      case 128: launch<true, 128, 2, 64>(a, stream); break;
+      default: launch<true, 256, 1, 64>(a, stream);
     }
   } else {
     switch (a.c.head_dim) {
-      case 64: launch<false, 64, 4>(a, stream); break;
-      case 96: launch<false, 96, 2>(a, stream); break;
-      case 128: launch<false, 128, 2>(a, stream); break;
-      default: launch<false, 256, 1>(a, stream);
+      case 64: launch<false, 64, 2, 64>(a, stream); break;
+      case 96: launch<false, 96, 1, 64>(a, stream); break;
+      case 128: launch<false, 128, 1, 64>(a, stream); break;
+      default: launch<false, 256, 1, 32>(a, stream);
     }
   }
   return hipGetLastError();
