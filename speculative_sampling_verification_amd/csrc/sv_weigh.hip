@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "sv_lds_load.hpp"
 #include "sv_step.hpp"
 
 namespace sv {
@@ -27,7 +28,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
-constexpr int kFewRows = 16;  // rows a kv head up to which k_weigh is taken
+constexpr int kFewRows = 16;    // rows a kv head up to which k_weigh is taken
+constexpr int kSomeRows = 256;  // ... and k_weigh_rows with 32 keys a wave
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Keys of sequence b that are weighed.
@@ -41,11 +43,13 @@ __device__ __forceinline__ long long pieces_of(const WeighArgs& a, int b) {
   return (long long)a.c.kv_heads * ((keys_of(a, b) + Keys - 1) / Keys);
 }
 
-// Where piece `pos` lies: pieces of a sequence are ordered by key tile, then head.  Every thread of
-// the workgroup gets the sequence and the piece in it.
+// This workgroup's share of the pieces: as many as any other's, or one less.  Pieces of a sequence
+// are ordered by key tile, then head; *off is the first one's number in sequence *b.
+struct Share {
+  long long first, end;
+};
 template <int Keys>
-__device__ __forceinline__ void find_piece(const WeighArgs& a, long long* total, int* b_out,
-                                           long long* off_out) {
+__device__ __forceinline__ Share find_pieces(const WeighArgs& a, int* b_out, long long* off_out) {
   __shared__ long long scan[kWeighWaves];
   __shared__ int start_b;
   __shared__ long long start_off;
@@ -68,7 +72,8 @@ __device__ __forceinline__ void find_piece(const WeighArgs& a, long long* total,
     before += i < wave ? scan[i] : 0;
     all += scan[i];
   }
-  const long long per = (all + gridDim.x - 1) / gridDim.x, pos = per * blockIdx.x;
+  const long long each = all / gridDim.x, left = all - each * gridDim.x, w = blockIdx.x;
+  const long long pos = each * w + (w < left ? w : left);
   long long p = before + incl - mine;
   if (pos >= p && pos < p + mine) {
     int b = b0;
@@ -81,9 +86,9 @@ __device__ __forceinline__ void find_piece(const WeighArgs& a, long long* total,
     start_off = pos - p;
   }
   __syncthreads();
-  *total = all;
   *b_out = pos < all ? start_b : a.c.seqs;
   *off_out = pos < all ? start_off : 0;
+  return Share{pos, pos + each + (w < left ? 1 : 0)};
 }
 
 // Up to 16 rows: a wave takes KT blocks of 16 keys at a time.  Its pieces' loads form a line: while one
@@ -111,16 +116,14 @@ __global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(W
     int b, h, key0, keys, held;
   };
   // the wave's place in the line of pieces
-  long long total, off;
+  long long off;
   int b;
-  find_piece<C::kKeys>(a, &total, &b, &off);
+  const Share share = find_pieces<C::kKeys>(a, &b, &off);
   b = __builtin_amdgcn_readfirstlane(b);
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  long long pos = per * blockIdx.x + wave;
-  const long long last = per * (blockIdx.x + 1), end = last < total ? last : total;
+  long long pos = share.first + wave;
   off += wave;
   auto next_piece = [&](Piece& p) __attribute__((always_inline)) {
-    if (pos >= end) return false;
+    if (pos >= share.end) return false;
     int keys = keys_of(a, b);
     long long n = (long long)Hkv * ((keys + C::kKeys - 1) / C::kKeys);
     while (off >= n) {
@@ -264,8 +267,10 @@ struct Rows {
   static constexpr int kFrags = kChunks / 2;           // ... that a lane holds
   static constexpr int kKeys = 32 * KB * kWeighWaves;  // of a workgroup
   static constexpr int kLoads = RT * kChunks / kWeighThreads;  // pieces a thread loads a stage
-  // the keys of 1024-byte rows take half of the registers of two waves a SIMD
-  static constexpr int kOcc = kRow > 512 ? 1 : 2;
+  // workgroups a compute unit: what the registers of the keys and products leave room for
+  static constexpr int kKeyRegs = KB * kRow / 8;
+  static constexpr int kOcc = kKeyRegs > 64 ? 1 : kKeyRegs == 64 && KB == 1 ? 2
+                              : kKeyRegs > 32 ? 3 : 4;
   static_assert(RT % 32 == 0 && RT <= kWeighThreads && RT * kChunks % kWeighThreads == 0, "stage");
 
   // Piece c of row r lies at place c ^ swz(r): rows read together lie in different banks.
@@ -288,17 +293,18 @@ __attribute__((amdgpu_waves_per_eu(Rows<BF16, D, KB, RT>::kOcc, Rows<BF16, D, KB
 void k_weigh_rows(WeighArgs a) {
   using C = Rows<BF16, D, KB, RT>;
   __shared__ typename C::Lds S;
+  const uint32_t q_lds =
+      (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&S.q[0][0]);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const float sl2 = a.scale * kLog2e;
-  long long total, off;
+  long long off;
   int b;
-  find_piece<C::kKeys>(a, &total, &b, &off);
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long last = per * (blockIdx.x + 1), end = last < total ? last : total;
+  const Share share = find_pieces<C::kKeys>(a, &b, &off);
+  constexpr int kAhead = 2;
   const int Hkv = a.c.kv_heads;
-  for (long long pos = per * blockIdx.x; pos < end; ++pos, ++off) {
+  for (long long pos = share.first; pos < share.end; ++pos, ++off) {
     for (; b < a.c.seqs; ++b) {
       const long long n = pieces_of<C::kKeys>(a, b);
       if (off < n) break;
@@ -313,56 +319,52 @@ void k_weigh_rows(WeighArgs a) {
     n = n < 0 ? 0 : n < a.N ? n : a.N;
     const int rows = n * a.G;
 
-    // a stage of rows: on its way in registers, then in LDS
-    u32x4 next[C::kLoads];
-    float next_lse = 0.0f;
-    int next_see = 0;
-    // this thread's pieces and row; from stage to stage they are a fixed step apart where a node's
-    // heads do not straddle stages
+    // A stage of rows on its way to LDS.  Loads fill LDS in lane order, so a lane loads the piece that
+    // belongs at its place.  From stage to stage a thread's pieces are a fixed step apart where a
+    // node's heads do not straddle stages.  (Behind the last row: the first one's, which no key takes.)
     auto row_at = [&](int r, int c) __attribute__((always_inline)) {
       const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
       return a.q.at + (int64_t)b * a.q.seq + (int64_t)node * a.q.node +
              (int64_t)(h * a.G + g) * a.q.head + c * 16;
     };
     const bool even = RT % a.G == 0;
-    const int64_t step = even ? (int64_t)(RT / a.G) * a.q.node : 0;
+    const int64_t step = (int64_t)(RT / a.G) * a.q.node;
     const char* piece[C::kLoads];
 #pragma unroll
     for (int i = 0; i < C::kLoads; ++i) {
-      const int x = tid + i * kWeighThreads;
-      piece[i] = row_at(x / C::kChunks, x % C::kChunks);
+      const int x = tid + i * kWeighThreads, r = x / C::kChunks;
+      piece[i] = row_at(r, (x % C::kChunks) ^ C::swz(r)) - step;
     }
-    auto load = [&](int r0) __attribute__((always_inline)) {
+    float next_lse = 0.0f;
+    int next_see = 0;
+    auto load = [&](int r0, int to) __attribute__((always_inline)) {
       const bool whole = even && r0 + RT <= rows;
 #pragma unroll
       for (int i = 0; i < C::kLoads; ++i) {
-        const int x = tid + i * kWeighThreads, r = r0 + x / C::kChunks;
-        if (whole) next[i] = *reinterpret_cast<const u32x4*>(piece[i]);
-        else if (r < rows) next[i] = *reinterpret_cast<const u32x4*>(row_at(r, x % C::kChunks));
+        const int x = tid + i * kWeighThreads, r = x / C::kChunks;
         piece[i] += step;
+        const char* p = piece[i];
+        if (!whole) p = row_at(r0 + r < rows ? r0 + r : 0, (x % C::kChunks) ^ C::swz(r));
+        load_to_lds(p, q_lds + to * (RT * C::kRow) + wave * 1024 + i * (kWeighThreads * 16));
       }
-      next_lse = -INFINITY;
-      next_see = 0;
-      const int r = r0 + tid;
-      if (tid < RT && r < rows) {
-        const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
-        next_lse = a.lse[((int64_t)b * a.N + node) * ((int64_t)Hkv * a.G) + h * a.G + g];
-        next_see = a.seen ? a.seen[(int64_t)b * a.N + node] : INT32_MAX;
+      if (tid < RT) {
+        const int r = r0 + tid;
+        next_lse = -INFINITY;
+        if (r < rows) {
+          const int node = (int)fast_div(a.g_div, (uint32_t)r), g = r - node * a.G;
+          next_lse = a.lse[((int64_t)b * a.N + node) * ((int64_t)Hkv * a.G) + h * a.G + g];
+          next_see = a.seen ? a.seen[(int64_t)b * a.N + node] : INT32_MAX;
+        }
       }
     };
     auto store = [&](int to) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < C::kLoads; ++i) {
-        const int x = tid + i * kWeighThreads, r = x / C::kChunks, c = x % C::kChunks;
-        *reinterpret_cast<u32x4*>(&S.q[to][r * C::kRow + (c ^ C::swz(r)) * 16]) = next[i];
-      }
       if (tid < RT) {
         const bool live = next_lse != -INFINITY;
         S.lse2[to][tid] = live ? next_lse * kLog2e : 0.0f;
         S.see[to][tid] = !live ? 0 : next_see < keys ? next_see : keys;
       }
     };
-    load(0);
+    if (rows > 0) load(0, 0);
 
     // this wave's keys
     const int key0 = tile * C::kKeys + wave * (32 * KB);
@@ -391,11 +393,11 @@ void k_weigh_rows(WeighArgs a) {
     for (int t = 0; t < KB; ++t) sum[t] = 0.0f;
 
     store(0);
-    __syncthreads();
+    tile_barrier();
     int at = 0;
     for (int r0 = 0; r0 < rows; r0 += RT, at ^= 1) {
       const bool more = r0 + RT < rows;
-      if (more) load(r0 + RT);
+      if (more) load(r0 + RT, at ^ 1);
       const int see = S.see[at][lane % RT];
       const bool open = __all(see >= key0 + 32 * KB);  // every row sees all of the wave's keys
       if (__any(see > key0)) {
@@ -403,28 +405,35 @@ void k_weigh_rows(WeighArgs a) {
         for (int m = 0; m < RT; m += 32) {
           if (r0 + m >= rows) break;
           f32x16 z[KB];
-          u32x4 qf[C::kFrags];
+          u32x4 qf[kAhead];  // read from LDS that far ahead of the products
           const char* q = &S.q[at][(m + col) * C::kRow];
+          auto frag = [&](int s) __attribute__((always_inline)) {
+            return *reinterpret_cast<const u32x4*>(q + ((2 * s + half) ^ C::swz(col)) * 16);
+          };
 #pragma unroll
-          for (int s = 0; s < C::kFrags; ++s)
-            qf[s] = *reinterpret_cast<const u32x4*>(q + ((2 * s + half) ^ C::swz(m + col)) * 16);
+          for (int s = 0; s < kAhead; ++s) qf[s] = frag(s);
 #pragma unroll
-          for (int t = 0; t < KB; ++t) {
+          for (int t = 0; t < KB; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) z[t][e] = 0.0f;
 #pragma unroll
-            for (int s = 0; s < C::kFrags; ++s) {
+          for (int s = 0; s < C::kFrags; ++s) {
+#pragma unroll
+            for (int t = 0; t < KB; ++t) {
               if constexpr (BF16) {
                 z[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, qf[s]), __builtin_bit_cast(bf16x8, kf[t][s]), z[t],
-                    0, 0, 0);
+                    __builtin_bit_cast(bf16x8, qf[s % kAhead]),
+                    __builtin_bit_cast(bf16x8, kf[t][s]), z[t], 0, 0, 0);
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  z[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                      __uint_as_float(qf[s][e]), __uint_as_float(kf[t][s][e]), z[t], 0, 0, 0);
+                  z[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(qf[s % kAhead][e]),
+                                                              __uint_as_float(kf[t][s][e]), z[t],
+                                                              0, 0, 0);
               }
             }
+            if (s + kAhead < C::kFrags) qf[s % kAhead] = frag(s + kAhead);
+            __builtin_amdgcn_sched_barrier(0);  // the order as it stands
           }
           // register e is row 8 (e / 4) + 4 half + e % 4
           auto add = [&](auto all) __attribute__((always_inline)) {
@@ -448,7 +457,7 @@ void k_weigh_rows(WeighArgs a) {
         }
       }
       if (more) store(at ^ 1);
-      __syncthreads();
+      tile_barrier();
     }
 #pragma unroll
     for (int t = 0; t < KB; ++t) {
@@ -473,13 +482,18 @@ unsigned grid_for(const WeighArgs& a, int waves_a_piece, int a_unit) {
 }
 
 template <bool BF16, int D, int KB, int RT>
+void launch_rows(const WeighArgs& a, hipStream_t stream) {
+  using C = Rows<BF16, D, KB, RT>;
+  hipLaunchKernelGGL((k_weigh_rows<BF16, D, KB, RT>),
+                     dim3(grid_for<C::kKeys>(a, kWeighWaves, C::kOcc)), dim3(kWeighThreads), 0,
+                     stream, a);
+}
+
+template <bool BF16, int D, int KB, int RT>
 void launch(const WeighArgs& a, hipStream_t stream) {
   if ((int64_t)a.N * a.G > kFewRows) {
-    using C = Rows<BF16, D, KB, RT>;
-    hipLaunchKernelGGL((k_weigh_rows<BF16, D, KB, RT>),
-                       dim3(grid_for<C::kKeys>(a, kWeighWaves, C::kOcc)),
-                       dim3(kWeighThreads), 0, stream, a);
-    return;
+    if (KB > 1 && (int64_t)a.N * a.G <= kSomeRows) return launch_rows<BF16, D, 1, RT>(a, stream);
+    return launch_rows<BF16, D, KB, RT>(a, stream);
   }
   using C = Few<BF16, D>;
   hipLaunchKernelGGL((k_weigh<BF16, D>), dim3(grid_for<C::kKeys>(a, 1, C::kOcc)),
