@@ -592,6 +592,14 @@ def _new_like(t, stream):
         return torch.empty_like(t)
 
 
+def _new(shape, dtype, device, stream):
+    """An output tensor of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _arg(t, name, cache, dtype, shape):
     """The address of an optional contiguous tensor argument on the cache's device."""
     if t is None:
@@ -804,8 +812,7 @@ def _turned_out(t, name, strides, given, stream):
     if given is None:
         if strides is None:
             return _new_like(t, stream)
-        with torch.cuda.stream(stream):  # None: the current one
-            return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return _new(t.shape, t.dtype, t.device, stream)
     if not isinstance(given, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if given.data_ptr() == t.data_ptr() and given.dtype is t.dtype and \
@@ -952,8 +959,7 @@ def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, 
     if "weights" not in out:
         out["weights"] = _new_like(weights, stream)
     if "kept" not in out:
-        with torch.cuda.stream(stream):  # None: the current one
-            out["kept"] = torch.empty(kept_shape, dtype=torch.int32, device=cache.device)
+        out["kept"] = _new(kept_shape, torch.int32, cache.device, stream)
     _cache_call(cache, "spec_cache_evict", _lib.spec_cache_evict, cache._ref, weights_at, length,
                 keep_at, max_keep, sinks, recent,
                 _arg(out["weights"], "out weights", cache, torch.float32, weights.shape),
