@@ -34,6 +34,7 @@ int spec_token_logprobs(const void* logits, sv_dtype dtype, int num_rows, int V,
   const int es = dtype == SV_DTYPE_BF16 ? 2 : 4;
   if (!logits || num_rows < 1 || !shape_ok(R, V, top_n) || (!rows && R != num_rows))
     return SV_ERR_INVALID_ARG;
+  if ((uint64_t)num_rows * V > (uint64_t)1 << 60) return SV_ERR_INVALID_ARG;  // no memory holds them
   const double c = 1.44269504088896340736 / (double)temperature;
   if (!(temperature > 0.0f) || !std::isfinite(temperature) || !(c > 0.0) ||
       !std::isfinite((float)c) || (float)c == 0.0f)

@@ -50,7 +50,9 @@ bool parts_apart(const void* a, const Rows& x, const void* b, const Rows& y) {
   const int64_t gap = p < q ? q - p : p - q;
   if (gap < (p < q ? span_x : span_y)) return false;
   const int64_t stride[2] = {x.s[0], x.s[1]}, size[2] = {x.size[0], x.size[1]};
-  return rows_apart(gap + (p < q ? span_y : span_x), stride, size);
+  int64_t both;
+  return !__builtin_add_overflow(gap, p < q ? span_y : span_x, &both) &&
+         rows_apart(both, stride, size);
 }
 
 bool in_place_ok(const Rows& x) {
