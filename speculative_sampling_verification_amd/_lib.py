@@ -9,6 +9,7 @@ missing the import fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -530,6 +531,7 @@ class PagedCache:
                 with them the other calls leave alone what another sequence holds by now
     """
 
+    _what = "cache is"
     _FIXED = frozenset(("k", "v", "page_table", "seq_lens", "seq_pages", "refcount", "device", "dtype",
                         "layers", "pages", "page_size", "kv_heads", "head_dim", "seqs"))
 
@@ -614,10 +616,10 @@ def _raw_stream(cache, stream):
     """The handle of the stream to launch on.  The lookup behind torch.cuda.current_stream, as
     these calls are short enough for a Stream object to show."""
     if cache._index is None:
-        raise ValueError(f"the cache is on {cache.device}, expected a GPU")
+        raise ValueError(f"the {cache._what} on {cache.device}, expected a GPU")
     if stream is not None:
         if stream.device != cache.device:
-            raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+            raise ValueError(f"the stream is on {stream.device}, the {cache._what} on {cache.device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(cache._index)
 
@@ -640,7 +642,9 @@ def _cache_call(cache, name, fn, *args):
 
 
 class _Place:
-    """Where a call without a cache runs: what the helpers above ask of a PagedCache."""
+    """Where a call without a cache runs: what the helpers here ask of a PagedCache."""
+
+    _what = "tensors are"
 
     def __init__(self, device):
         self.device, self._index = device, device.index
@@ -797,6 +801,8 @@ def rotary_frequencies(rot_dim, *, theta=10000.0, scaling=None, factor=1.0, orig
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {list(ROTARY_SCALINGS)}, got {scaling!r}")
     rot_dim = int(rot_dim)
+    if not 0 < rot_dim <= 4096:
+        raise SpecVerifyError("spec_rotary_frequencies", 1)
     freq = (ctypes.c_double * max(1, rot_dim // 2))()
     amplitude = ctypes.c_float()
     code = _lib.spec_rotary_frequencies(rot_dim, float(theta), ROTARY_SCALINGS[scaling],
@@ -968,6 +974,14 @@ def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, 
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _logprob_workspace(R, V, dt, top_n):
+    need = _lib.spec_token_logprobs_workspace_size(R, V, dt, top_n)
+    if need == 0:
+        raise SpecVerifyError("spec_token_logprobs_workspace_size", 1)
+    return need
+
+
 def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_n=0,
                         want_rank=False, want_entropy=False, out=None, stream=None):
     """Log probabilities of tokens under softmax(logits / temperature) (see include/spec_verify.h).
@@ -1003,9 +1017,7 @@ def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_
     if V < 1 or max(R, logits.numel() // V) >= 2**31:
         raise ValueError(f"logits {tuple(logits.shape)} for {R} tokens is out of range")
     raw = _raw_stream(place, None)
-    need = _lib.spec_token_logprobs_workspace_size(R, V, dt, top_n)
-    if need == 0:
-        raise SpecVerifyError("spec_token_logprobs_workspace_size", 1)
+    need = _logprob_workspace(R, V, dt, top_n)
     out = dict(out) if out else {}
     at = {}
 

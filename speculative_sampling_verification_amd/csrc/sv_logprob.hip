@@ -26,7 +26,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVecs = 8;              // vectors a thread and tile
+constexpr int kVecs = 4;              // vectors a thread and tile
 constexpr int kTile = kThreads * kVecs;
 constexpr int kSpare = 48;            // vectors a wave keeps beyond n until it cuts its list
 constexpr int kList = kLogprobMaxTop + kSpare + 64 * kVecs;
@@ -254,7 +254,7 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 }
 
 template <bool BF16, bool Entropy, bool Rank, bool Top>
-__global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
+__global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   using R = Row<BF16>;
   constexpr int kPer = R::kPer;
   __shared__ Lds s;
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_logprob(LogprobArgs a) {
     return __builtin_nontemporal_load(&vecs[j < v1 ? j : v1 - 1]);
   };
 
-  // One tile.  A vector's registers take the next tile's as soon as it is done, so that 8 KB a wave
+  // One tile.  A vector's registers take the next tile's as soon as it is done, so that 4 KB a wave
   // are always on their way.  The sums are formed at the shift as it is, and again (`redo`) where
   // that does not do.  Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and
   // far shifts are subtracted first.
