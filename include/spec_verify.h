@@ -464,9 +464,10 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* ds
  *               (NULL if top_n is 0).  A logit of -inf is no alternative: where there are fewer than
  *               top_n others, the rest holds -1 and -inf
  * A token outside [0, V) has log probability -inf and rank -1.  A row outside [0, num_rows), or
- * without a finite logit, has no distribution: -inf, entropy 0, no alternatives.  Sums are in fp32
- * a thread and joined in 64 bits.  Outputs and workspace share no memory with each other or the
- * inputs.
+ * without a finite logit, has no distribution: -inf, entropy 0, no alternatives.  What a row with a
+ * logit of NaN or +inf gets is not defined (tokens stay in [-1, V)); it touches no other row.  Sums
+ * are in fp32 a thread and joined in 64 bits.  Outputs and workspace share no memory with each other
+ * or the inputs.
  */
 size_t spec_token_logprobs_workspace_size(int R, int V, sv_dtype dtype, int top_n);
 int spec_token_logprobs(const void* logits, sv_dtype dtype, int num_rows, int V,
@@ -488,7 +489,7 @@ int spec_token_logprobs(const void* logits, sv_dtype dtype, int num_rows, int V,
  * so that a tree's nodes are given their depths (spec_build_tree's out_depth) and a chain nothing;
  * positions may be negative: the turn of -t undoes that of t, and is its gradient.  Positions are
  * not slots: after spec_cache_evict a sequence's next position is still the number of tokens
- * before it.  Angles are brought to their remainder in 64 bits, so far positions lose nothing;
+ * before it.  Angles are formed and brought to their remainder in 64 bits (off by 2^-51 of the angle);
  * sums are in fp32, results rounded once.
  * ---------------------------------------------------------------------------------------------
  */
@@ -593,7 +594,8 @@ int spec_cache_weigh(const void* q, const int64_t* q_strides, int N, int q_heads
  *               another sequence too.  Stored by spec_cache_resize
  *   out_kept    [layers, seqs, kv_heads, max_keep]: former position of each token kept, -1 behind
  *               the last; all -1 where the sequence was left alone
- * Apart from out_weights, what is written shares no memory with the other arrays.
+ * Without refcount, the pages that are written have to be the sequence's own.  Apart from
+ * out_weights, what is written shares no memory with the other arrays.
  */
 int spec_cache_evict(const sv_cache* cache, const float* weights, int length, const int32_t* keep,
                      int max_keep, int sinks, int recent, float* out_weights, int32_t* out_lens,

@@ -821,8 +821,10 @@ def _turned_out(t, name, strides, given, stream):
         return _new(t.shape, t.dtype, t.device, stream)
     if not isinstance(given, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if given.data_ptr() == t.data_ptr() and given.dtype is t.dtype and \
-            given.shape == t.shape and given.stride() == t.stride():
+    if given.data_ptr() == t.data_ptr() and given.dtype is t.dtype and given.shape == t.shape:
+        # in place: where rows lie is then said once, by t's strides
+        if any(n > 1 and x != y for n, x, y in zip(t.shape, given.stride(), t.stride())):
+            raise ValueError(f"{name} shares memory with the rows that it is made of")
         return given
     _need(given, name, t.device, t.dtype, t.shape)
     return given

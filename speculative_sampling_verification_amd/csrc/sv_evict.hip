@@ -40,6 +40,12 @@ __device__ __forceinline__ void all_read() {
   __syncthreads();
 }
 
+// Workgroups go to the 8 XCDs in turn: gives each of these a stretch of the `count` units.
+__device__ __forceinline__ int64_t xcd_order(int64_t unit, int64_t count) {
+  const int64_t each = count / 8;
+  return unit < 8 * each ? (unit & 7) * each + (unit >> 3) : unit;
+}
+
 struct Lds {
   int hist[kBins];
   float held[kHeld];
@@ -183,11 +189,18 @@ __device__ __forceinline__ void list_largest(Lds& s, const float* x, int m, int 
   });
 }
 
+// One workgroup a (layer, sequence, head).  The weights come from memory once, into LDS; what remains
+// are the passes over them there: 32 layers, 16 sequences of up to 4096 tokens, 8 heads (4096
+// workgroups) take 103 us; 12 layers of one sequence of 200 tokens 8 us, latency alone.  Weights read
+// from memory in each pass, as where more than kHeld are looked at: 883 us for selection and move
+// together against 857.  256 threads 911, 1024 threads 1017; keys in registers instead of weights in
+// LDS spill (965).
 __global__ __launch_bounds__(kThreads, 6) void k_evict_select(EvictArgs a, int64_t groups) {
   __shared__ Lds s;
   const CacheView& c = a.c;
   const int tid = threadIdx.x;
-  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {  // (layer, sequence, head)
+  for (int64_t unit = blockIdx.x; unit < groups; unit += gridDim.x) {
+    const int64_t group = xcd_order(unit, groups);  // (layer, sequence, head)
     const int64_t lb = group / c.kv_heads;
     const int b = (int)(lb % c.seqs);
     const float* w = a.w + group * a.length;
@@ -242,14 +255,19 @@ __global__ __launch_bounds__(kThreads, 6) void k_evict_select(EvictArgs a, int64
   }
 }
 
-// One workgroup for the keys or the values of a (layer, sequence, head).
+// One workgroup for the keys or the values of a (layer, sequence, head).  Bound by memory: rows of
+// 256 bytes, each read and written once: 3.6 GB in 754 us, 4.8 TB/s (a large copy: 5.2).  Rounds of
+// four rows a thread; of two 912 us for selection and move together against 857, of eight (registers
+// leave fewer waves) 1190.  Moving in the selection's own launch, a sequence's rows behind its own
+// selection, took 937: the selection's LDS then holds back the waves that move.
 __global__ __launch_bounds__(kThreads) void k_evict_move(EvictArgs a, int64_t groups,
                                                          FastDiv row_div) {
   const CacheView& c = a.c;
   const int tid = threadIdx.x;
   const int vecs = (int)row_div.d, step = kThreads / vecs;  // rows that the threads cover
   const int my = (int)fast_div(row_div, (uint32_t)tid), at = (tid - my * vecs) * 16;
-  for (int64_t x = blockIdx.x; x < 2 * groups; x += gridDim.x) {
+  for (int64_t unit = blockIdx.x; unit < 2 * groups; unit += gridDim.x) {
+    const int64_t x = xcd_order(unit, 2 * groups);
     const int64_t group = x >> 1;
     const int32_t* kept = a.kept + group * a.max_keep;
     const int64_t lb = group / c.kv_heads;
@@ -263,20 +281,31 @@ __global__ __launch_bounds__(kThreads) void k_evict_move(EvictArgs a, int64_t gr
       return base + (int64_t)table[pi] * c.page_stride +
              (int64_t)(pos - (int)(pi * c.page_div.d)) * c.token_stride;
     };
-    for (int j0 = a.sinks; j0 < want; j0 += kMoveRows * step) {
-      u32x4 r[kMoveRows];
-      int from[kMoveRows];
+    // a round's rows are known a round ahead: from[] is nullptr where there is nothing to move
+    const char *from[kMoveRows], *next[kMoveRows];
+    auto find = [&](int j0, const char* (&at)[kMoveRows]) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kMoveRows; ++i) {
-        const int j = j0 + i * step + my;
-        from[i] = my < step && j < want ? kept[j] : j;
-        if (from[i] != j) r[i] = *reinterpret_cast<const u32x4*>(row(from[i]));
+        const int j = j0 + i * step + my, k = my < step && j < want ? kept[j] : j;
+        at[i] = k != j ? row(k) : nullptr;
       }
+    };
+    find(a.sinks, from);
+    for (int j0 = a.sinks; j0 < want; j0 += kMoveRows * step) {
+      u32x4 r[kMoveRows];
+      char* to[kMoveRows];
+#pragma unroll
+      for (int i = 0; i < kMoveRows; ++i)
+        if (from[i]) r[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from[i]));
+#pragma unroll
+      for (int i = 0; i < kMoveRows; ++i)
+        if (from[i]) to[i] = row(j0 + i * step + my);
+      find(j0 + kMoveRows * step, next);
       all_read();
 #pragma unroll
       for (int i = 0; i < kMoveRows; ++i) {
-        const int j = j0 + i * step + my;
-        if (from[i] != j) *reinterpret_cast<u32x4*>(row(j)) = r[i];
+        if (from[i]) __builtin_nontemporal_store(r[i], reinterpret_cast<u32x4*>(to[i]));
+        from[i] = next[i];
       }
     }
   }

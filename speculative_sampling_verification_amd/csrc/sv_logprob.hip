@@ -253,6 +253,12 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
   return i >= 0 && i < a.num_rows ? i : -1;
 }
 
+// One workgroup a row, or part of one.  Bound by memory: 2048 rows of 128256 bf16 logits (525 MB) take
+// 95 us, 5.5 TB/s, 512 rows of 256000 in fp32 87 us, 6.0 (a large copy runs at 5.2, a sum over 2 GiB
+// at 4.0).  Loads pass the caches (nothing is read twice).  4 KB on their way a wave and six waves a
+// SIMD; 8 KB at four 100 and 95 us, loads of a whole tile ahead of its arithmetic 103.  Rows in
+// stretches an XCD made no difference.  With logits decoded again for the maximum, the sums, the rank
+// and the alternatives the same pass took 464 us.
 template <bool BF16, bool Entropy, bool Rank, bool Top>
 __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   using R = Row<BF16>;
@@ -559,8 +565,11 @@ LogprobPlan plan_logprobs(int R, int V, sv_dtype dt, int n) {
   const int per = dt == SV_DTYPE_BF16 ? 8 : 4;
   const int64_t vecs = V / per > 1 ? V / per : 1;  // whole ones of a row, at most
   const int64_t tiles = (vecs + kTile - 1) / kTile;
-  // two workgroups a compute unit, a tile each at least
-  int64_t parts = (512 + (int64_t)R - 1) / R;
+  // Rows of their own workgroup from one a compute unit on, else parts of them, a tile each at
+  // least, for two.  128256 bf16 (32000 fp32) logits a row, both launches in a graph: 64 rows at two
+  // workgroups a unit 26.3 (25.6) us, at one 27.5 (24.2), at four 29.6 (25.4); 128 rows 29.3 (25.1),
+  // 33.1 (27.4), 29.7 (28.2); 256 rows in one part each 33.0 (21.3), in two 36.7 (29.1).
+  int64_t parts = R >= 256 ? 1 : (512 + (int64_t)R - 1) / R;
   parts = parts < tiles ? parts : tiles;
   parts = parts < kMaxParts ? parts : kMaxParts;
   const int64_t each = (tiles + parts - 1) / parts;

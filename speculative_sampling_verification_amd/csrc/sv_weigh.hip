@@ -28,8 +28,17 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
-constexpr int kFewRows = 16;    // rows a kv head up to which k_weigh is taken
-constexpr int kSomeRows = 256;  // ... and k_weigh_rows with 32 keys a wave
+// Rows a kv head up to which k_weigh is taken, the one matrix instruction's: one token of 32 query
+// heads to 8 kv heads of 128 in 64 sequences of up to 8191 tokens takes 128 us (k_weigh_rows 155),
+// 16 rows in 32 sequences of up to 4096 31 us (39); 17 rows there 37.
+constexpr int kFewRows = 16;
+// Rows up to which k_weigh_rows has 32 keys of 256 bytes a wave, 64 beyond.  One sequence of 131072
+// tokens, 8 kv heads, 32 keys (64): 24 rows 62 us (66), 64 rows 62 (67), 128 rows 76 (79), 160 rows
+// 92 (90), 256 rows 114 (109), 512 rows 195 (180).  Shorter keys always go 64 a wave (of 128 bytes:
+// 24 rows 34 us, 41 with 32; of 192: 48, 51), longer ones 32 (64 do not fit the registers); fp32 of
+// 256 bytes, where products take the time, 32 (64 and 32 alike on long sequences, 70 us against 58 for
+// 256 rows in 16 sequences of 2048).
+constexpr int kSomeRows = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Keys of sequence b that are weighed.
@@ -94,6 +103,12 @@ __device__ __forceinline__ Share find_pieces(const WeighArgs& a, int* b_out, lon
 // Up to 16 rows: a wave takes KT blocks of 16 keys at a time.  Its pieces' loads form a line: while one
 // piece is computed the next one's keys and queries are on their way, and the page numbers of the one
 // after that before them (loads come back in order, so none waits for a younger one).
+//
+// Bound by the keys' bytes: each is read once, 16 products of a matrix instruction on it take less
+// time than its load.  Pieces of a page a workgroup, loaded and computed one after the other, took
+// 179 us where this takes 128 (620 MB of bf16 keys, 4.85 TB/s; a large copy runs at 5.2).  Three
+// workgroups a compute unit as the registers of the line allow, and no more than run at once: a
+// fourth waiting its turn made it 179.  Keys loaded past the caches: 139.
 template <bool BF16, int D>
 struct Few {
   static constexpr int kRow = D * (BF16 ? 2 : 4);
@@ -257,8 +272,16 @@ __global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(W
   }
 }
 
-// Many rows: a workgroup takes 32 KB keys, 32 (KB a wave) at a time in registers, and all rows come
-// by through LDS, RT at a time, two stages of them.
+// Many rows: a workgroup takes 128 KB keys, a wave 32 KB of them in registers, and all rows come by
+// through LDS, RT at a time, two stages of them.  Products are 32x32 instructions: half the reads
+// from LDS that 16x16 ones need for as many products.
+//
+// Bound by the matrix instructions and, between them, an exponential a product of 2 D operations: 64
+// nodes of 64 query heads to 8 kv heads of 128 on 131072 tokens (512 rows) take 180 us, 775 TFLOP/s,
+// and 256 nodes 616 us, 903 (a library product of 8192^3 runs at 1350).  Rows staged through
+// registers took 209 us, with one workgroup a compute unit less 204; 128 rows a stage 272; products of
+// the next 32 rows begun before the last ones' exponentials 217 (registers spill); four workgroups
+// a unit 218.  The exponentials of one wave run beside the products of the others.
 template <bool BF16, int D, int KB, int RT>
 struct Rows {
   static constexpr int kES = BF16 ? 2 : 4;
@@ -491,8 +514,10 @@ void launch_rows(const WeighArgs& a, hipStream_t stream) {
 
 template <bool BF16, int D, int KB, int RT>
 void launch(const WeighArgs& a, hipStream_t stream) {
+  constexpr bool kWide = KB > 1 && Rows<BF16, D, KB, RT>::kRow >= 256;
   if ((int64_t)a.N * a.G > kFewRows) {
-    if (KB > 1 && (int64_t)a.N * a.G <= kSomeRows) return launch_rows<BF16, D, 1, RT>(a, stream);
+    if constexpr (kWide)
+      if ((int64_t)a.N * a.G <= kSomeRows) return launch_rows<BF16, D, 1, RT>(a, stream);
     return launch_rows<BF16, D, KB, RT>(a, stream);
   }
   using C = Few<BF16, D>;
@@ -512,7 +537,7 @@ hipError_t launch_cache_weigh(const WeighArgs& a, sv_dtype dt, hipStream_t strea
     }
   } else {
     switch (a.c.head_dim) {
-      case 64: launch<false, 64, 2, 64>(a, stream); break;
+      case 64: launch<false, 64, 1, 64>(a, stream); break;
       case 96: launch<false, 96, 1, 64>(a, stream); break;
       case 128: launch<false, 128, 1, 64>(a, stream); break;
       default: launch<false, 256, 1, 32>(a, stream);

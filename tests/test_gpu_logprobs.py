@@ -150,6 +150,25 @@ def test_rows_without_a_distribution(svm):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [300, 150001])
+def test_rows_of_nan_and_infinity_touch_no_other(svm, V, dtype):
+    announce(f"rows with NaN and +inf beside others, V={V} {dtype}")
+    rng = np.random.default_rng(V)
+    z = logits_of(rng, 6, V, dtype, "peaked")
+    bad, good = [0, 2, 4], [1, 3, 5]
+    z[0, V // 3] = torch.nan
+    z[2, [0, V - 1]] = torch.inf
+    z[4] = torch.nan
+    tokens = rng.integers(0, V, 6).astype(np.int32)
+    got = svm.spec_token_logprobs(z.cuda(), ints(tokens), top_n=64, want_rank=True,
+                                  want_entropy=True)
+    ref = O.token_logprobs(z[good].double().numpy(), tokens[good], top_n=64)
+    check({k: x[good] for k, x in got.items()}, ref, V, 1.0)
+    top = got["top_tokens"][bad]
+    assert ((top >= -1) & (top < V)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_what_is_not_wanted_changes_nothing(svm, dtype):
     announce(f"logprobs: subsets of the outputs, shapes, {dtype}")
     rng = np.random.default_rng(4)

@@ -121,6 +121,21 @@ def test_strided_parts_of_one_product_in_place(svm, interleaved):
         check(host(got), host(x), at, freq, interleaved, 1.0, "f32")
 
 
+def test_out_of_other_rows_at_the_same_place(svm):
+    announce("a dense out that begins where a strided q does")
+    qkv = normal(np.random.default_rng(6), (2, 3, 4, 64), "f32")
+    freq = table(O.rotary_frequencies(64)[0])
+    q = qkv[:, :, :2]
+    with pytest.raises(ValueError):
+        svm.spec_rotary(q, freq, out={"q": qkv.view(-1)[:q.numel()].view(q.shape)})
+    # strides that move nothing may differ
+    one = qkv[:, :1, :1]
+    want = svm.spec_rotary(one, freq, base=ints(np.array([5, 9], dtype=np.int32)))["q"]
+    same = qkv.as_strided(one.shape, (one.stride(0), 64, 64, 1))
+    svm.spec_rotary(one, freq, base=ints(np.array([5, 9], dtype=np.int32)), out={"q": same})
+    assert torch.equal(one, want)
+
+
 def test_turn_back(svm):
     announce("the turn of -t undoes that of t")
     rng = np.random.default_rng(6)
