@@ -255,9 +255,11 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 
 // One workgroup a row, or part of one.  Bound by memory: 2048 rows of 128256 bf16 logits (525 MB) take
 // 95 us, 5.5 TB/s, 512 rows of 256000 in fp32 87 us, 6.0 (a large copy runs at 5.2, a sum over 2 GiB
-// at 4.0).  Loads pass the caches (nothing is read twice).  4 KB on their way a wave and six waves a
-// SIMD; 8 KB at four 100 and 95 us, loads of a whole tile ahead of its arithmetic 103.  Rows in
-// stretches an XCD made no difference.  With logits decoded again for the maximum, the sums, the rank
+// at 4.0).  Loads pass the caches, as nothing is read twice (else 110 and 101 us).  4 KB on their way a
+// wave and six to eight waves a SIMD; 2 KB 101 and 120 us, 8 KB at four waves 100 and 95, loads of a
+// whole tile ahead of its arithmetic 103.  Rows in stretches an XCD: no difference.  In bf16 the
+// exponential and five more instructions a logit take two thirds of that time beside the loads: 2048
+// rows of 32000, 1195 different ones, take 26 us.  With logits decoded again for the maximum, the sums, the rank
 // and the alternatives the same pass took 464 us.
 template <bool BF16, bool Entropy, bool Rank, bool Top>
 __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
