@@ -43,5 +43,8 @@ def test_loads_to_lds(assembly):
 @pytest.mark.timeout(700)
 def test_kernels_call_nothing(assembly):
     code = "\n".join(x for x in assembly.splitlines() if not x.lstrip().startswith((".", ";")))
-    assert len(re.findall(r"^_ZN.*k_weigh.*:", code, re.M)) >= 20
+    # of both types and four head sizes each
+    for name in ("k_weigh", "k_weigh_rows"):
+        found = re.findall(rf"^_ZN\w*\d{name}ILb([01])ELi(\d+)E\w*:", code, re.M)
+        assert set(found) == {(t, d) for t in "01" for d in ("64", "96", "128", "256")}
     assert not re.search(r"\b(s_swappc|s_call|flat_(load|store|atomic))", code)
