@@ -191,7 +191,7 @@ __device__ __forceinline__ void list_largest(Lds& s, const float* x, int m, int 
 
 // One workgroup a (layer, sequence, head).  The weights come from memory once, into LDS; what remains
 // are the passes over them there: 32 layers, 16 sequences of up to 4096 tokens, 8 heads (4096
-// workgroups) take 103 us, 12 of them for the second and third histogram; 12 layers of one sequence of
+// workgroups) take 80 us, 12 of them for the second and third histogram; 12 layers of one sequence of
 // 200 tokens 8 us, latency alone.  Weights read from memory in each pass, as where more than kHeld
 // are looked at, take 26 us more; 256 threads 53 more; keys in registers instead of weights in LDS
 // spill, 1024 threads leave too few waves.  Several histograms, so that fewer lanes meet in a bin, and a
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_evict_select(EvictArgs a, int64
 }
 
 // One workgroup for the keys or the values of a (layer, sequence, head).  Bound by memory: rows of
-// 256 bytes, each read and written once, 3.4 GB in 672 us, 5.1 TB/s (a large copy: 5.2).  Selection
+// 256 bytes, each read and written once, 3.4 GB in 697 us, 4.9 TB/s (a large copy: 5.2).  Selection
 // and move together: loads and stores past the caches, as no row is needed again, 859 -> 817 us, the
 // heads of a token on one XCD at about the same time -> 795, rows known a round ahead -> 775.  Four
 // rows a thread in flight; two 783, five 779, eight, before that, 1039 against 802 (registers leave
