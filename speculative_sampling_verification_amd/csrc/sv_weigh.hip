@@ -30,7 +30,7 @@ constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
 // Rows a kv head up to which k_weigh is taken, the one matrix instruction's: one token of 32 query
 // heads to 8 kv heads of 128 in 64 sequences of up to 8191 tokens takes 128 us (k_weigh_rows 155),
-// 16 rows in 32 sequences of up to 4096 31 us (39); 17 rows there 37.
+// 16 rows in 32 sequences of up to 4096 31 us (38); 20 rows there 35.
 constexpr int kFewRows = 16;
 // Rows up to which k_weigh_rows has 32 keys of 256 bytes a wave, 64 beyond.  One sequence of 131072
 // tokens, 8 kv heads, 32 keys (64): 24 rows 62 us (66), 64 rows 62 (67), 128 rows 76 (79), 160 rows
@@ -296,6 +296,10 @@ struct Rows {
   static constexpr int kKeyRegs = KB * kRow / 8;
   static constexpr int kOcc = kKeyRegs > 64 ? 1 : kKeyRegs == 64 && KB == 1 ? 2
                               : kKeyRegs > 32 ? 3 : 4;
+  // Whether the weights so far come with the keys: 20 rows of 32 sequences of up to 4096 tokens and 8
+  // heads of 128 in bf16 37.2 -> 35.2 us, 64 rows 39.1 -> 36.9; with 64 keys of 256 bytes a wave more
+  // registers spill (256 rows 72.8 -> 74.6), in fp32 too (64 rows 145 -> 150).
+  static constexpr bool kEarly = BF16 && (KB == 1 || kKeyRegs < 64);
   static_assert(RT % 32 == 0 && RT <= kWeighThreads && RT * kChunks % kWeighThreads == 0, "stage");
 
   // Piece c of row r lies at place c ^ swz(r): rows read together lie in different banks.
@@ -413,9 +417,14 @@ void k_weigh_rows(WeighArgs a) {
 #pragma unroll
       for (int s = 0; s < C::kFrags; ++s) kf[t][s] = *reinterpret_cast<const u32x4*>(p + s * 32);
     }
-    float sum[KB];
+    float* w = a.w + ((int64_t)b * Hkv + h) * a.length + key0 + col;
+    float sum[KB], old[KB];
 #pragma unroll
-    for (int t = 0; t < KB; ++t) sum[t] = 0.0f;
+    for (int t = 0; t < KB; ++t) {
+      sum[t] = old[t] = 0.0f;
+      if (C::kEarly && a.decay != 0.0f && half == 0 && key0 + t * 32 + col < keys)
+        old[t] = w[t * 32];
+    }
 
     store(0);
     tile_barrier();
@@ -487,11 +496,9 @@ void k_weigh_rows(WeighArgs a) {
 #pragma unroll
     for (int t = 0; t < KB; ++t) {
       const float x = sum[t] + __shfl_xor(sum[t], 32);
-      const int key = key0 + t * 32 + col;
-      if (half == 0 && key < keys) {
-        float* w = a.w + ((int64_t)b * Hkv + h) * a.length + key;
+      if (half == 0 && key0 + t * 32 + col < keys) {
         const float mine = number[t] >= 0 ? x : 0.0f;
-        *w = a.decay == 0.0f ? mine : fmaf(a.decay, *w, mine);
+        w[t * 32] = a.decay == 0.0f ? mine : fmaf(a.decay, C::kEarly ? old[t] : w[t * 32], mine);
       }
     }
   }
