@@ -258,8 +258,8 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 // at 4.0).  Loads pass the caches, as nothing is read twice (else 110 and 101 us).  4 KB on their way a
 // wave and six to eight waves a SIMD; 2 KB 101 and 120 us, 8 KB at four waves 100 and 95, loads of a
 // whole tile ahead of its arithmetic 103.  Rows in stretches an XCD: no difference.  In bf16 the
-// exponential and five more instructions a logit take two thirds of that time beside the loads: 2048
-// rows of 32000, 1195 different ones, take 26 us.  With logits decoded again for the maximum, the sums, the rank
+// instructions, an exponential and five more a logit, weigh nearly as much (waves wait for 23% of their
+// cycles, in fp32 for 56%): 2048 rows of 32000, 1200 different ones, take 26 us.  With logits decoded again for the maximum, the sums, the rank
 // and the alternatives the same pass took 464 us.
 template <bool BF16, bool Entropy, bool Rank, bool Top>
 __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
