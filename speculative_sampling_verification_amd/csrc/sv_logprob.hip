@@ -294,7 +294,8 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   int above = 0;
   Kept<BF16> kept{s.val[wave], s.pos[wave], 0, -INFINITY};
 
-  bool clamp = false;  // logits of -inf, or far: pass<true>
+  // pass<true>: logits of -inf, far ones, or a temperature that brings -1e30 near to 0
+  bool clamp = a.c < 0x1p-77f;
 
   // the shift follows a maximum that lies 2^24 above it
   auto raise = [&](float most) SV_INLINE {
@@ -393,13 +394,16 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   };
   auto step = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
     float vm[kVecs], most;
+    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(v[0]) : -INFINITY);
     if (t + kTile > v1) {
-      const uint32_t none = BF16 ? 0xF149F149u : 0xF149F2CAu;  // about -1e30, of no weight
+      // of no weight: -inf, or (no 0 * inf then) about -1e30, 2^22.6 / c below 0 at least, where the
+      // shift is less than 2^22 from it
+      const uint32_t none = clamp ? BF16 ? 0xFF80FF80u : 0xFF800000u
+                                  : BF16 ? 0xF149F149u : 0xF149F2CAu;
 #pragma unroll
       for (int u = 0; u < kVecs; ++u)
         if (t + u * kThreads + tid >= v1) v[u] = u32x4{none, none, none, none};
     }
-    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(v[0]) : -INFINITY);
     const bool done = clamp ? pass(std::true_type{}, t, v, vm, most)
                             : pass(std::false_type{}, t, v, vm, most);
     if (!done) redo(t, most);
