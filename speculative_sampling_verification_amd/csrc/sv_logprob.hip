@@ -178,7 +178,7 @@ struct Kept {
   }
 };
 
-// Sums of several parts on one shift.
+// Sums of a few parts on one shift.
 __device__ __forceinline__ LogprobPart joined(const LogprobPart* p, int count) {
   LogprobPart r{-INFINITY, 0.0f, 0.0f, -INFINITY, 0, {0, 0}};
   double sum = 0.0, sum_x = 0.0;
@@ -194,6 +194,28 @@ __device__ __forceinline__ LogprobPart joined(const LogprobPart* p, int count) {
   }
   r.sum = (float)sum;
   r.sum_x = (float)sum_x;
+  return r;
+}
+
+// The same of up to 64 parts, one a lane: one load's latency instead of one a part.
+__device__ __forceinline__ LogprobPart joined_lanes(const LogprobPart* p, int count) {
+  const int lane = threadIdx.x & 63;
+  LogprobPart r{-INFINITY, 0.0f, 0.0f, -INFINITY, 0, {0, 0}};
+  if (lane < count) r = p[lane];
+  const double own = r.shift;
+  r.shift = wave_all(own, [](double x, double y) { return x > y ? x : y; });
+  double sum = 0.0, sum_x = 0.0;
+  if (own > -INFINITY) {  // there is a finite logit
+    const double d = own - r.shift;
+    const double f = (double)exp2f((float)d);
+    sum = f * r.sum;
+    if (f > 0.0) sum_x = f * ((double)r.sum_x + d * r.sum);
+  }
+  auto add = [](auto x, auto y) { return x + y; };
+  r.sum = (float)wave_all(sum, add);
+  r.sum_x = (float)wave_all(sum_x, add);
+  r.top = wave_all(r.top, [](float x, float y) { return fmaxf(x, y); });
+  r.above = wave_all(r.above, add);
   return r;
 }
 
@@ -236,6 +258,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, Lds& s, const Row<B
   for (int e = tid; e < near; e += kThreads) {
     const unsigned long long me = s.elems[e];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < near; ++j) rank += s.elems[j] > me;
     if (rank < a.n) {
       a.top_tokens[(int64_t)r * a.n + rank] = (int32_t) ~(uint32_t)me;
@@ -480,6 +503,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
     auto rank_of = [&](unsigned long long me) SV_INLINE {
       int rank = (s.edge[0] > me) + (s.edge[1] > me);
       for (int i = 0; i < kWaves; ++i)
+#pragma unroll 8
         for (int j = 0; j < s.count[i]; ++j) rank += s.keys[i][j] > me;
       return rank;
     };
@@ -506,31 +530,70 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   }
 }
 
-// Joins the parts of a row: one lane a part holds the first of its vectors that is left.
+// Joins the parts of a row, whose lists of vectors are in order each.  A vector is among the first n
+// only if it comes no later than a bound that n vectors reach: the n-th of the list whose n-th
+// comes first, or, for any m, the m-th largest of the parts' (n / m)-th vectors' elements.  The few
+// vectors that reach the best of these bounds are ranked against each other.  Latency alone, 7.6 us
+// for 16 parts' 20 alternatives each; 15 with the lists merged one vector after the other and the
+// parts' sums read likewise, and 2 more with one key of the ranking in flight.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a) {
   __shared__ Lds s;
+  __shared__ unsigned long long lists[kMaxParts * kLogprobMaxTop];
+  __shared__ unsigned long long bounds[kWaves];
+  constexpr int kMine = kMaxParts * kLogprobMaxTop / kThreads;
   const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
     const int at = row_index(a, r);
     if (at < 0) continue;  // written already
     const Row<BF16> row(a.logits + (int64_t)at * a.V * Row<BF16>::kES, a.V);
-    const LogprobPart st = joined(a.part + (int64_t)r * a.parts, a.parts);
-    if (a.n && tid < 64) {
-      const unsigned long long* mine = a.part_top + ((int64_t)r * a.parts + lane) * a.n;
-      int next = 0, found = 0;
-      unsigned long long head = lane < a.parts ? mine[0] : 0ull;
-      for (; found < a.n; ++found) {
-        const unsigned long long best = wave_all(
-            head, [](unsigned long long x, unsigned long long y) { return x > y ? x : y; });
-        if (!best) break;
-        if (head == best) {
-          s.picked[found] = best;
-          ++next;
-          head = next < a.n ? mine[next] : 0ull;
-        }
+    const int all = a.parts * a.n;
+    const unsigned long long* given = a.part_top + (int64_t)r * all;
+    unsigned long long mine[kMine];
+    if (a.n) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int e = tid + i * kThreads;
+        mine[i] = e < all ? given[e] : 0ull;
+        if (e < all) lists[e] = mine[i];
       }
-      if (lane == 0) s.found = found;
+    }
+    const LogprobPart st = joined_lanes(a.part + (int64_t)r * a.parts, a.parts);
+    if (a.n) {
+      if (tid == 0) s.near = 0;
+      __syncthreads();
+      unsigned long long bound = 0;
+      for (int m = wave; m < 7; m += kWaves) {  // the 2^m-th vectors, in the end the n-th
+        const int each = 1 << m < a.n ? 1 << m : a.n, parts = (a.n + each - 1) / each;
+        const unsigned long long key = lane < a.parts ? lists[lane * a.n + each - 1] : 0ull;
+        if (parts == 1) {
+          const unsigned long long b = wave_all(
+              key, [](unsigned long long x, unsigned long long y) { return x > y ? x : y; });
+          bound = b > bound ? b : bound;
+          break;
+        }
+        const uint32_t one[1] = {(uint32_t)(key >> 32)};
+        const unsigned long long b = (unsigned long long)nth_key<BF16>(one, parts) << 32;
+        bound = b > bound ? b : bound;
+      }
+      if (lane == 0) bounds[wave] = bound;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) bound = bounds[i] > bound ? bounds[i] : bound;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (mine[i] && mine[i] >= bound) lists[atomicAdd(&s.near, 1)] = mine[i];
+      __syncthreads();
+      const int near = s.near;
+      for (int e = tid; e < near; e += kThreads) {  // in no order, as they are all different
+        const unsigned long long me = lists[e];
+        int rank = 0;
+#pragma unroll 8
+        for (int k = 0; k < near; ++k) rank += lists[k] > me;
+        if (rank < a.n) s.picked[rank] = me;
+      }
+      if (tid == 0) s.found = near < a.n ? near : a.n;
     }
     __syncthreads();
     finish<BF16>(a, s, &row, r, st, a.tokens ? a.tokens[r] : -1);
@@ -573,8 +636,9 @@ LogprobPlan plan_logprobs(int R, int V, sv_dtype dt, int n) {
   const int64_t tiles = (vecs + kTile - 1) / kTile;
   // Rows of their own workgroup from one a compute unit on, else parts of them, a tile each at
   // least, for two.  128256 bf16 (32000 fp32) logits a row, both launches in a graph: 64 rows at two
-  // workgroups a unit 26.3 (25.6) us, at one 27.5 (24.2), at four 29.6 (25.4); 128 rows 29.3 (25.1),
-  // 33.1 (27.4), 29.7 (28.2); 256 rows in one part each 33.0 (21.3), in two 36.7 (29.1).
+  // workgroups a unit 20.4 (20.6) us, at one 23.1 (20.5), at four 21.5 (20.7); 128 rows 25.0 (21.4),
+  // 29.0 (24.2), 24.1 (23.0); 256 rows in one part each 32.5 (21.5), in two 31.4 (25.8), 384 rows
+  // 37.9 (23.8), 40.4 (28.9).
   int64_t parts = R >= 256 ? 1 : (512 + (int64_t)R - 1) / R;
   parts = parts < tiles ? parts : tiles;
   parts = parts < kMaxParts ? parts : kMaxParts;
