@@ -281,8 +281,8 @@ __global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(W
 // and 256 nodes 616 us, 903 (a library product of 8192^3 runs at 1350).  Rows staged through
 // registers took 209 us, with one workgroup a compute unit less 204; 128 rows a stage 272; products of
 // the next 32 rows begun before the last ones' exponentials 217 (registers spill); four workgroups
-// a unit 218; pieces that are left over when all workgroups have as many, in halves for two: no
-// difference.  The exponentials of one wave run beside the products of the others: matrix units are
+// a unit 218; pieces that are left over when all workgroups have as many, in halves for two, or three
+// stages with loads two ahead: no difference.  The exponentials of one wave run beside the products of the others: matrix units are
 // busy a third of the time at 2.15 GHz.
 template <bool BF16, int D, int KB, int RT>
 struct Rows {
