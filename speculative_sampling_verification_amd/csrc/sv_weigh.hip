@@ -278,12 +278,12 @@ __global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(W
 //
 // Bound by the matrix instructions and, between them, an exponential a product of 2 D operations: 64
 // nodes of 64 query heads to 8 kv heads of 128 on 131072 tokens (512 rows) take 180 us, 775 TFLOP/s,
-// and 256 nodes 616 us, 903 (a library product of 8192^3 runs at 1350).  Rows staged through
-// registers took 209 us, with one workgroup a compute unit less 204; 128 rows a stage 272; products of
-// the next 32 rows begun before the last ones' exponentials 217 (registers spill); four workgroups
-// a unit 218; pieces that are left over when all workgroups have as many, in halves for two, or three
-// stages with loads two ahead: no difference.  The exponentials of one wave run beside the products of the others: matrix units are
-// busy a third of the time at 2.15 GHz.
+// and 256 nodes 590 us, 945 (a library product of 8192^3 runs at 1350).  Vector instructions fill 85 us
+// of the 180, products 61 (at 2.15 GHz), and the two overlap little: waves wait 47% of their time.
+// Rows staged through registers took 209 us, with one workgroup a compute unit less 204; 128 rows a
+// stage 272; products of the next 32 rows begun before the last ones' exponentials 217 (registers
+// spill); four workgroups a unit 218; pieces that are left over when all workgroups have as many, in
+// halves for two, or three stages with loads two ahead: no difference.
 template <bool BF16, int D, int KB, int RT>
 struct Rows {
   static constexpr int kES = BF16 ? 2 : 4;
