@@ -83,11 +83,39 @@ struct Row {
   }
 };
 
+// A value of the lane that a DPP control names, and of a given lane.
+template <int Control, class T>
+__device__ __forceinline__ T across(T x) {
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &x, sizeof(T));
+#pragma unroll
+  for (int& y : w) y = __builtin_amdgcn_update_dpp(y, y, Control, 0xF, 0xF, false);
+  __builtin_memcpy(&x, w, sizeof(T));
+  return x;
+}
+template <class T>
+__device__ __forceinline__ T of_lane(T x, int lane) {
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &x, sizeof(T));
+#pragma unroll
+  for (int& y : w) y = __builtin_amdgcn_readlane(y, lane);
+  __builtin_memcpy(&x, w, sizeof(T));
+  return x;
+}
+
+// op over four neighbouring lanes, and over the wave (all lanes active): within rows of 16 lanes
+// by DPP (neighbours, pairs, then halves mirrored), the four rows as scalars.
+template <class T, class Op>
+__device__ __forceinline__ T quad_all(T x, Op op) {
+  x = op(x, across<0xB1>(x));  // lanes 1 0 3 2
+  return op(x, across<0x4E>(x));  // lanes 2 3 0 1
+}
 template <class T, class Op>
 __device__ __forceinline__ T wave_all(T x, Op op) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
-  return x;
+  x = quad_all(x, op);
+  x = op(x, across<0x141>(x));  // 7 .. 0 of each 8
+  x = op(x, across<0x140>(x));  // 15 .. 0 of each 16
+  return op(op(of_lane(x, 0), of_lane(x, 16)), op(of_lane(x, 32), of_lane(x, 48)));
 }
 
 // The n-th largest of the wave's keys, several a lane (the largest k with n keys >= k).  Keys of
@@ -178,44 +206,24 @@ struct Kept {
   }
 };
 
-// Sums of a few parts on one shift.
-__device__ __forceinline__ LogprobPart joined(const LogprobPart* p, int count) {
-  LogprobPart r{-INFINITY, 0.0f, 0.0f, -INFINITY, 0, {0, 0}};
-  double sum = 0.0, sum_x = 0.0;
-  for (int i = 0; i < count; ++i) r.shift = p[i].shift > r.shift ? p[i].shift : r.shift;
-  for (int i = 0; i < count; ++i) {
-    r.top = fmaxf(r.top, p[i].top);
-    r.above += p[i].above;
-    if (p[i].shift == -INFINITY) continue;  // no finite logit
-    const double d = p[i].shift - r.shift;
-    const double f = (double)exp2f((float)d);
-    sum += f * p[i].sum;
-    if (f > 0.0) sum_x += f * ((double)p[i].sum_x + d * p[i].sum);
-  }
-  r.sum = (float)sum;
-  r.sum_x = (float)sum_x;
-  return r;
-}
-
-// The same of up to 64 parts, one a lane: one load's latency instead of one a part.
-__device__ __forceinline__ LogprobPart joined_lanes(const LogprobPart* p, int count) {
-  const int lane = threadIdx.x & 63;
-  LogprobPart r{-INFINITY, 0.0f, 0.0f, -INFINITY, 0, {0, 0}};
-  if (lane < count) r = p[lane];
+// Parts, one a lane, on one shift: all(x, op) is op over the lanes that hold them.  In 64 bits, as 1
+// less a row's largest probability may be far below half a step of fp32.
+template <class All>
+__device__ __forceinline__ LogprobPart joined(LogprobPart r, All all) {
   const double own = r.shift;
-  r.shift = wave_all(own, [](double x, double y) { return x > y ? x : y; });
+  r.shift = all(own, [](double x, double y) { return x > y ? x : y; });
   double sum = 0.0, sum_x = 0.0;
   if (own > -INFINITY) {  // there is a finite logit
     const double d = own - r.shift;
-    const double f = (double)exp2f((float)d);
+    const double f = exp2(d);
     sum = f * r.sum;
-    if (f > 0.0) sum_x = f * ((double)r.sum_x + d * r.sum);
+    if (f > 0.0) sum_x = f * (r.sum_x + d * r.sum);
   }
   auto add = [](auto x, auto y) { return x + y; };
-  r.sum = (float)wave_all(sum, add);
-  r.sum_x = (float)wave_all(sum_x, add);
-  r.top = wave_all(r.top, [](float x, float y) { return fmaxf(x, y); });
-  r.above = wave_all(r.above, add);
+  r.sum = all(sum, add);
+  r.sum_x = all(sum_x, add);
+  r.top = all(r.top, [](float x, float y) { return fmaxf(x, y); });
+  r.above = all(r.above, add);
   return r;
 }
 
@@ -226,7 +234,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, Lds& s, const Row<B
                        const LogprobPart& st, int token) {
   const int tid = threadIdx.x;
   const bool some = row && st.top > -INFINITY;
-  const double ln_s = some ? log((double)st.sum) : 0.0;
+  const double ln_s = some ? log(st.sum) : 0.0;
   auto logprob = [&](float z) -> float {
     return some ? (float)(kLn2 * ((double)a.c * z - st.shift) - ln_s) : -INFINITY;
   };
@@ -335,6 +343,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
     }
     m0 = m;
     k = kn;
+    asm("" : "+v"(m0), "+v"(k));  // in vector registers: the loop's products have a scalar, a.c
     far = far_n;
     clamp |= far;
   };
@@ -482,13 +491,12 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   }
 
   // the waves' sums, then the part's
-  auto add = [](float x, float y) SV_INLINE { return x + y; };
-  sum = wave_all(sum, add);
-  sum_x = wave_all(sum_x, add);
+  auto add = [](double x, double y) SV_INLINE { return x + y; };
+  const double all = wave_all((double)sum, add), all_x = wave_all((double)sum_x, add);
   top = wave_all(top, [](float x, float y) { return fmaxf(x, y); });
   if (lane == 0) {
     const double shift = m0 == -INFINITY ? -INFINITY : far ? (double)a.c * m0 : (double)k;
-    s.stat[wave] = LogprobPart{shift, sum, sum_x, top, above, {0, 0}};
+    s.stat[wave] = LogprobPart{shift, all, all_x, top, above};
   }
   if constexpr (Top) {
     if (kept.count > a.n) kept.cut(a.n);
@@ -498,7 +506,9 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
     if (lane == 0) s.count[wave] = kept.count;
   }
   __syncthreads();
-  LogprobPart st = joined(s.stat, kWaves);
+  static_assert(kWaves == 4, "a lane of four a wave");
+  const LogprobPart st =
+      joined(s.stat[lane & 3], [](auto x, auto op) { return quad_all(x, op); });
   if constexpr (Top) {
     // a vector's rank among the waves' kept ones and the two that are not whole
     auto rank_of = [&](unsigned long long me) SV_INLINE {
@@ -560,7 +570,9 @@ __global__ __launch_bounds__(kThreads) void k_logprob_join(LogprobArgs a) {
         if (e < all) lists[e] = mine[i];
       }
     }
-    const LogprobPart st = joined_lanes(a.part + (int64_t)r * a.parts, a.parts);
+    LogprobPart mine_st{-INFINITY, 0.0, 0.0, -INFINITY, 0};
+    if (lane < a.parts) mine_st = a.part[(int64_t)r * a.parts + lane];
+    const LogprobPart st = joined(mine_st, [](auto x, auto op) { return wave_all(x, op); });
     if (a.n) {
       if (tid == 0) s.near = 0;
       __syncthreads();

@@ -15,10 +15,9 @@ constexpr int kLogprobMaxTop = 64;  // alternatives a row
 // What a part of a row leaves for the others: sums of 2^(x - shift), x = z log2(e) / T.
 struct alignas(16) LogprobPart {
   double shift;
-  float sum, sum_x;  // of e and of e (x - shift)
-  float top;         // largest logit
-  int above;         // logits that come before the token's
-  int pad[2];
+  double sum, sum_x;  // of e and of e (x - shift)
+  float top;          // largest logit
+  int above;          // logits that come before the token's
 };
 
 struct LogprobArgs {
