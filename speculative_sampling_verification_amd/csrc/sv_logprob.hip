@@ -3,8 +3,9 @@
 //
 // With x = z log2(e) / T, a shift k and S = sum 2^(x - k), X = sum 2^(x - k) (x - k):
 //   log p(t) = ln2 (x_t - k) - ln S,   H = ln S - ln2 X / S
-// k is near the first tile's maximum and follows it when a later one is far above; sums are in
-// fp32 a lane, joined in 64 bits.
+// k is never far below the largest x so far: H is the difference of two numbers that both grow with
+// that distance, and S and X take their rounding errors from it.  Sums are in fp32 a lane, joined in
+// 64 bits.
 //
 // Alternatives: the top n elements (larger first, ties to the lower index) lie in the n vectors of
 // 16 bytes that come first by (their largest element, position): an element of another vector comes
@@ -32,6 +33,7 @@ constexpr int kSpare = 48;            // vectors a wave keeps beyond n until it 
 constexpr int kList = kLogprobMaxTop + kSpare + 64 * kVecs;
 constexpr int kMaxParts = 64;         // of a row: one a lane of the join
 constexpr int64_t kMaxBlocks = 1 << 20;
+constexpr float kRise = 2.0f;         // how far x may lie above the shift
 constexpr double kLn2 = 0.69314718055994530942;
 
 // Every lambda of the kernel is part of its loop: the captures of one that the compiler calls
@@ -285,16 +287,23 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 }
 
 // One workgroup a row, or part of one.  Bound by memory: 2048 rows of 128256 bf16 logits (525 MB) take
-// 95 us, 5.5 TB/s, 512 rows of 256000 in fp32 87 us, 6.0 (a large copy runs at 5.2, a sum over 2 GiB
+// 96 us, 5.5 TB/s, 512 rows of 256000 in fp32 87 us, 6.0 (a large copy runs at 5.2, a sum over 2 GiB
 // at 4.0).  Loads pass the caches, as nothing is read twice (else 110 and 101 us).  4 KB on their way a
-// wave and six to eight waves a SIMD; 2 KB 101 and 120 us, 8 KB at four waves 100 and 95, loads of a
-// whole tile ahead of its arithmetic 103.  Rows in stretches an XCD: no difference.  In bf16 the
-// instructions, an exponential and five more a logit, weigh nearly as much (waves wait for 23% of their
-// cycles, in fp32 for 56%): 2048 rows of 32000, 1200 different ones, take 26 us.  With logits decoded
-// again for the maximum, the sums, the rank and the alternatives the same pass took 464 us.  Where there
-// is about one row a compute unit, the alternatives cost 10 of 36 us (300 rows), as nothing else runs.
+// wave and eight waves a SIMD, all 2048 rows at once (seven, with 71 registers: 102); 2 KB 101 and 120
+// us, 8 KB at four waves 100 and 95, loads of a whole tile ahead of its arithmetic 103.  Rows in
+// stretches an XCD: no difference.  In bf16 the instructions, an exponential and five more a logit,
+// weigh nearly as much (waves wait for 23% of their cycles, in fp32 for 56%): 2048 rows of 32000, 1200
+// different ones, take 26 us.  With logits decoded again for the maximum, the sums, the rank and the
+// alternatives the same pass took 464 us.  Where there is about one row a compute unit, the alternatives
+// cost 10 of 38 us (300 rows), as nothing else runs.
+//
+// The shift follows the maximum vector by vector, kRise = 2.  A tile that is only read again where a
+// logit lies 24 above it takes 95 us, and 36 for the 300 rows, but the entropy of a row with one token of
+// 2^18 to 2^23 times any other's weight is then off by up to 3e-6, here by 2e-7; 2 or 4: no difference in
+// time; a tile read again at 2: 108 us, a vector read again 98 (loads come back in order, so it waits
+// for the next tile's); the maximum before the exponentials 97, and 105 in fp32.
 template <bool BF16, bool Entropy, bool Rank, bool Top>
-__global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void k_logprob(LogprobArgs a) {
   using R = Row<BF16>;
   constexpr int kPer = R::kPer;
   __shared__ Lds s;
@@ -321,6 +330,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
 
   float sum = 0.0f, sum_x = 0.0f, top = -INFINITY;
   float m0 = -INFINITY, k = 0.0f;  // the shift as a logit (wave-wide), and as c m0
+  float limit = -INFINITY;         // logits above it move the shift
   bool far = false;                // |c m0| is 2^22 or more, and its rounding (then over
                                    // 1/8) shows in x - k: differences of logits first
   int above = 0;
@@ -329,24 +339,32 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   // pass<true>: logits of -inf, far ones, or a temperature that brings -1e30 near to 0
   bool clamp = a.c < 0x1p-77f;
 
-  // the shift follows a maximum that lies 2^24 above it
-  auto raise = [&](float most) SV_INLINE {
-    if (!__any(most > m0 && (m0 == -INFINITY || (most - m0) * a.c > 24.0f))) return;
+  const float rise = kRise / a.c;
+
+  // Where a lane's `most` lies above the limit: moves the shift to the wave's largest, with the sums so
+  // far and those of a tile, f and fx.
+  auto raise = [&](float most, float& f, float& fx) SV_INLINE {
+    if (__builtin_expect(!__any(most > limit), 1)) return false;
     const float m = wave_all(most, [](float x, float y) { return fmaxf(x, y); });
     const float kn = a.c * m;
     const bool far_n = !(fabsf(kn) < 4194304.0f);
     if (m0 > -INFINITY) {
       const float d = far || far_n ? (m0 - m) * a.c : k - kn;
-      const float f = exp2f(d);
-      sum_x = f > 0.0f ? f * fmaf(d, sum, sum_x) : 0.0f;
-      sum *= f;
+      const float w = exp2f(d);
+      sum_x = w > 0.0f ? w * fmaf(d, sum, sum_x) : 0.0f;
+      sum *= w;
+      fx = w > 0.0f ? w * fmaf(d, f, fx) : 0.0f;
+      f *= w;
     }
     m0 = m;
     k = kn;
     asm("" : "+v"(m0), "+v"(k));  // in vector registers: the loop's products have a scalar, a.c
+    limit = m + rise;
     far = far_n;
     clamp |= far;
+    return true;
   };
+  float none = 0.0f, none_x = 0.0f;  // no tile's sums
   // one logit, whatever it is
   auto take = [&](float z) SV_INLINE {
     const float x = fmaxf(far ? (z - m0) * a.c : fmaf(z, a.c, -k), -200.0f);
@@ -369,22 +387,20 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   };
 
   // One tile.  A vector's registers take the next tile's as soon as it is done, so that 4 KB a wave
-  // are always on their way.  The sums are formed at the shift as it is, and again (`redo`) where
-  // that does not do.  Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and
-  // far shifts are subtracted first.
+  // are always on their way.  A vector's sums are formed at the shift as it is, and again where one
+  // of its logits lies above the limit; the whole tile's (`redo`) where that turns out to need the
+  // other form.  Clamp: logits of -inf, or of no weight at all, do not count as 0 * inf, and far
+  // shifts are subtracted first.
   auto pass = [&](auto clamped, int t, u32x4 (&v)[kVecs], float (&vm)[kVecs],
                   float& most) SV_INLINE {
     constexpr bool Clamp = decltype(clamped)::value;
-    const float z0 = Clamp && far ? m0 : 0.0f, k0 = Clamp && far ? 0.0f : k;
     float f = 0.0f, fx = 0.0f;
     most = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int j = t + u * kThreads + tid;
-      float m = -INFINITY;
+    auto add = [&](const u32x4& y, float& m) SV_INLINE {
+      const float z0 = Clamp && far ? m0 : 0.0f, k0 = Clamp && far ? 0.0f : k;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        const float z = R::elem(v[u], e);
+        const float z = R::elem(y, e);
         float x = fmaf(Clamp ? z - z0 : z, a.c, -k0);
         if constexpr (Clamp) x = fmaxf(x, -200.0f);
         const float w = __builtin_amdgcn_exp2f(x);
@@ -392,7 +408,18 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
         f += w;
         if constexpr (Entropy) fx = fmaf(w, x, fx);
       }
+    };
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int j = t + u * kThreads + tid;
+      float m = -INFINITY, before = f, before_x = fx;
+      add(v[u], m);
       vm[u] = j < v1 ? m : -INFINITY;
+      if (raise(vm[u], before, before_x)) {
+        f = before;
+        fx = before_x;
+        add(v[u], m);
+      }
       most = fmaxf(most, vm[u]);
       if constexpr (Rank) {
         const float th = j >= v1 ? INFINITY : j < token_vec ? level : beyond;
@@ -408,15 +435,13 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
     }
     const bool odd = !Clamp && Entropy && fx != fx;
     if (__any(odd)) clamp = true;
-    else if (!__any((most - m0) * a.c > 24.0f)) {
-      sum += f;
-      sum_x += fx;
-      return true;
-    }
-    return false;
+    if (!Clamp && clamp) return false;
+    sum += f;
+    sum_x += fx;
+    return true;
   };
   auto redo = [&](int t, float most) SV_INLINE {
-    raise(most);
+    raise(most, none, none_x);
 #pragma unroll 1
     for (int u = 0; u < kVecs; ++u) {
       if (t + u * kThreads + tid >= v1) continue;
@@ -427,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   };
   auto step = [&](int t, u32x4 (&v)[kVecs]) SV_INLINE {
     float vm[kVecs], most;
-    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(v[0]) : -INFINITY);
+    if (m0 == -INFINITY) raise(t + tid < v1 ? vec_max(v[0]) : -INFINITY, none, none_x);
     if (t + kTile > v1) {
       // of no weight: -inf, or (no 0 * inf then) about -1e30, 2^22.6 / c below 0 at least, where the
       // shift is less than 2^22 from it
@@ -460,7 +485,10 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
   if (v0 < v1) {
     u32x4 v[kVecs];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = load_vec(v0, u);
+    for (int u = 0; u < kVecs; ++u) {
+      v[u] = load_vec(v0, u);
+      __builtin_amdgcn_sched_barrier(0);  // in this order, in which they are waited for
+    }
     for (int t = v0; t < v1; t += kTile) step(t, v);
   }
 
@@ -471,7 +499,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_logprob(LogprobArgs a) {
     const int64_t i = lane < 8 ? (lane < row.head ? lane : a.V) : row.tail() + lane - 8;
     const bool mine = lane < 16 && i < a.V;
     const float z = mine ? row.load(i) : -INFINITY;
-    raise(z);
+    raise(z, none, none_x);
     take(z);
     top = fmaxf(top, z);
     if constexpr (Rank) {
