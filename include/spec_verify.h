@@ -553,8 +553,9 @@ int spec_rotary_append(const void* q, const int64_t* q_strides, int q_heads, voi
  * Eviction by accumulated attention weight: sequences kept at a budget of tokens.
  *
  * weights [layers, seqs, kv_heads, length] float holds what the queries so far gave to the token at
- * each position, one number a layer and kv head.  A step adds its own behind spec_tree_attention
- * (spec_cache_weigh, layer by layer); spec_cache_evict then keeps the tokens of largest weight, each
+ * each position, one number a layer and kv head.  A step adds its own once its nodes are verified and
+ * committed (spec_cache_weigh, layer by layer, with the queries and lse of spec_tree_attention, so that
+ * rejected nodes add nothing and accepted ones count for each other); spec_cache_evict then keeps the tokens of largest weight, each
  * head its own, and spec_cache_resize stores the lengths and gives the pages back, as after
  * spec_cache_commit.  New tokens start at the weights that lie behind the length: zeros, if the
  * array began as zeros.
@@ -568,8 +569,9 @@ int spec_rotary_append(const void* q, const int64_t* q_strides, int q_heads, voi
  *   q, q_strides, N, q_heads, layer, num_nodes, scale   as spec_tree_attention takes them
  *   lse         [seqs, N, q_heads] of that call; a row of -inf gives nothing
  *   seen        [seqs, N] or NULL (all): how many of the committed tokens the node sees: its own
- *               position + 1 where the nodes are committed already (the last tokens of a prompt
- *               after spec_cache_commit), 0 for a node that is not to count
+ *               position + 1 where the nodes are committed already (the last tokens of a prompt, or
+ *               the accepted nodes of a tree, after spec_cache_commit and the spec_cache_resize that
+ *               stores the lengths), 0 for a node that is not to count (a rejected one)
  *   decay       in [0, 1]; 0: the array's values are replaced, whatever they are
  *   weights     as above; positions from `length` on are not weighed, those from seq_lens on are
  *               left as they are.  Shares no memory with the other arrays

@@ -928,7 +928,8 @@ def spec_cache_weigh(q, lse, cache, weights, *, layer=0, seen=None, num_nodes=No
 
     lse [seqs, N, q_heads] as spec_tree_attention(want_lse=True) returns it for the same q; seen
     [seqs, N] int32: how many committed tokens each node sees (None: all; 0: the node does not
-    count).  Returns weights."""
+    count).  Behind a verified tree, once its nodes are committed: own position + 1 for the accepted
+    nodes, 0 for the others.  Returns weights."""
     q_strides = _row_strides(q, "q", cache, None)
     B, N, H, D = q.shape
     lse_at = _arg(lse, "lse", cache, torch.float32, (B, N, H))
