@@ -650,6 +650,12 @@ class _Place:
         self.device, self._index = device, device.index
 
 
+def _sizes(name, *values):
+    """Refuses what a 32-bit integer does not hold: ctypes would pass its lower half on."""
+    if max(values) >= 2**31 or min(values) < -2**31:
+        raise ValueError(f"{name} {', '.join(map(str, values))} is out of range")
+
+
 def _row_strides(t, name, cache, heads):
     """The element strides of a [seqs, N, heads, head_dim] tensor, None where it is dense."""
     if not isinstance(t, torch.Tensor):
@@ -663,6 +669,8 @@ def _row_strides(t, name, cache, heads):
             heads is not None and shape[2] != heads):
         raise ValueError(f"{name} must be [{cache.seqs}, N, {heads or 'heads'}, "
                          f"{cache.head_dim}], got {tuple(shape)}")
+    if max(shape) >= 2**31:
+        raise ValueError(f"{name} {tuple(shape)} is out of range")
     if t.is_contiguous():
         return None
     s = t.stride()
@@ -894,6 +902,7 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
                                          or list(new_strides) != list(v_strides)):
         raise ValueError("k_new and v_new must have the same strides")
     N = k_new.shape[1]
+    _sizes("layer", layer)
     q_strides = _row_strides(q, "q", cache, None)
     if q.shape[1] != N:
         raise ValueError(f"q must be [{cache.seqs}, {N}, heads, {cache.head_dim}], "
@@ -916,6 +925,7 @@ def _weights_arg(weights, name, cache):
     if not isinstance(weights, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     length = weights.shape[3] if weights.dim() == 4 else 0
+    _sizes(f"length of {name}", length)
     return _arg(weights, name, cache, torch.float32,
                 (cache.layers, cache.seqs, cache.kv_heads, length))
 
@@ -931,6 +941,7 @@ def spec_cache_weigh(q, lse, cache, weights, *, layer=0, seen=None, num_nodes=No
     count).  Behind a verified tree, once its nodes are committed: own position + 1 for the accepted
     nodes, 0 for the others.  Returns weights."""
     q_strides = _row_strides(q, "q", cache, None)
+    _sizes("layer", layer)
     B, N, H, D = q.shape
     lse_at = _arg(lse, "lse", cache, torch.float32, (B, N, H))
     if lse_at is None:
@@ -960,6 +971,7 @@ def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, 
     if keep_at is None:
         raise TypeError("keep must be a torch.Tensor")
     max_keep = length if max_keep is None else int(max_keep)
+    _sizes("max_keep, sinks, recent", max_keep, sinks, recent)
     kept_shape = (cache.layers, cache.seqs, cache.kv_heads, max(0, max_keep))
     raw = _raw_stream(cache, stream)
     out = dict(out) if out else {}
@@ -1017,8 +1029,9 @@ def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_
     if want_rank and tokens is None:
         raise ValueError("ranks need tokens")
     R, top_n = math.prod(shape), int(top_n)
-    if V < 1 or max(R, logits.numel() // V) >= 2**31:
+    if V < 1 or max(V, R, logits.numel() // V) >= 2**31:
         raise ValueError(f"logits {tuple(logits.shape)} for {R} tokens is out of range")
+    _sizes("top_n", top_n)
     raw = _raw_stream(place, None)
     need = _logprob_workspace(R, V, dt, top_n)
     out = dict(out) if out else {}
