@@ -893,7 +893,7 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
     (see include/spec_verify.h).  base [seqs] int32 defaults to the cache's seq_lens: give a tree's
     depths as ``positions``, and the tokens' number as ``base`` once some were evicted.  Returns
     the turned queries: ``out`` (dense, or q itself to turn it in place), or a new tensor; rows past
-    num_nodes are left as they were."""
+    num_nodes are left as they were.  q may be None: keys and values alone, and None is returned."""
     new_strides = _row_strides(k_new, "k_new", cache, cache.kv_heads)
     v_strides = _row_strides(v_new, "v_new", cache, cache.kv_heads)
     if k_new.shape != v_new.shape:
@@ -903,20 +903,26 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
         raise ValueError("k_new and v_new must have the same strides")
     N = k_new.shape[1]
     _sizes("layer", layer)
-    q_strides = _row_strides(q, "q", cache, None)
-    if q.shape[1] != N:
-        raise ValueError(f"q must be [{cache.seqs}, {N}, heads, {cache.head_dim}], "
-                         f"got {tuple(q.shape)}")
+    q_strides, heads, q_at, out_at = None, 0, None, None
+    if q is not None:
+        q_strides, heads, q_at = _row_strides(q, "q", cache, None), q.shape[2], q.data_ptr()
+        if q.shape[1] != N:
+            raise ValueError(f"q must be [{cache.seqs}, {N}, heads, {cache.head_dim}], "
+                             f"got {tuple(q.shape)}")
+    elif out is not None:
+        raise ValueError("out is given, but no q")
     freq_at = _rotary_arg(inv_freq, cache)
     base_at = _arg(base, "base", cache, torch.int32, (cache.seqs,))
     at = _arg(positions, "positions", cache, torch.int32, (cache.seqs, N))
     nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (cache.seqs,))
     raw = _raw_stream(cache, stream)
-    out = _turned_out(q, "out", q_strides, out, stream)
-    _cache_call(cache, "spec_rotary_append", _lib.spec_rotary_append, q.data_ptr(), q_strides,
-                q.shape[2], out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new_strides, N,
-                cache._ref, layer, nodes_at, freq_at, 2 * inv_freq.numel(), int(interleaved),
-                amplitude, base_at, at, raw)
+    if q is not None:
+        out = _turned_out(q, "out", q_strides, out, stream)
+        out_at = out.data_ptr()
+    _cache_call(cache, "spec_rotary_append", _lib.spec_rotary_append, q_at, q_strides, heads,
+                out_at, k_new.data_ptr(), v_new.data_ptr(), new_strides, N, cache._ref, layer,
+                nodes_at, freq_at, 2 * inv_freq.numel(), int(interleaved), amplitude, base_at, at,
+                raw)
     return out
 
 
