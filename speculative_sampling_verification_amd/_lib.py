@@ -651,7 +651,8 @@ class _Place:
 
 
 def _sizes(name, *values):
-    """Refuses what a 32-bit integer does not hold: ctypes would pass its lower half on."""
+    """Refuses what a 32-bit integer does not hold: ctypes would pass its lower half on.  Short calls
+    ask for it only where some size's upper bits are set (a negative one's are)."""
     if max(values) >= 2**31 or min(values) < -2**31:
         raise ValueError(f"{name} {', '.join(map(str, values))} is out of range")
 
@@ -669,8 +670,6 @@ def _row_strides(t, name, cache, heads):
             heads is not None and shape[2] != heads):
         raise ValueError(f"{name} must be [{cache.seqs}, N, {heads or 'heads'}, "
                          f"{cache.head_dim}], got {tuple(shape)}")
-    if max(shape) >= 2**31:
-        raise ValueError(f"{name} {tuple(shape)} is out of range")
     if t.is_contiguous():
         return None
     s = t.stride()
@@ -699,6 +698,8 @@ def spec_tree_attention(q, cache, *, layer=0, mask=None, num_nodes=None, scale=N
     strides = _row_strides(q, "q", cache, None)
     shape = q.shape
     B, N, H, D = shape
+    if (N | H | layer) >> 31:
+        _sizes("nodes, heads, layer", N, H, layer)
     dev = cache.device
     mask_at = _arg(mask, "mask", cache, torch.uint8, (B, N, N))
     nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (B,))
@@ -735,9 +736,12 @@ def spec_cache_append(k_new, v_new, cache, *, layer=0, num_nodes=None, stream=No
     if strides is not v_strides and (strides is None or v_strides is None
                                      or list(strides) != list(v_strides)):
         raise ValueError("k_new and v_new must have the same strides")
+    N = k_new.shape[1]
+    if (N | layer) >> 31:
+        _sizes("nodes, layer", N, layer)
     nodes_at = _arg(num_nodes, "num_nodes", cache, torch.int32, (cache.seqs,))
     _cache_call(cache, "spec_cache_append", _lib.spec_cache_append, k_new.data_ptr(),
-                v_new.data_ptr(), strides, k_new.shape[1], cache._ref, layer, nodes_at,
+                v_new.data_ptr(), strides, N, cache._ref, layer, nodes_at,
                 _raw_stream(cache, stream))
 
 
@@ -869,6 +873,9 @@ def spec_rotary(q, inv_freq, *, k=None, base=None, positions=None, interleaved=F
         if k.shape[1] != N:
             raise ValueError(f"k must be [{place.seqs}, {N}, heads, {place.head_dim}], "
                              f"got {tuple(k.shape)}")
+    k_heads = 0 if k is None else k.shape[2]
+    if (place.seqs | N | heads | k_heads) >> 31:
+        _sizes("sequences, tokens, heads", place.seqs, N, heads, k_heads)
     freq_at = _rotary_arg(inv_freq, place)
     base_at = _arg(base, "base", place, torch.int32, (place.seqs,))
     at = _arg(positions, "positions", place, torch.int32, (place.seqs, N))
@@ -881,7 +888,7 @@ def spec_rotary(q, inv_freq, *, k=None, base=None, positions=None, interleaved=F
         raise ValueError("out holds k, but no k is given")
     _cache_call(place, "spec_rotary", _lib.spec_rotary, q.data_ptr(), strides["q"], heads,
                 out["q"].data_ptr(), None if k is None else k.data_ptr(), strides.get("k"),
-                0 if k is None else k.shape[2], None if k is None else out["k"].data_ptr(), dt,
+                k_heads, None if k is None else out["k"].data_ptr(), dt,
                 place.seqs, N, place.head_dim, freq_at, 2 * inv_freq.numel(), int(interleaved),
                 amplitude, base_at, at, raw)
     return out
@@ -902,7 +909,6 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
                                          or list(new_strides) != list(v_strides)):
         raise ValueError("k_new and v_new must have the same strides")
     N = k_new.shape[1]
-    _sizes("layer", layer)
     q_strides, heads, q_at, out_at = None, 0, None, None
     if q is not None:
         q_strides, heads, q_at = _row_strides(q, "q", cache, None), q.shape[2], q.data_ptr()
@@ -911,6 +917,8 @@ def spec_rotary_append(q, k_new, v_new, cache, inv_freq, *, layer=0, base=None, 
                              f"got {tuple(q.shape)}")
     elif out is not None:
         raise ValueError("out is given, but no q")
+    if (N | heads | layer) >> 31:
+        _sizes("nodes, heads, layer", N, heads, layer)
     freq_at = _rotary_arg(inv_freq, cache)
     base_at = _arg(base, "base", cache, torch.int32, (cache.seqs,))
     at = _arg(positions, "positions", cache, torch.int32, (cache.seqs, N))
@@ -931,7 +939,8 @@ def _weights_arg(weights, name, cache):
     if not isinstance(weights, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     length = weights.shape[3] if weights.dim() == 4 else 0
-    _sizes(f"length of {name}", length)
+    if length >> 31:
+        _sizes(f"length of {name}", length)
     return _arg(weights, name, cache, torch.float32,
                 (cache.layers, cache.seqs, cache.kv_heads, length))
 
@@ -947,8 +956,9 @@ def spec_cache_weigh(q, lse, cache, weights, *, layer=0, seen=None, num_nodes=No
     count).  Behind a verified tree, once its nodes are committed: own position + 1 for the accepted
     nodes, 0 for the others.  Returns weights."""
     q_strides = _row_strides(q, "q", cache, None)
-    _sizes("layer", layer)
     B, N, H, D = q.shape
+    if (N | H | layer) >> 31:
+        _sizes("nodes, heads, layer", N, H, layer)
     lse_at = _arg(lse, "lse", cache, torch.float32, (B, N, H))
     if lse_at is None:
         raise TypeError("lse must be a torch.Tensor")
@@ -977,7 +987,8 @@ def spec_cache_evict(cache, weights, keep, *, sinks=0, recent=0, max_keep=None, 
     if keep_at is None:
         raise TypeError("keep must be a torch.Tensor")
     max_keep = length if max_keep is None else int(max_keep)
-    _sizes("max_keep, sinks, recent", max_keep, sinks, recent)
+    if (max_keep | sinks | recent) >> 31:
+        _sizes("max_keep, sinks, recent", max_keep, sinks, recent)
     kept_shape = (cache.layers, cache.seqs, cache.kv_heads, max(0, max_keep))
     raw = _raw_stream(cache, stream)
     out = dict(out) if out else {}
@@ -1037,7 +1048,8 @@ def spec_token_logprobs(logits, tokens=None, *, rows=None, temperature=1.0, top_
     R, top_n = math.prod(shape), int(top_n)
     if V < 1 or max(V, R, logits.numel() // V) >= 2**31:
         raise ValueError(f"logits {tuple(logits.shape)} for {R} tokens is out of range")
-    _sizes("top_n", top_n)
+    if top_n >> 31:
+        _sizes("top_n", top_n)
     raw = _raw_stream(place, None)
     need = _logprob_workspace(R, V, dt, top_n)
     out = dict(out) if out else {}
