@@ -465,9 +465,9 @@ int spec_cache_fork(const sv_cache* cache, const int32_t* src, const int32_t* ds
  *               top_n others, the rest holds -1 and -inf
  * A token outside [0, V) has log probability -inf and rank -1.  A row outside [0, num_rows), or
  * without a finite logit, has no distribution: -inf, entropy 0, no alternatives.  What a row with a
- * logit of NaN or +inf gets is not defined (tokens stay in [-1, V)); it touches no other row.  Sums
- * are in fp32 a thread and joined in 64 bits.  Outputs and workspace share no memory with each other
- * or the inputs.
+ * logit of NaN or +inf gets is not defined (tokens stay in [-1, V)); it touches no other row.  Weights
+ * are taken relative to one near the largest, summed in fp32 a thread and joined in 64 bits.  Outputs
+ * and workspace share no memory with each other or the inputs.
  */
 size_t spec_token_logprobs_workspace_size(int R, int V, sv_dtype dtype, int top_n);
 int spec_token_logprobs(const void* logits, sv_dtype dtype, int num_rows, int V,

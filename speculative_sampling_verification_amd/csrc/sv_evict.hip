@@ -263,6 +263,9 @@ __global__ __launch_bounds__(kThreads, 6) void k_evict_select(EvictArgs a, int64
 // rows a thread in flight; two 783, five 779, eight, before that, 1039 against 802 (registers leave
 // fewer waves).  Moving in the selection's own launch spills: 769 here, but 113 us against 93 for two
 // sequences of 4096 tokens, and 77 against 68 for eight of 400; one of 200 tokens 16 against 17.
+//
+// One workgroup a head, whatever its length: a few long lists leave the GPU idle.  30000 of 32768 tokens
+// in 8 heads take 390 us with the selection (what they move 48), in one 500 (6), in 64 430 (385).
 __global__ __launch_bounds__(kThreads) void k_evict_move(EvictArgs a, int64_t groups,
                                                          FastDiv row_div) {
   const CacheView& c = a.c;

@@ -292,7 +292,7 @@ __device__ __forceinline__ int row_index(const LogprobArgs& a, int r) {
 // wave and eight waves a SIMD, all 2048 rows at once (seven, with 71 registers: 102); 2 KB 101 and 120
 // us, 8 KB at four waves 100 and 95, loads of a whole tile ahead of its arithmetic 103.  Rows in
 // stretches an XCD: no difference.  In bf16 the instructions, an exponential and five more a logit,
-// weigh nearly as much (waves wait for 23% of their cycles, in fp32 for 56%): 2048 rows of 32000, 1200
+// weigh nearly as much (waves wait for 25% of their cycles, in fp32 for 52%): 2048 rows of 32000, 1200
 // different ones, take 26 us.  With logits decoded again for the maximum, the sums, the rank and the
 // alternatives the same pass took 464 us.  Where there is about one row a compute unit, the alternatives
 // cost 10 of 38 us (300 rows), as nothing else runs.

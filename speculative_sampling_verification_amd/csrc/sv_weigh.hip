@@ -100,15 +100,16 @@ __device__ __forceinline__ Share find_pieces(const WeighArgs& a, int* b_out, lon
   return Share{pos, pos + each + (w < left ? 1 : 0)};
 }
 
-// Up to 16 rows: a wave takes KT blocks of 16 keys at a time.  Its pieces' loads form a line: while one
-// piece is computed the next one's keys and queries are on their way, and the page numbers of the one
-// after that before them (loads come back in order, so none waits for a younger one).
+// Up to 16 rows: a wave takes KT blocks of 16 keys at a time.  The next piece's page numbers are on
+// their way while one is computed.  Its keys and queries are not: they take the same registers, so a
+// wave loads them behind its products and waits, and the compute unit's other waves fill the time.
 //
-// Bound by the keys' bytes: each is read once, 16 products of a matrix instruction on it take less
-// time than its load.  Pieces of a page a workgroup, loaded and computed one after the other, took
-// 179 us where this takes 128 (620 MB of bf16 keys, 4.85 TB/s; a large copy runs at 5.2).  Three
-// workgroups a compute unit as the registers of the line allow, and no more than run at once: a
-// fourth waiting its turn made it 179.  Keys loaded past the caches: 139.
+// Bound by the keys' bytes where rows are long: 620 MB of bf16 keys of 128 columns in 128 us, 4.85 TB/s (a
+// large copy runs at 5.2).  Pieces of a page a workgroup took 179 us, three workgroups a compute unit
+// and no more than run at once as here 128: a fourth waiting its turn made it 179 again.  Keys loaded
+// past the caches: 139.  Shorter pieces wait for their loads more than that hides: 16 sequences of 512 to
+// 4096 tokens take 17 us at 64 columns of bf16 (2.35 TB/s), 15 at 96 (3.9), 22 at 64 of fp32 (3.5),
+// 35 at 128 (4.35).
 template <bool BF16, int D>
 struct Few {
   static constexpr int kRow = D * (BF16 ? 2 : 4);
@@ -279,11 +280,13 @@ __global__ __launch_bounds__(kWeighThreads, (Few<BF16, D>::kOcc)) void k_weigh(W
 // Bound by the matrix instructions and, between them, an exponential a product of 2 D operations: 64
 // nodes of 64 query heads to 8 kv heads of 128 on 131072 tokens (512 rows) take 180 us, 775 TFLOP/s,
 // and 256 nodes 590 us, 945 (a library product of 8192^3 runs at 1350).  Vector instructions fill 85 us
-// of the 180, products 61 (at 2.15 GHz), and the two overlap little: waves wait 47% of their time.
+// of the 180, products 61 (at 2.15 GHz), and the two overlap little: waves wait 47% of their time.  The
+// compiler waits for the keys, in order of the loads, where the loop of rows first uses them, and in
+// every turn: so the first 32 rows of a stage wait for the next stage's, just asked for.
 // Rows staged through registers took 209 us, with one workgroup a compute unit less 204; 128 rows a
 // stage 272; products of the next 32 rows begun before the last ones' exponentials 217 (registers
 // spill); four workgroups a unit 218; pieces that are left over when all workgroups have as many, in
-// halves for two, or three stages with loads two ahead: no difference.
+// halves for two, or three stages with loads two ahead: no difference (with that wait in place).
 template <bool BF16, int D, int KB, int RT>
 struct Rows {
   static constexpr int kES = BF16 ? 2 : 4;
@@ -292,7 +295,8 @@ struct Rows {
   static constexpr int kFrags = kChunks / 2;           // ... that a lane holds
   static constexpr int kKeys = 32 * KB * kWeighWaves;  // of a workgroup
   static constexpr int kLoads = RT * kChunks / kWeighThreads;  // pieces a thread loads a stage
-  // workgroups a compute unit: what the registers of the keys and products leave room for
+  // workgroups a compute unit: what the registers of the keys and products leave room for, but for a
+  // few a piece that are spilled (bf16: 11 of 64 keys of 256 bytes, 4 of 32, 2 of 64 keys of 128)
   static constexpr int kKeyRegs = KB * kRow / 8;
   static constexpr int kOcc = kKeyRegs > 64 ? 1 : kKeyRegs == 64 && KB == 1 ? 2
                               : kKeyRegs > 32 ? 3 : 4;
